@@ -163,10 +163,10 @@ def _quantize(x):
     return code[..., 0::2] | (code[..., 1::2] << 4), b.squeeze(-1).to(torch.uint8)
 
 
-def _dequantize(codes, scales, dtype=torch.float32):
-    table = torch.tensor(VALUES + tuple(-v for v in VALUES), device=codes.device, dtype=dtype)
+def _dequantize(codes, scales):
+    table = torch.tensor(VALUES + tuple(-v for v in VALUES), device=codes.device)
     code = torch.stack([codes & 15, codes >> 4], dim=-1).flatten(-2).int()
-    power = torch.ldexp(torch.ones((), device=codes.device, dtype=dtype), scales.int() - 127)
+    power = torch.where(scales == 0, 1 << 22, scales.int() << 23).view(torch.float32)  # 2^(b - 127), subnormal at b = 0
     return (table[code].unflatten(-1, (-1, BLOCK)) * power.unsqueeze(-1)).flatten(-2)
 
 
@@ -229,7 +229,7 @@ def _own(s):
         return ex.mxfp4_linear(s["x"], s["codes"], s["scales"], offsets=s["offsets"])
     if op == "dispatch":
         order, position, offsets = ex.moe_sort(s["ids"], s["experts"])
-        rows = ex.moe_gather(s["x"], order, offsets)
+        rows = ex.moe_gather(s["x"], position, offsets)
         return order, position, offsets, rows, ex.moe_gather_backward(s["dy"], position, offsets)
     y = ex.moe_combine(s["x"], s["position"], s["offsets"], s["weights"])
     return (y, *ex.moe_combine_backward(s["dy"], s["x"], s["position"], s["offsets"], s["weights"]))
@@ -264,17 +264,22 @@ def work(case):
 
 # ---- the definition in 64 bits ----
 
+def _power(e):
+    """2^e in 64 bits for whole e."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def _exact_values(x):
     """The values of the MXFP4 quantisation of x, in 64 bits: nearest code by the midpoints, a tie to the even code."""
     v = x.double().reshape(-1, BLOCK)
     exponent = torch.frexp(v.abs().amax(1, keepdim=True))[1] - 1
-    shared = torch.where(v.abs().amax(1, keepdim=True) == 0, -127, (exponent - 2).clamp(min=-127)).double()
-    a = v.abs() / torch.exp2(shared)
+    shared = _power(torch.where(v.abs().amax(1, keepdim=True) == 0, -127, (exponent - 2).clamp(min=-127)))
+    a = v.abs() / shared
     q = torch.zeros_like(a)
     for k in range(7):
         middle = (VALUES[k] + VALUES[k + 1]) / 2
         q = torch.where(a >= middle if k % 2 else a > middle, VALUES[k + 1], q)
-    return (torch.sign(v) * q * torch.exp2(shared)).reshape(x.shape)
+    return (torch.sign(v) * q * shared).reshape(x.shape)
 
 
 def _exact_weight(codes, scales):
@@ -282,7 +287,7 @@ def _exact_weight(codes, scales):
     value = torch.tensor(VALUES, device=codes.device, dtype=torch.float64)
     for half, code in enumerate((codes % 16, codes // 16)):
         out[:, half::2] = value[(code % 8).long()] * (1.0 - 2.0 * (code // 8).double())
-    return out * torch.exp2(scales.double() - 127).repeat_interleave(BLOCK, dim=1)
+    return out * _power(scales.int() - 127).repeat_interleave(BLOCK, dim=1)
 
 
 def exact(case, seed):
