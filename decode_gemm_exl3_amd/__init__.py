@@ -21,7 +21,8 @@ import os
 
 __all__ = ["Exl3Error", "lib_path", "load", "pack_info", "Workspace", "decode_tile", "gemv", "gemv_multi",
            "gemm", "linear", "linear_noalloc", "status_string", "MAX_PROJ", "CODEBOOK_BYTE_SUM", "bits_arg", "encode_slot_bytes",
-           "encode_tiles"]
+           "encode_tiles", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear", "mxfp4_matmul", "mxfp4_workspace_bytes",
+           "moe_sort", "moe_gather", "moe_gather_backward", "moe_combine", "moe_combine_backward"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -301,3 +302,18 @@ def encode_tiles(w, bits: int, codebook: int = 0, workspace=None, words=None, co
 def gemm(x, trellis, sign, out_scale, bits: int, workspace=None, y=None, stream=None, codebook: int = 0):
     """The same result for any m >= 1 through the matrix-core GEMM path."""
     return _linear("exl3_gemm", x, trellis, sign, out_scale, bits, workspace, y, stream, codebook)
+
+
+# The MXFP4 and expert operators live in modules of their own, imported on the
+# first use of one of their names (they import torch, this module does not).
+_LAZY = {**dict.fromkeys(("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear", "mxfp4_matmul", "mxfp4_workspace_bytes"), "mxfp4"),
+         **dict.fromkeys(("moe_sort", "moe_gather", "moe_gather_backward", "moe_combine", "moe_combine_backward"), "moe")}
+
+
+def __getattr__(name: str):
+    if name not in _LAZY:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+    value = getattr(importlib.import_module("." + _LAZY[name], __name__), name)
+    globals()[name] = value
+    return value

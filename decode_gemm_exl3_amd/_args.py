@@ -1,0 +1,116 @@
+"""Argument checks shared by the bindings of the MXFP4 and expert operators.
+
+The library reads and writes raw device memory, so every tensor is checked for
+element type, shape, contiguity, 16-byte alignment and device before a call
+reaches it.  The calls run on the device of their first tensor: the launch goes
+to `stream` or to that device's current stream, with the device made current for
+the time of the call.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import Exl3Error, _check, load
+
+VOID, I32, I64, SIZE = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+FLOATS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}  # enum exl3_dtype
+BYTES = {torch.uint8: None}
+INDEX = {torch.int32: None}
+
+
+def declare(name: str, *argtypes, restype=ctypes.c_int):
+    """The library's function of that name, its types set on the first use."""
+    slot = []
+
+    def get():
+        if not slot:
+            f = getattr(load(), name)
+            f.argtypes, f.restype = argtypes, restype
+            slot.append(f)
+        return slot[0]
+    return get
+
+
+def dtype_code(t, name: str) -> int:
+    """exl3_dtype of a floating tensor (or dtype)."""
+    dtype = t if isinstance(t, torch.dtype) else getattr(t, "dtype", None)
+    code = FLOATS.get(dtype)
+    if code is None:
+        if dtype is None:
+            raise Exl3Error(f"{name}: expected a torch tensor")
+        raise Exl3Error(f"{name}: dtype {dtype}, expected one of {tuple(str(d) for d in FLOATS)}")
+    return code
+
+
+def need(t, name: str, dtypes, shape) -> int:
+    """Checks all but the device; returns the address."""
+    if not isinstance(t, torch.Tensor):
+        raise Exl3Error(f"{name}: expected a torch tensor")
+    if t.dtype not in dtypes:
+        raise Exl3Error(f"{name}: dtype {t.dtype}, expected one of {tuple(str(d) for d in dtypes)}")
+    if t.shape != shape:
+        raise Exl3Error(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise Exl3Error(f"{name}: must be contiguous")
+    at = t.data_ptr()
+    if at & 15:
+        raise Exl3Error(f"{name}: data must be 16-byte aligned (a view at an offset is not)")
+    return at
+
+
+def need_rows(t, name: str) -> int:
+    """A 2-dimensional floating tensor whose rows are contiguous and start at
+    multiples of 16 bytes; returns the row stride in elements."""
+    dtype_code(t, name)
+    if t.dim() != 2:
+        raise Exl3Error(f"{name}: expected two dimensions, got shape {tuple(t.shape)}")
+    rows, n = t.shape
+    ld, inner = t.stride()
+    if rows <= 1:
+        ld = n
+    if (inner != 1 and n > 1) or ld < n:
+        raise Exl3Error(f"{name}: the values of a row must be contiguous and rows must not overlap")
+    if t.data_ptr() & 15 or ld * t.element_size() & 15:
+        raise Exl3Error(f"{name}: rows must start at multiples of 16 bytes")
+    return ld
+
+
+def on_device(dev: int, **tensors) -> None:
+    """Every tensor on GPU `dev`, the device of the first."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        at = t.get_device()
+        if at < 0:
+            raise Exl3Error(f"{name}: must be on a GPU device")
+        if at != dev:
+            raise Exl3Error(f"{name}: on GPU {at}, the first tensor is on GPU {dev}")
+
+
+def call(fn, what: str, dev: int, stream, *args) -> None:
+    """fn(*args, stream) on GPU `dev`."""
+    if stream is not None and stream.device_index != dev:
+        raise Exl3Error(f"{what}: the stream is of GPU {stream.device_index}, the tensors are on GPU {dev}")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return call(fn, what, dev, stream, *args)
+    handle = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    status = fn()(*args, handle)
+    if status != 0:
+        _check(status, what)
+
+
+def scratch(workspace, nbytes: int, like, stream):
+    """`workspace` when given, else scratch of the caching allocator, kept from
+    reuse until `stream` is done with it."""
+    if workspace is not None:
+        need(workspace, "workspace", BYTES, (workspace.numel(),) if isinstance(workspace, torch.Tensor) else None)
+        return workspace
+    if nbytes == 0:
+        return None
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if stream is not None:
+        buf.record_stream(stream)
+    return buf

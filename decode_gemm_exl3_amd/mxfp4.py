@@ -1,0 +1,118 @@
+"""MXFP4 operators (include/exl3_mxfp4.h): quantise, dequantise, products.
+
+Tensors:
+  codes  : uint8 [..., n / 2], two codes a byte, the lower column in the low half
+  scales : uint8 [..., n / 32], 2^(b - 127) for each block of 32 columns
+  x      : float16, bfloat16 or float32 [m, n_in]; its rows may be a slice of wider ones
+A weight is codes [n_out, n_in / 2] and scales [n_out, n_in / 32]; with offsets
+(int32 [groups + 1]) there is one per group, [groups, n_out, ...], and rows
+offsets[g] .. offsets[g + 1] - 1 go through weight g.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import Exl3Error, _check
+from ._args import BYTES, FLOATS, I32, I64, INDEX, SIZE, VOID, call, declare, dtype_code, need, need_rows, on_device, scratch
+
+BLOCK = 32  # EXL3_MXFP4_BLOCK
+
+_quantize = declare("exl3_mxfp4_quantize", VOID, I32, I64, I32, I64, VOID, VOID, VOID)
+_dequantize = declare("exl3_mxfp4_dequantize", VOID, VOID, I64, I32, VOID, I32, VOID)
+_bytes = declare("exl3_mxfp4_workspace_bytes", I32, I32, I32, restype=I64)
+_matmul = declare("exl3_mxfp4_matmul", VOID, VOID, I32, VOID, I32, VOID, VOID, I32, I32, VOID, I32, VOID)
+_linear = declare("exl3_mxfp4_linear", VOID, I32, I32, I64, VOID, I32, VOID, VOID, I32, I32, VOID, VOID, SIZE, VOID)
+
+
+def _blocks(n: int, name: str) -> int:
+    if n < BLOCK or n % BLOCK:
+        raise Exl3Error(f"{name}: {n} columns, expected a positive multiple of {BLOCK}")
+    return n // BLOCK
+
+
+def mxfp4_quantize(x, codes=None, scales=None, stream=None):
+    """x [rows, n] to (codes [rows, n / 2], scales [rows, n / 32])."""
+    ld = need_rows(x, "x")
+    rows, n = x.shape
+    blocks = _blocks(n, "x")
+    if codes is None:
+        codes = torch.empty((rows, n // 2), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((rows, blocks), dtype=torch.uint8, device=x.device)
+    c, s = need(codes, "codes", BYTES, (rows, n // 2)), need(scales, "scales", BYTES, (rows, blocks))
+    dev = x.get_device()
+    on_device(dev, x=x, codes=codes, scales=scales)
+    call(_quantize, "exl3_mxfp4_quantize", dev, stream, x.data_ptr(), FLOATS[x.dtype], rows, n, ld, c, s)
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
+    """The values of codes [rows, n / 2] and scales [rows, n / 32], as dtype [rows, n]."""
+    code = dtype_code(dtype, "dtype")
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise Exl3Error("codes: expected a torch tensor of two dimensions")
+    rows, n = codes.shape[0], codes.shape[1] * 2
+    blocks = _blocks(n, "codes")
+    if out is None:
+        out = torch.empty((rows, n), dtype=dtype, device=codes.device)
+    c, s = need(codes, "codes", BYTES, (rows, n // 2)), need(scales, "scales", BYTES, (rows, blocks))
+    o = need(out, "out", (dtype,), (rows, n))
+    dev = codes.get_device()
+    on_device(dev, codes=codes, scales=scales, out=out)
+    call(_dequantize, "exl3_mxfp4_dequantize", dev, stream, c, s, rows, n, o, code)
+    return out
+
+
+def mxfp4_workspace_bytes(rows: int, n_in: int, groups: int = 1) -> int:
+    """Bytes of device scratch that mxfp4_linear needs (0: none)."""
+    n = int(_bytes()(rows, groups, n_in))
+    if n < 0:
+        _check(n, "exl3_mxfp4_workspace_bytes")
+    return n
+
+
+def _weight(codes, scales, offsets, n_in: int, blocks: int):
+    """Addresses of a weight and its offsets, with the group count and n_out."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != (2 if offsets is None else 3):
+        raise Exl3Error("codes: expected a torch tensor [n_out, n_in / 2], or [groups, n_out, n_in / 2] with offsets")
+    lead = codes.shape[:-1]
+    c, s = need(codes, "codes", BYTES, (*lead, n_in // 2)), need(scales, "scales", BYTES, (*lead, blocks))
+    if offsets is None:
+        return c, s, None, 1, lead[0]
+    return c, s, need(offsets, "offsets", INDEX, (lead[0] + 1,)), lead[0], lead[1]
+
+
+def mxfp4_matmul(x_codes, x_scales, codes, scales, dtype=torch.bfloat16, offsets=None, y=None, stream=None):
+    """y [m, n_out] = X @ W^T for quantised rows X (x_codes [m, n_in / 2], x_scales
+    [m, n_in / 32]): several projections of one input quantise it once."""
+    code = dtype_code(dtype, "dtype")
+    if not isinstance(x_codes, torch.Tensor) or x_codes.dim() != 2:
+        raise Exl3Error("x_codes: expected a torch tensor of two dimensions")
+    m, n_in = x_codes.shape[0], x_codes.shape[1] * 2
+    blocks = _blocks(n_in, "x_codes")
+    xc, xs = need(x_codes, "x_codes", BYTES, (m, n_in // 2)), need(x_scales, "x_scales", BYTES, (m, blocks))
+    c, s, at, groups, n_out = _weight(codes, scales, offsets, n_in, blocks)
+    if y is None:
+        y = torch.empty((m, n_out), dtype=dtype, device=x_codes.device)
+    o = need(y, "y", (dtype,), (m, n_out))
+    dev = x_codes.get_device()
+    on_device(dev, x_codes=x_codes, x_scales=x_scales, codes=codes, scales=scales, offsets=offsets, y=y)
+    call(_matmul, "exl3_mxfp4_matmul", dev, stream, xc, xs, m, at, groups, c, s, n_in, n_out, o, code)
+    return y
+
+
+def mxfp4_linear(x, codes, scales, offsets=None, workspace=None, y=None, stream=None):
+    """y [m, n_out] = Q(x) @ W^T in x's type, Q(x) the MXFP4 quantisation of x."""
+    ld = need_rows(x, "x")
+    m, n_in = x.shape
+    blocks = _blocks(n_in, "x")
+    c, s, at, groups, n_out = _weight(codes, scales, offsets, n_in, blocks)
+    if y is None:
+        y = torch.empty((m, n_out), dtype=x.dtype, device=x.device)
+    o = need(y, "y", (x.dtype,), (m, n_out))
+    dev = x.get_device()
+    on_device(dev, x=x, codes=codes, scales=scales, offsets=offsets, y=y, workspace=workspace)
+    ws = scratch(workspace, mxfp4_workspace_bytes(m, n_in, groups) if workspace is None else 0, x, stream)
+    call(_linear, "exl3_mxfp4_linear", dev, stream, x.data_ptr(), FLOATS[x.dtype], m, ld, at, groups, c, s, n_in, n_out,
+         o, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
+    return y
