@@ -1,6 +1,8 @@
 // mxfp4.hip - MXFP4 quantisation, dequantisation and products (gfx950).
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "../../include/exl3_mxfp4.h"
 #include "mxfp4_device.hpp"
 
@@ -188,7 +190,7 @@ template <typename OT> __device__ inline void store4(void* y, int64_t at, int co
 template <typename OT, bool FUSED, int MT, int NS, int W>
 __global__ __launch_bounds__(W * 64) void skinny_kernel(const ProductParams p) {
     __shared__ f32x4_t red[W][NS * MT][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
     const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, blockIdx.y, 16 * MT);
     if (t.rows == 0) return;
     const int n0 = blockIdx.x * 16 * NS;
@@ -272,95 +274,229 @@ __global__ __launch_bounds__(W * 64) void skinny_kernel(const ProductParams p) {
     }
 }
 
-// Many rows: a workgroup of four waves owns 16 RT rows and 256 outputs, wave w
-// all the rows and outputs 64 w .. 64 w + 63.  The quantised rows of a span (256
-// bytes each) are staged in LDS, double buffered and loaded there directly; the
-// weight goes from memory into the operands, as no other wave needs it.  Block c
-// of row r sits in 16-byte slot c ^ (r & 15) of the row's 256 bytes: the 16 rows
-// of an operand then read 16 different slots.
-template <typename OT, int RT>
-__global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p) {
-    constexpr int BM = 16 * RT;
-    __shared__ i32x4_t As[2][BM * 16];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
-    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, blockIdx.y, BM);
-    if (t.rows == 0) return;
-    const int n0 = blockIdx.x * 256 + wave * 64;
-    const int nb = p.n_in / BLOCK, spans = (nb + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
-    const bool whole = (nb & 3) == 0, vec = (p.n_out & 3) == 0;
-    const int half = p.n_in / 2;
+// Many rows: a workgroup of four waves owns 64 RT rows and 256 outputs, each wave
+// a quarter of them, 32 RT rows and 128 outputs.  Stages of 256 inputs (128 bytes
+// of codes a row) of both sides go straight from memory into LDS, double
+// buffered; the waves read their operands from there.  (A weight operand read
+// from memory by its lanes would touch 64 cache lines for 1 KB.)
+//
+// Block c of row r sits in 16-byte slot c ^ (r / 2 & 7) of the row's 128 bytes:
+// the 16 lanes that LDS serves together (0-3, 12-15, 20-23, 24-27 and so on) then
+// read 16 different slots of its 256-byte width.
+//
+// A stage is four steps of 64 inputs; lane half h holds blocks 4h .. 4h + 3 of the
+// stage's eight, one dword of scales, and feeds block 4h + j to step j.
 
-    f32x4_t acc[RT][4];
-#pragma unroll
-    for (int m = 0; m < RT; ++m)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[m][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+// Workgroup b of a launch to tile index: units of 32 consecutive tiles go to the
+// same XCD (workgroups go round the 8 XCDs one by one), so that the tiles that
+// run together on an XCD share rows and weights in its L2.
+constexpr int XCDS = 8, XCD_UNIT = 32;
+__device__ inline int xcd_tile(int b) {
+    const int xcd = b % XCDS, local = b / XCDS;
+    return (local / XCD_UNIT * XCDS + xcd) * XCD_UNIT + local % XCD_UNIT;
+}
+// Tiles of a launch, padded to whole rounds of units.
+inline int64_t xcd_padded(int64_t tiles) { return (tiles + XCDS * XCD_UNIT - 1) / (XCDS * XCD_UNIT) * (XCDS * XCD_UNIT); }
+constexpr int BAND = 8;  // row tiles that share a run of output tiles
 
-    if (t.group < p.n_groups) {
-        // load i of a wave brings 4 rows: lane l writes slot l % 16 of row l / 16.
-        // Rows behind the tile re-read its last, blocks behind the row's end its last
-        // block: what they multiply is zero or never stored.
-        const uint8_t* xc = p.xc + (int64_t)t.row0 * half;
-        auto stage = [&](int sp, int buf) {
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const int row = (i * 4 + wave) * 4 + (lane >> 4);
-                const int c = min((lane & 15) ^ (row & 15), nb - 1 - sp * SPAN_BLOCKS);
-                const uint8_t* src = xc + (int64_t)min(row, t.rows - 1) * half + sp * 256 + c * 16;
-                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                                 (__attribute__((address_space(3))) void*)(&As[buf][(i * 4 + wave) * 64]), 16, 0, 0);
-            }
-        };
-        const uint8_t *wc[4], *ws[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int64_t o = (int64_t)t.group * p.n_out + min(n0 + 16 * c + r, p.n_out - 1);
-            wc[c] = p.wc + o * half + 64 * q;
-            ws[c] = p.ws + o * nb + 4 * q;
-        }
-        stage(0, 0);
-        for (int sp = 0; sp < spans; ++sp) {
-            const int left = nb - sp * SPAN_BLOCKS - 4 * q;
-            i32x4_t wv[4][4];
-            uint32_t wsc[4], xsc[RT];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                load_codes(wc[c] + sp * 256, left, wv[c]);
-                wsc[c] = load_scales(ws[c] + sp * 16, left, whole);
-            }
-#pragma unroll
-            for (int m = 0; m < RT; ++m) {
-                const int row = t.row0 + min(16 * m + r, t.rows - 1);
-                xsc[m] = load_scales(p.xs + (int64_t)row * nb + sp * 16 + 4 * q, left, whole);
-            }
-            __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this span's rows have landed
-            __syncthreads();
-            if (sp + 1 < spans) stage(sp + 1, (sp + 1) & 1);
-            const i32x4_t* a = As[sp & 1];
-#pragma unroll
-            for (int m = 0; m < RT; ++m) {
-                i32x4_t xv[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) xv[j] = a[(16 * m + r) * 16 + ((4 * q + j) ^ r)];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    acc[m][c] = mfma<0>(wv[c][0], wsc[c], xv[0], xsc[m], acc[m][c]);
-                    acc[m][c] = mfma<1>(wv[c][1], wsc[c], xv[1], xsc[m], acc[m][c]);
-                    acc[m][c] = mfma<2>(wv[c][2], wsc[c], xv[2], xsc[m], acc[m][c]);
-                    acc[m][c] = mfma<3>(wv[c][3], wsc[c], xv[3], xsc[m], acc[m][c]);
-                }
-            }
-            __syncthreads();  // the buffer is free for the span after next
+// Memory from `base` on, read at 32-bit offsets.
+__device__ inline __amdgpu_buffer_rsrc_t buffer(const uint8_t* base, int64_t bytes) {
+    const uint32_t n = bytes > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)bytes;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, n, 0x00020000);
+}
+__device__ inline i32x4_t load16(__amdgpu_buffer_rsrc_t b, uint32_t voff, uint32_t soff) {
+    return __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(b, voff, soff, 0));
+}
+// Straight into LDS: lane l's 16 bytes at dst + 16 l.
+__device__ inline void load16_to_lds(__amdgpu_buffer_rsrc_t b, i32x4_t* dst, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)dst, 16, voff, soff, 0, 0);
+}
+constexpr uint32_t OUTSIDE = 0x7FFFFFF0u;  // an offset past every buffer: the load gives zeros
+
+// Four scale bytes of one lane.  WHOLE: rows of a multiple of 4 blocks, aligned
+// dwords.  Otherwise the one or two aligned dwords that hold them, which meet in
+// join().
+template <bool WHOLE> struct Scales {
+    uint32_t lo, hi;
+    // `left` blocks of the row are left from this lane's first on
+    __device__ inline void load(__amdgpu_buffer_rsrc_t b, uint32_t voff, uint32_t soff, int left) {
+        if constexpr (WHOLE) {
+            lo = __builtin_amdgcn_raw_buffer_load_b32(b, left > 0 ? voff : OUTSIDE, soff, 0);
+        } else {
+            lo = __builtin_amdgcn_raw_buffer_load_b32(b, left > 0 ? voff & ~3u : OUTSIDE, soff, 0);
+            hi = __builtin_amdgcn_raw_buffer_load_b32(b, left > 0 ? (voff + min(left, 4) - 1) & ~3u : OUTSIDE, soff, 0);
         }
     }
+    // The bytes of the next row, which may stand for NaN, give way to zeros.
+    __device__ inline uint32_t join(uint32_t voff, int left) const {
+        if constexpr (WHOLE) return lo;
+        const uint32_t v = __builtin_amdgcn_alignbyte(hi, lo, voff & 3u);
+        return left >= 4 ? v : (left > 0 ? v & ((1u << (8 * left)) - 1u) : 0u);
+    }
+};
+
+constexpr int STAGE_BLOCKS = 8;
+
+template <typename OT, int RT, bool WHOLE>
+__global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int row_tiles, int col_tiles) {
+    constexpr int BM = 64 * RT, BN = 256;
+    constexpr int STAGE = (BM + BN) * 8;  // 16-byte slots: the rows', then the weight's
+    constexpr int ROW_LOADS = BM / 32, W_LOADS = BN / 32;  // a wave's loads per stage, 8 rows each
+    __shared__ i32x4_t lds[2 * STAGE];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 31, h = lane >> 5, wy = wave >> 1, wx = wave & 1;
+    const int tile = xcd_tile(blockIdx.x);
+    const int band = tile / (BAND * col_tiles), band_rows = min(BAND, row_tiles - band * BAND);
+    if (band_rows <= 0) return;
+    const int in_band = tile - band * BAND * col_tiles;
+    const int col = in_band / band_rows;
+    if (col >= col_tiles) return;
+    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, band * BAND + in_band - col * band_rows, BM);
+    if (t.rows == 0) return;
+    const int n0 = col * BN, cols = min(BN, p.n_out - n0);
+    const int nb = p.n_in / BLOCK, stages = (nb + STAGE_BLOCKS - 1) / STAGE_BLOCKS;
+    const int half = p.n_in / 2;
+
+    f32x16_t acc[RT][4];
 #pragma unroll
     for (int m = 0; m < RT; ++m)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int row = 16 * m + r, o = n0 + 16 * c + 4 * q;
-            if (row < t.rows && o < p.n_out)
-                store4<OT>(p.y, (int64_t)(t.row0 + row) * p.n_out + o, p.n_out - o, vec, acc[m][c]);
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[m][c][i] = 0.f;
+
+    if (t.group < p.n_groups) {
+        const int64_t w0 = (int64_t)t.group * p.n_out + n0;
+        // scales from the 16-byte border at or before the tile's first
+        const int64_t xs0 = (int64_t)t.row0 * nb, ws0 = w0 * nb;
+        const __amdgpu_buffer_rsrc_t bxc = buffer(p.xc + (int64_t)t.row0 * half, (int64_t)t.rows * half);
+        const __amdgpu_buffer_rsrc_t bwc = buffer(p.wc + w0 * half, (int64_t)cols * half);
+        const __amdgpu_buffer_rsrc_t bxs = buffer(p.xs + (xs0 & ~int64_t(15)), ((xs0 & 15) + (int64_t)t.rows * nb + 3) & ~int64_t(3));
+        const __amdgpu_buffer_rsrc_t bws = buffer(p.ws + (ws0 & ~int64_t(15)), ((ws0 & 15) + (int64_t)cols * nb + 3) & ~int64_t(3));
+        // Byte offsets of this lane from those.  Rows behind the tile re-read its
+        // last, outputs behind the last re-read that one (never stored).  Load i
+        // of a wave brings rows 32 i + 8 wave .. + 7, lane l slot l % 8 of row l / 8.
+        const int srow = 8 * wave + (lane >> 3), sblock = (lane & 7) ^ ((srow >> 1) & 7);
+        uint32_t rc[ROW_LOADS], wc[W_LOADS], xso[RT], wso[4];
+#pragma unroll
+        for (int i = 0; i < ROW_LOADS; ++i) rc[i] = (uint32_t)min(32 * i + srow, t.rows - 1) * half;
+#pragma unroll
+        for (int i = 0; i < W_LOADS; ++i) wc[i] = (uint32_t)min(32 * i + srow, cols - 1) * half;
+#pragma unroll
+        for (int m = 0; m < RT; ++m) xso[m] = (uint32_t)min((wy * RT + m) * 32 + r, t.rows - 1) * nb + 4 * h + (uint32_t)(xs0 & 15);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) wso[c] = (uint32_t)min((wx * 4 + c) * 32 + r, cols - 1) * nb + 4 * h + (uint32_t)(ws0 & 15);
+
+        Scales<WHOLE> wsn[4], xsn[RT];  // of the next stage
+        // Codes and scales of stage st.  Rows: blocks behind the end re-read the
+        // last (any codes: the weight's are zeros there).
+        auto ask = [&](int st, int buf) {
+            const int rest = nb - st * STAGE_BLOCKS, left = rest - 4 * h;
+            const uint32_t xb = 16 * min(sblock, rest - 1), wb = sblock < rest ? 16 * sblock : OUTSIDE;
+            const uint32_t soff = (uint32_t)st * 128;
+            i32x4_t* dst = lds + buf * STAGE + wave * 64;
+#pragma unroll
+            for (int i = 0; i < ROW_LOADS; ++i) load16_to_lds(bxc, dst + i * 256, rc[i] + xb, soff);
+#pragma unroll
+            for (int i = 0; i < W_LOADS; ++i) load16_to_lds(bwc, dst + BM * 8 + i * 256, sblock < rest ? wc[i] + wb : OUTSIDE, soff);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) wsn[c].load(bws, wso[c], (uint32_t)st * 8, left);
+#pragma unroll
+            for (int m = 0; m < RT; ++m) xsn[m].load(bxs, xso[m], (uint32_t)st * 8, left);
+        };
+        // slot of this lane's block of step j in row r of a 32-row tile
+        int frag[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) frag[j] = r * 8 + ((4 * h + j) ^ ((r >> 1) & 7));
+
+        ask(0, 0);
+        for (int st = 0; st < stages; ++st) {
+            // everything asked for is here, in every wave, and the other buffer is read
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            const int left = nb - st * STAGE_BLOCKS - 4 * h;
+            uint32_t wsc[4], xsc[RT];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) wsc[c] = wsn[c].join(wso[c], left);
+#pragma unroll
+            for (int m = 0; m < RT; ++m) xsc[m] = xsn[m].join(xso[m], left);
+            const i32x4_t* xa = lds + (st & 1) * STAGE + wy * RT * 256;
+            const i32x4_t* wa = lds + (st & 1) * STAGE + BM * 8 + wx * 4 * 256;
+            i32x4_t xv[2][RT], wv[2][4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) wv[0][c] = wa[frag[0] + c * 256];
+#pragma unroll
+            for (int m = 0; m < RT; ++m) xv[0][m] = xa[frag[0] + m * 256];
+            if (st + 1 < stages) ask(st + 1, (st & 1) ^ 1);
+            __builtin_amdgcn_sched_barrier(0);
+            auto step = [&](auto jc) {
+                constexpr int j = decltype(jc)::value;
+                if constexpr (j < 3) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) wv[(j + 1) & 1][c] = wa[frag[j + 1] + c * 256];
+#pragma unroll
+                    for (int m = 0; m < RT; ++m) xv[(j + 1) & 1][m] = xa[frag[j + 1] + m * 256];
+                }
+#pragma unroll
+                for (int m = 0; m < RT; ++m)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[m][c] = mfma32<j>(wv[j & 1][c], wsc[c], xv[j & 1][m], xsc[m], acc[m][c]);
+#pragma unroll
+                for (int i = 0; i < 4 + RT; ++i) {  // the next step's reads between this step's MFMAs
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, RT == 4 ? 2 : 1, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            step(std::integral_constant<int, 0>{});
+            step(std::integral_constant<int, 1>{});
+            step(std::integral_constant<int, 2>{});
+            step(std::integral_constant<int, 3>{});
         }
+        __builtin_amdgcn_s_barrier();  // the buffers are read
+    }
+    // Results: a lane holds 4 consecutive outputs of a row.  32 rows at a time they
+    // go through LDS (this wave's own part), so that a store writes 256 bytes and
+    // more of a row.
+    constexpr int PITCH = 128 * OT::bytes + 16;
+    static_assert(4 * 32 * PITCH <= (int)sizeof(lds), "the waves' parts fit");
+    char* part = reinterpret_cast<char*>(lds) + wave * 32 * PITCH;
+    const int wcols = min(128, cols - wx * 128);
+    const bool vec = (p.n_out * OT::bytes) % 16 == 0;
+#pragma unroll
+    for (int m = 0; m < RT; ++m) {
+        const int mrow = (wy * RT + m) * 32, live = min(32, t.rows - mrow);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4_t v = {acc[m][c][4 * g], acc[m][c][4 * g + 1], acc[m][c][4 * g + 2], acc[m][c][4 * g + 3]};
+                store4<OT>(part + r * PITCH, 32 * c + 8 * g + 4 * h, 4, true, v);
+            }
+        __builtin_amdgcn_wave_barrier();
+        const int64_t y0 = (int64_t)(t.row0 + mrow) * p.n_out + n0 + wx * 128;
+        typedef typename OT::raw raw;
+        raw* y = static_cast<raw*>(p.y);
+        if (vec) {
+            constexpr int PER = 16 / OT::bytes, LANES = 128 / PER;  // outputs of a lane, lanes of a row
+#pragma unroll
+            for (int i = 0; i < 32; i += 64 / LANES) {
+                const int row = i + lane / LANES, o = lane % LANES * PER;
+                const i32x4_t v = *reinterpret_cast<const i32x4_t*>(part + row * PITCH + o * OT::bytes);
+                if (row < live && o < wcols) *reinterpret_cast<i32x4_t*>(y + y0 + (int64_t)row * p.n_out + o) = v;
+            }
+        } else {
+            for (int row = 0; row < live; ++row)
+#pragma unroll
+                for (int o = 0; o < 128; o += 64) {
+                    const raw v = reinterpret_cast<const raw*>(part + row * PITCH)[o + lane];
+                    if (o + lane < wcols) y[y0 + (int64_t)row * p.n_out + o + lane] = v;
+                }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
 }
 
 // ---- launches ----
@@ -392,20 +528,23 @@ inline int64_t typical_rows(int64_t rows, int n_groups) { return (rows + n_group
 // Whether a product quantises its rows itself.
 inline bool fused(int64_t rows, int n_groups) { return typical_rows(rows, n_groups) <= 16; }
 
+template <typename OT, int RT> hipError_t launch_gemm(const ProductParams& p, hipStream_t s) {
+    const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, 64 * RT), cols = (p.n_out + 255) / 256;
+    const int64_t tiles = xcd_padded(rows * cols);
+    if (tiles > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    if (p.n_in % (4 * BLOCK) == 0) gemm_kernel<OT, RT, true><<<(unsigned)tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
+    else gemm_kernel<OT, RT, false><<<(unsigned)tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
+    return hipGetLastError();
+}
+
 template <typename OT> hipError_t launch_product(const ProductParams& p, hipStream_t s) {
     const int64_t m = typical_rows(p.rows, p.n_groups);
     if (p.x) return launch_skinny<OT, true, 1, 1>(p, s);
     if (m <= 16) return launch_skinny<OT, false, 1, 1>(p, s);
     if (m <= 32) return launch_skinny<OT, false, 2, 1>(p, s);
     if (m <= SKINNY_MAX_ROWS) return launch_skinny<OT, false, 4, 1>(p, s);
-    if (m <= 128) {
-        const dim3 grid((unsigned)((p.n_out + 255) / 256), (unsigned)max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, 128));
-        gemm_kernel<OT, 8><<<grid, 256, 0, s>>>(p);
-    } else {
-        const dim3 grid((unsigned)((p.n_out + 255) / 256), (unsigned)max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, 256));
-        gemm_kernel<OT, 16><<<grid, 256, 0, s>>>(p);
-    }
-    return hipGetLastError();
+    if (m <= 128) return launch_gemm<OT, 2>(p, s);
+    return launch_gemm<OT, 4>(p, s);
 }
 
 hipError_t product(int dtype, const ProductParams& p, hipStream_t s) {
