@@ -286,6 +286,12 @@ __global__ __launch_bounds__(W * 64) void skinny_kernel(const ProductParams p) {
 //
 // A stage is four steps of 64 inputs; lane half h holds blocks 4h .. 4h + 3 of the
 // stage's eight, one dword of scales, and feeds block 4h + j to step j.
+//
+// The scales of two stages (16 bytes a row) go through LDS as well, four lanes a
+// row: read by the lanes that use them they would be one dword from each of 64
+// places, 64 cycles of the address unit a load and twice the time of all codes.
+// Where rows start at any byte (WHOLE false: n_in % 128 != 0) the eight aligned
+// dwords that hold them are staged and two of them meet in an alignbyte.
 
 // Workgroup b of a launch to tile index: units of 32 consecutive tiles go to the
 // same XCD (workgroups go round the 8 XCDs one by one), so that the tiles that
@@ -313,27 +319,9 @@ __device__ inline void load16_to_lds(__amdgpu_buffer_rsrc_t b, i32x4_t* dst, uin
 }
 constexpr uint32_t OUTSIDE = 0x7FFFFFF0u;  // an offset past every buffer: the load gives zeros
 
-// Four scale bytes of one lane.  WHOLE: rows of a multiple of 4 blocks, aligned
-// dwords.  Otherwise the one or two aligned dwords that hold them, which meet in
-// join().
-template <bool WHOLE> struct Scales {
-    uint32_t lo, hi;
-    // `left` blocks of the row are left from this lane's first on
-    __device__ inline void load(__amdgpu_buffer_rsrc_t b, uint32_t voff, uint32_t soff, int left) {
-        if constexpr (WHOLE) {
-            lo = __builtin_amdgcn_raw_buffer_load_b32(b, left > 0 ? voff : OUTSIDE, soff, 0);
-        } else {
-            lo = __builtin_amdgcn_raw_buffer_load_b32(b, left > 0 ? voff & ~3u : OUTSIDE, soff, 0);
-            hi = __builtin_amdgcn_raw_buffer_load_b32(b, left > 0 ? (voff + min(left, 4) - 1) & ~3u : OUTSIDE, soff, 0);
-        }
-    }
-    // The bytes of the next row, which may stand for NaN, give way to zeros.
-    __device__ inline uint32_t join(uint32_t voff, int left) const {
-        if constexpr (WHOLE) return lo;
-        const uint32_t v = __builtin_amdgcn_alignbyte(hi, lo, voff & 3u);
-        return left >= 4 ? v : (left > 0 ? v & ((1u << (8 * left)) - 1u) : 0u);
-    }
-};
+__device__ inline void load4_to_lds(__amdgpu_buffer_rsrc_t b, uint32_t* dst, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)dst, 4, voff, soff, 0, 0);
+}
 
 constexpr int STAGE_BLOCKS = 8;
 
@@ -342,7 +330,10 @@ __global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int
     constexpr int BM = 64 * RT, BN = 256;
     constexpr int STAGE = (BM + BN) * 8;  // 16-byte slots: the rows', then the weight's
     constexpr int ROW_LOADS = BM / 32, W_LOADS = BN / 32;  // a wave's loads per stage, 8 rows each
-    __shared__ i32x4_t lds[2 * STAGE];
+    constexpr int SDW = WHOLE ? 4 : 8;    // dwords of scales a row holds in LDS
+    constexpr int SPAIR = (BM + BN) * SDW, SCALE_LOADS = (BM + BN) * SDW / 256;
+    __shared__ i32x4_t lds[2 * STAGE + SPAIR / 2];  // one object: the compiler then keeps loads into it in flight over reads of it
+    uint32_t* const lds_scales = reinterpret_cast<uint32_t*>(lds + 2 * STAGE);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 31, h = lane >> 5, wy = wave >> 1, wx = wave & 1;
     const int tile = xcd_tile(blockIdx.x);
@@ -377,51 +368,68 @@ __global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int
         // last, outputs behind the last re-read that one (never stored).  Load i
         // of a wave brings rows 32 i + 8 wave .. + 7, lane l slot l % 8 of row l / 8.
         const int srow = 8 * wave + (lane >> 3), sblock = (lane & 7) ^ ((srow >> 1) & 7);
-        uint32_t rc[ROW_LOADS], wc[W_LOADS], xso[RT], wso[4];
+        uint32_t rc[ROW_LOADS], wc[W_LOADS], so[SCALE_LOADS];
 #pragma unroll
         for (int i = 0; i < ROW_LOADS; ++i) rc[i] = (uint32_t)min(32 * i + srow, t.rows - 1) * half;
 #pragma unroll
         for (int i = 0; i < W_LOADS; ++i) wc[i] = (uint32_t)min(32 * i + srow, cols - 1) * half;
+        // load i of a wave brings the scales of 64 / SDW rows
+        const int sdw = lane % SDW;
 #pragma unroll
-        for (int m = 0; m < RT; ++m) xso[m] = (uint32_t)min((wy * RT + m) * 32 + r, t.rows - 1) * nb + 4 * h + (uint32_t)(xs0 & 15);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) wso[c] = (uint32_t)min((wx * 4 + c) * 32 + r, cols - 1) * nb + 4 * h + (uint32_t)(ws0 & 15);
-
-        Scales<WHOLE> wsn[4], xsn[RT];  // of the next stage
-        // Codes and scales of stage st.  Rows: blocks behind the end re-read the
+        for (int i = 0; i < SCALE_LOADS; ++i) {
+            const int row = (4 * i + wave) * (64 / SDW) + lane / SDW;
+            const uint32_t first = row < BM ? (uint32_t)min(row, t.rows - 1) * nb + (uint32_t)(xs0 & 15)
+                                            : (uint32_t)min(row - BM, cols - 1) * nb + (uint32_t)(ws0 & 15);
+            so[i] = (first & ~3u) + 4 * sdw;
+        }
+        // Load k of a wave for stage st.  Rows: blocks behind the end re-read the
         // last (any codes: the weight's are zeros there).
-        auto ask = [&](int st, int buf) {
-            const int rest = nb - st * STAGE_BLOCKS, left = rest - 4 * h;
-            const uint32_t xb = 16 * min(sblock, rest - 1), wb = sblock < rest ? 16 * sblock : OUTSIDE;
+        auto ask_codes = [&](int k, int st, int buf) {
+            const int rest = nb - st * STAGE_BLOCKS;
             const uint32_t soff = (uint32_t)st * 128;
             i32x4_t* dst = lds + buf * STAGE + wave * 64;
-#pragma unroll
-            for (int i = 0; i < ROW_LOADS; ++i) load16_to_lds(bxc, dst + i * 256, rc[i] + xb, soff);
-#pragma unroll
-            for (int i = 0; i < W_LOADS; ++i) load16_to_lds(bwc, dst + BM * 8 + i * 256, sblock < rest ? wc[i] + wb : OUTSIDE, soff);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) wsn[c].load(bws, wso[c], (uint32_t)st * 8, left);
-#pragma unroll
-            for (int m = 0; m < RT; ++m) xsn[m].load(bxs, xso[m], (uint32_t)st * 8, left);
+            if (k < ROW_LOADS) load16_to_lds(bxc, dst + k * 256, rc[k] + 16 * min(sblock, rest - 1), soff);
+            else load16_to_lds(bwc, dst + BM * 8 + (k - ROW_LOADS) * 256, sblock < rest ? wc[k - ROW_LOADS] + 16 * sblock : OUTSIDE, soff);
         };
+        // Load k of a wave for the scales of stages 2 pair and 2 pair + 1.
+        auto ask_scales = [&](int k, uint32_t off, int pair) {
+            const bool in = pair * SPAN_BLOCKS + 4 * sdw < nb + (WHOLE ? 0 : 4);
+            load4_to_lds((4 * k + wave) * (64 / SDW) < BM ? bxs : bws, lds_scales + (pair & 1) * SPAIR + (4 * k + wave) * 64,
+                         in ? off : OUTSIDE, (uint32_t)pair * SPAN_BLOCKS);
+        };
+        // The dword of this lane's four blocks of stage st, of staged row `row`.
+        auto scales = [&](int row, int shift, int st) {
+            const uint32_t* s = lds_scales + (st >> 1 & 1) * SPAIR + row * SDW + 2 * (st & 1) + h;
+            if constexpr (WHOLE) return s[0];
+            const int left = nb - st * STAGE_BLOCKS - 4 * h;  // the bytes of the next row, which may be NaN, give way to zeros
+            const uint32_t v = __builtin_amdgcn_alignbyte(s[1], s[0], shift);
+            return left >= 4 ? v : (left > 0 ? v & ((1u << (8 * left)) - 1u) : 0u);
+        };
+        uint32_t xshift[RT], wshift[4];  // bytes from an aligned dword to a row's scales
+#pragma unroll
+        for (int m = 0; m < RT; ++m) xshift[m] = ((uint32_t)min((wy * RT + m) * 32 + r, t.rows - 1) * nb + (uint32_t)(xs0 & 15)) & 3;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) wshift[c] = ((uint32_t)min((wx * 4 + c) * 32 + r, cols - 1) * nb + (uint32_t)(ws0 & 15)) & 3;
         // slot of this lane's block of step j in row r of a 32-row tile
         int frag[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) frag[j] = r * 8 + ((4 * h + j) ^ ((r >> 1) & 7));
 
-        ask(0, 0);
+#pragma unroll
+        for (int k = 0; k < ROW_LOADS + W_LOADS; ++k) ask_codes(k, 0, 0);
+#pragma unroll
+        for (int k = 0; k < SCALE_LOADS; ++k) ask_scales(k, so[k], 0);
         for (int st = 0; st < stages; ++st) {
             // everything asked for is here, in every wave, and the other buffer is read
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
-            const int left = nb - st * STAGE_BLOCKS - 4 * h;
             uint32_t wsc[4], xsc[RT];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) wsc[c] = wsn[c].join(wso[c], left);
+            for (int c = 0; c < 4; ++c) wsc[c] = scales(BM + (wx * 4 + c) * 32 + r, wshift[c], st);
 #pragma unroll
-            for (int m = 0; m < RT; ++m) xsc[m] = xsn[m].join(xso[m], left);
+            for (int m = 0; m < RT; ++m) xsc[m] = scales((wy * RT + m) * 32 + r, xshift[m], st);
             const i32x4_t* xa = lds + (st & 1) * STAGE + wy * RT * 256;
             const i32x4_t* wa = lds + (st & 1) * STAGE + BM * 8 + wx * 4 * 256;
             i32x4_t xv[2][RT], wv[2][4];
@@ -429,33 +437,49 @@ __global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int
             for (int c = 0; c < 4; ++c) wv[0][c] = wa[frag[0] + c * 256];
 #pragma unroll
             for (int m = 0; m < RT; ++m) xv[0][m] = xa[frag[0] + m * 256];
-            if (st + 1 < stages) ask(st + 1, (st & 1) ^ 1);
+            // The next stage is asked for between the MFMAs of the first steps (a wave
+            // that issues its loads in a row waits for the address unit, with the
+            // matrix core idle) and has at least a step left to arrive; the last stage
+            // asks for itself again.
+            const int next = min(st + 1, stages - 1), nbuf = (st & 1) ^ 1, next_pair = (st >> 1) + 1;
             __builtin_amdgcn_sched_barrier(0);
             auto step = [&](auto jc) {
                 constexpr int j = decltype(jc)::value;
-                if constexpr (j < 3) {
+                constexpr int MFMAS = 4 * RT, READS = 4 + RT, CODES = (ROW_LOADS + W_LOADS) / 2;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) wv[(j + 1) & 1][c] = wa[frag[j + 1] + c * 256];
+                for (int i = 0; i < MFMAS; ++i) {
+                    // READS operands of the next step and CODES loads, spread over the MFMAs
+                    if constexpr (j < 3) {
 #pragma unroll
-                    for (int m = 0; m < RT; ++m) xv[(j + 1) & 1][m] = xa[frag[j + 1] + m * 256];
+                        for (int k = i * READS / MFMAS; k < (i + 1) * READS / MFMAS; ++k) {
+                            if (k < 4) wv[(j + 1) & 1][k] = wa[frag[j + 1] + k * 256];
+                            else xv[(j + 1) & 1][k - 4] = xa[frag[j + 1] + (k - 4) * 256];
+                        }
+                    }
+                    if constexpr (j < 2) {
+#pragma unroll
+                        for (int k = i * CODES / MFMAS; k < (i + 1) * CODES / MFMAS; ++k) ask_codes(j * CODES + k, next, nbuf);
+                    }
+                    // half of the scales of the next two stages at each of these two
+                    if constexpr (j == 2) {
+                        constexpr int EACH = (SCALE_LOADS + 1) / 2;
+#pragma unroll
+                        for (int k = i * EACH / MFMAS; k < (i + 1) * EACH / MFMAS; ++k) {
+                            const bool odd = (st & 1) && k + EACH < SCALE_LOADS;  // the one left over is loaded twice
+                            ask_scales(odd ? k + EACH : k, odd ? so[min(k + EACH, SCALE_LOADS - 1)] : so[k], next_pair);
+                        }
+                    }
+                    acc[i / 4][i % 4] = mfma32<j>(wv[j & 1][i % 4], wsc[i % 4], xv[j & 1][i / 4], xsc[i / 4], acc[i / 4][i % 4]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-#pragma unroll
-                for (int m = 0; m < RT; ++m)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[m][c] = mfma32<j>(wv[j & 1][c], wsc[c], xv[j & 1][m], xsc[m], acc[m][c]);
-#pragma unroll
-                for (int i = 0; i < 4 + RT; ++i) {  // the next step's reads between this step's MFMAs
-                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x008, RT == 4 ? 2 : 1, 0);
-                }
-                __builtin_amdgcn_sched_barrier(0);
             };
             step(std::integral_constant<int, 0>{});
             step(std::integral_constant<int, 1>{});
             step(std::integral_constant<int, 2>{});
             step(std::integral_constant<int, 3>{});
         }
-        __builtin_amdgcn_s_barrier();  // the buffers are read
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the last stage's second copy is here
+        __builtin_amdgcn_s_barrier();        // and the buffers are read
     }
     // Results: a lane holds 4 consecutive outputs of a row.  32 rows at a time they
     // go through LDS (this wave's own part), so that a store writes 256 bytes and
