@@ -398,8 +398,8 @@ __global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int
                          in ? off : OUTSIDE, (uint32_t)pair * SPAN_BLOCKS);
         };
         // The dword of this lane's four blocks of stage st, of staged row `row`.
-        auto scales = [&](int row, int shift, int st) {
-            const uint32_t* s = lds_scales + (st >> 1 & 1) * SPAIR + row * SDW + 2 * (st & 1) + h;
+        auto scales = [&](int row, int shift, int st, int par) {  // par = st & 1
+            const uint32_t* s = lds_scales + (st >> 1 & 1) * SPAIR + row * SDW + 2 * par + h;
             if constexpr (WHOLE) return s[0];
             const int left = nb - st * STAGE_BLOCKS - 4 * h;  // the bytes of the next row, which may be NaN, give way to zeros
             const uint32_t v = __builtin_amdgcn_alignbyte(s[1], s[0], shift);
@@ -415,58 +415,76 @@ __global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int
 #pragma unroll
         for (int j = 0; j < 4; ++j) frag[j] = r * 8 + ((4 * h + j) ^ ((r >> 1) & 7));
 
+        // Operands run one step ahead, across the stages' borders: a stage's barrier
+        // comes before its last step, when that step's operands are in registers (so
+        // the buffer is free) and the next stage has landed.  From there on the last
+        // step reads the next stage's first operands and scales and asks for half of
+        // the stage after next; the next stage's first step asks for the other half.
+        // The loads go between the MFMAs: a wave that issues them in a row waits for
+        // the address unit with the matrix core idle.  Stages behind the last re-read it.
+        constexpr int MFMAS = 4 * RT, READS = 4 + RT, CODES = (ROW_LOADS + W_LOADS) / 2, EACH = (SCALE_LOADS + 1) / 2;
+        const int last = stages - 1;
+        i32x4_t xv[2][RT], wv[2][4];
+        uint32_t wsc[4], xsc[RT], wsn[4], xsn[RT];  // scales of this stage and the next
+        auto read_operand = [&](int k, int j, int par, int to) {  // operand k of step j of a stage of this parity
+            const i32x4_t* a = lds + par * STAGE + frag[j];
+            if (k < 4) wv[to][k] = a[BM * 8 + (wx * 4 + k) * 256];
+            else xv[to][k - 4] = a[(wy * RT + k - 4) * 256];
+        };
+        auto read_scale = [&](int k, int st, int par) {
+            if (k < 4) wsn[k] = scales(BM + (wx * 4 + k) * 32 + r, wshift[k], st, par);
+            else xsn[k - 4] = scales((wy * RT + k - 4) * 32 + r, xshift[k - 4], st, par);
+        };
 #pragma unroll
-        for (int k = 0; k < ROW_LOADS + W_LOADS; ++k) ask_codes(k, 0, 0);
+        for (int k = 0; k < 2 * CODES; ++k) ask_codes(k, 0, 0);
 #pragma unroll
         for (int k = 0; k < SCALE_LOADS; ++k) ask_scales(k, so[k], 0);
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = 0; k < CODES; ++k) ask_codes(k, min(1, last), 1);
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) ask_scales(k, so[k], 1);
+#pragma unroll
+        for (int k = 0; k < READS; ++k) {
+            read_operand(k, 0, 0, 0);
+            read_scale(k, 0, 0);
+        }
         for (int st = 0; st < stages; ++st) {
-            // everything asked for is here, in every wave, and the other buffer is read
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
-            uint32_t wsc[4], xsc[RT];
+            const int par = st & 1;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) wsc[c] = scales(BM + (wx * 4 + c) * 32 + r, wshift[c], st);
+            for (int c = 0; c < 4; ++c) wsc[c] = wsn[c];
 #pragma unroll
-            for (int m = 0; m < RT; ++m) xsc[m] = scales((wy * RT + m) * 32 + r, xshift[m], st);
-            const i32x4_t* xa = lds + (st & 1) * STAGE + wy * RT * 256;
-            const i32x4_t* wa = lds + (st & 1) * STAGE + BM * 8 + wx * 4 * 256;
-            i32x4_t xv[2][RT], wv[2][4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) wv[0][c] = wa[frag[0] + c * 256];
-#pragma unroll
-            for (int m = 0; m < RT; ++m) xv[0][m] = xa[frag[0] + m * 256];
-            // The next stage is asked for between the MFMAs of the first steps (a wave
-            // that issues its loads in a row waits for the address unit, with the
-            // matrix core idle) and has at least a step left to arrive; the last stage
-            // asks for itself again.
-            const int next = min(st + 1, stages - 1), nbuf = (st & 1) ^ 1, next_pair = (st >> 1) + 1;
-            __builtin_amdgcn_sched_barrier(0);
+            for (int m = 0; m < RT; ++m) xsc[m] = xsn[m];
             auto step = [&](auto jc) {
                 constexpr int j = decltype(jc)::value;
-                constexpr int MFMAS = 4 * RT, READS = 4 + RT, CODES = (ROW_LOADS + W_LOADS) / 2;
+                if constexpr (j == 3) {
+                    // this step's operands are here, the next stage has landed, in every wave
+                    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+                    __builtin_amdgcn_s_barrier();
+                    __builtin_amdgcn_sched_barrier(0);
+                }
 #pragma unroll
                 for (int i = 0; i < MFMAS; ++i) {
-                    // READS operands of the next step and CODES loads, spread over the MFMAs
-                    if constexpr (j < 3) {
 #pragma unroll
-                        for (int k = i * READS / MFMAS; k < (i + 1) * READS / MFMAS; ++k) {
-                            if (k < 4) wv[(j + 1) & 1][k] = wa[frag[j + 1] + k * 256];
-                            else xv[(j + 1) & 1][k - 4] = xa[frag[j + 1] + (k - 4) * 256];
+                    for (int k = i * READS / MFMAS; k < (i + 1) * READS / MFMAS; ++k) {
+                        read_operand(k, (j + 1) & 3, j == 3 ? par ^ 1 : par, (j + 1) & 1);
+                        if constexpr (j == 3) read_scale(k, st + 1, par ^ 1);
+                    }
+                    if constexpr (j == 0 || j == 3) {
+#pragma unroll
+                        for (int k = i * CODES / MFMAS; k < (i + 1) * CODES / MFMAS; ++k) {
+                            if (j == 3) ask_codes(k, min(st + 2, last), par);
+                            else ask_codes(CODES + k, min(st + 1, last), par ^ 1);
                         }
                     }
-                    if constexpr (j < 2) {
-#pragma unroll
-                        for (int k = i * CODES / MFMAS; k < (i + 1) * CODES / MFMAS; ++k) ask_codes(j * CODES + k, next, nbuf);
-                    }
-                    // half of the scales of the next two stages at each of these two
-                    if constexpr (j == 2) {
-                        constexpr int EACH = (SCALE_LOADS + 1) / 2;
+                    if constexpr (j == 3) {
+                        // scales of pair p + 1: one half at stage 2p - 1, the other at 2p
 #pragma unroll
                         for (int k = i * EACH / MFMAS; k < (i + 1) * EACH / MFMAS; ++k) {
-                            const bool odd = (st & 1) && k + EACH < SCALE_LOADS;  // the one left over is loaded twice
-                            ask_scales(odd ? k + EACH : k, odd ? so[min(k + EACH, SCALE_LOADS - 1)] : so[k], next_pair);
+                            constexpr int end = SCALE_LOADS - 1;
+                            ask_scales(par ? k : min(EACH + k, end), par ? so[k] : so[EACH + k < end ? EACH + k : end], ((st + 1) >> 1) + 1);
                         }
                     }
                     acc[i / 4][i % 4] = mfma32<j>(wv[j & 1][i % 4], wsc[i % 4], xv[j & 1][i / 4], xsc[i / 4], acc[i / 4][i % 4]);
