@@ -15,6 +15,20 @@ namespace mx {
 // magnitude is a maximum over the quad (two DPP moves), then each lane converts
 // its own values to one dword of codes, so codes leave a wave as 256 consecutive
 // bytes.
+template <typename T> __device__ inline uint32_t quantize_quad(const uint32_t (&w)[2 * T::bytes], uint32_t& b) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 2 * T::bytes; ++e) m = abs_max<T>(m, w[e]);
+    uint32_t a = abs_max_f32_bits<T>(m);
+    uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0xB1, 0xF, 0xF, true);  // lanes 1 0 3 2
+    a = a > o ? a : o;
+    o = (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x4E, 0xF, 0xF, true);  // lanes 2 3 0 1
+    a = a > o ? a : o;
+    b = scale_byte(a);
+    const uint32_t c = cvt8<T>(w, scale_value(b));
+    return b == 255u ? 0u : c;
+}
+
 constexpr int QUANT_UNROLL = 4;
 
 template <typename T, bool FLAT>
@@ -45,17 +59,8 @@ __global__ __launch_bounds__(256) void quantize_kernel(const void* __restrict__ 
     for (int u = 0; u < QUANT_UNROLL; ++u) {
         const int64_t i = base + u * 256;
         if (i >= units) continue;  // whole quads: units is a multiple of 4
-        uint32_t m = 0;
-#pragma unroll
-        for (int e = 0; e < NW; ++e) m = abs_max<T>(m, w[u][e]);
-        uint32_t a = abs_max_f32_bits<T>(m);
-        uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0xB1, 0xF, 0xF, true);  // lanes 1 0 3 2
-        a = a > o ? a : o;
-        o = (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x4E, 0xF, 0xF, true);  // lanes 2 3 0 1
-        a = a > o ? a : o;
-        const uint32_t b = scale_byte(a);
-        const uint32_t c = cvt8<T>(w[u], scale_value(b));
-        codes[i] = b == 255u ? 0u : c;
+        uint32_t b;
+        codes[i] = quantize_quad<T>(w[u], b);
         if ((i & 3) == 0) scales[i >> 2] = (uint8_t)b;
     }
 }
@@ -123,43 +128,19 @@ struct ProductParams {
     void* y;
 };
 
-// This lane's four scales of a span: bytes at s[0..3], `left` of them in the row
-// (others read as 1).  whole: every row has a multiple of 4 blocks, so the dword
-// is aligned and all in the row or all behind it.
-__device__ inline uint32_t load_scales(const uint8_t* s, int left, bool whole) {
-    uint32_t v = UNIT_SCALES;
-    if (whole) {
-        if (left > 0) v = *reinterpret_cast<const uint32_t*>(s);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < left) v = (v & ~(0xFFu << (8 * j))) | ((uint32_t)s[j] << (8 * j));
-    }
-    return v;
+// Memory from `base` on, read at 32-bit offsets.
+__device__ inline __amdgpu_buffer_rsrc_t buffer(const uint8_t* base, int64_t bytes) {
+    const uint32_t n = bytes > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)bytes;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, n, 0x00020000);
 }
-// This lane's four blocks of codes, zeros behind the row's end.
-__device__ inline void load_codes(const uint8_t* c, int left, i32x4_t (&v)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[j] = i32x4_t{0, 0, 0, 0};
-        if (j < left) v[j] = reinterpret_cast<const i32x4_t*>(c)[j];
-    }
+// Straight into LDS: lane l's 16 bytes at dst + 16 l.
+__device__ inline void load16_to_lds(__amdgpu_buffer_rsrc_t b, i32x4_t* dst, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)dst, 16, voff, soff, 0, 0);
 }
+constexpr uint32_t OUTSIDE = 0x7FFFFFF0u;  // an offset past every buffer: the load gives zeros
 
-// One block of 32 values to an operand: its 16 bytes of codes and scale byte.
-template <typename T> __device__ inline i32x4_t quantize_block(const uint32_t (&w)[8 * T::bytes], uint32_t& b) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < 8 * T::bytes; ++e) m = abs_max<T>(m, w[e]);
-    b = scale_byte(abs_max_f32_bits<T>(m));
-    const float s = scale_value(b);
-    i32x4_t c;
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        const uint32_t v = cvt8<T>(w + d * 2 * T::bytes, s);
-        c[d] = b == 255u ? 0 : (int)v;
-    }
-    return c;
+__device__ inline void load4_to_lds(__amdgpu_buffer_rsrc_t b, uint32_t* dst, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)dst, 4, voff, soff, 0, 0);
 }
 
 template <typename OT> __device__ inline void store4(void* y, int64_t at, int count, bool vec, const f32x4_t v) {
@@ -181,97 +162,357 @@ template <typename OT> __device__ inline void store4(void* y, int64_t at, int co
     }
 }
 
-// Few rows: a workgroup owns 16 NS outputs for a tile of 16 MT rows; its W waves
-// share the spans of the input (wave w takes spans w, w + W, ...) and read the
-// weight from memory straight into the operand, once.  The rows come quantised,
-// or (FUSED) as values that each lane quantises into the operand it needs: a
-// lane's block is its own, so this takes no exchange.  The waves' sums meet in
-// LDS and are added in the order of the waves.
-template <typename OT, bool FUSED, int MT, int NS, int W>
-__global__ __launch_bounds__(W * 64) void skinny_kernel(const ProductParams p) {
-    __shared__ f32x4_t red[W][NS * MT][64];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
-    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, blockIdx.y, 16 * MT);
-    if (t.rows == 0) return;
-    const int n0 = blockIdx.x * 16 * NS;
-    const int nb = p.n_in / BLOCK, spans = (nb + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
-    const bool whole = (nb & 3) == 0, vec = (p.n_out & 3) == 0;
+// Dwords of scales that a row of a span holds in LDS: its 16 bytes, or where rows
+// start at any byte (WHOLE false: n_in % 128 != 0) the aligned dwords around them.
+template <bool WHOLE> constexpr int SCALE_DWORDS = WHOLE ? 4 : 8;
 
-    f32x4_t acc[NS][MT];
+// Four scale bytes out of staged dwords: s[0], or with a row that starts `shift`
+// bytes into a dword s[0] and s[1].  `left` blocks of the row are left from the
+// first of these on; bytes of the next row, which may stand for NaN, give way to zeros.
+template <bool WHOLE> __device__ inline uint32_t staged_scales(const uint32_t* s, uint32_t shift, int left) {
+    if constexpr (WHOLE) return s[0];
+    const uint32_t v = __builtin_amdgcn_alignbyte(s[1], s[0], shift);
+    return left >= 4 ? v : (left > 0 ? v & ((1u << (8 * left)) - 1u) : 0u);
+}
+// The offset of dword `dw` of a span's staged scales, or OUTSIDE behind the row's end.
+template <bool WHOLE> __device__ inline uint32_t scale_offset(uint32_t row_first, int dw, int span, int nb) {
+    return span * SPAN_BLOCKS + 4 * dw < nb + (WHOLE ? 0 : 4) ? (row_first & ~3u) + 4 * dw : OUTSIDE;
+}
+
+// A tile of one side of a product: codes and scales of `rows` rows from row
+// `first` of a matrix of nb blocks a row.
+struct Side {
+    __amdgpu_buffer_rsrc_t codes, scales;
+    uint32_t lead;  // bytes from the scale buffer's 16-byte border to the first row's
+    int rows;
+};
+__device__ inline Side side(const uint8_t* codes, const uint8_t* scales, int64_t first, int rows, int nb) {
+    const int64_t at = first * nb;
+    return Side{buffer(codes + at * 16, (int64_t)rows * nb * 16),
+                buffer(scales + (at & ~int64_t(15)), ((at & 15) + (int64_t)rows * nb + 3) & ~int64_t(3)), (uint32_t)(at & 15), rows};
+}
+
+// Few rows: a workgroup of eight waves owns 16 outputs for up to 16 rows, wave w
+// the spans w, w + 8, ... of the input.  Each wave brings its spans of the weight
+// straight into a ring of its own in LDS, four rows of 256 bytes a load, and
+// waits for nobody (a weight operand read from memory by its lanes would be 64
+// places for 1 KB, 64 cycles of the address unit instead of 16).  The rows come
+// quantised, the same way, or (FUSED) as values, which the workgroup quantises
+// into LDS while the weight is on its way: FUSED_ROW_SPANS spans of them, all rows
+// together, so that two workgroups fit a CU.  The waves' sums meet in LDS and are
+// added in the order of the waves.
+//
+// Block b of row r sits in 16-byte slot b ^ swizzle(r): the 16 lanes that LDS
+// serves together (rows 0-3 and 12-15 of one quarter, 4-11 of the next) then
+// read 16 different slots of its 256-byte width.
+constexpr int SMALL_WAVES = 8, SMALL_RING = 2, SMALL_MAX_ROWS = 16;
+constexpr int FUSED_ROW_SPANS = 32;
+// Rows of a tile that quantises them itself (0: none fits).
+__host__ __device__ inline int fused_rows(int n_in) {
+    const int rows = FUSED_ROW_SPANS / ((n_in + SPAN_BLOCKS * BLOCK - 1) / (SPAN_BLOCKS * BLOCK));
+    return rows < SMALL_MAX_ROWS ? rows : SMALL_MAX_ROWS;
+}
+
+__device__ inline int small_swizzle(int row) {  // rows / 4: 0 1 2 3 -> 0 2 3 1
+    return (row & 3) | (((0x78 >> (row >> 2 << 1)) & 3) << 2);
+}
+
+template <typename OT, bool FUSED, bool WHOLE>
+__global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductParams p) {
+    constexpr int SDW = SCALE_DWORDS<WHOLE>, SIDES = FUSED ? 1 : 2, LOADS = SIDES * (4 + SDW / 4);
+    constexpr int BUF = SIDES * (256 + 4 * SDW);  // slots: codes of each side, then scales
+    constexpr int RING = SMALL_WAVES * SMALL_RING * BUF;
+    __shared__ i32x4_t lds[RING + (FUSED ? FUSED_ROW_SPANS * 17 : 0)];  // and the quantised rows: codes, scales
+    static_assert(SMALL_RING * BUF >= 64, "the sums of a wave fit its ring");
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
+    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, blockIdx.y, FUSED ? fused_rows(p.n_in) : SMALL_MAX_ROWS);
+    if (t.rows == 0) return;
+    const int n0 = blockIdx.x * 16, cols = min(16, p.n_out - n0);
+    const int nb = p.n_in / BLOCK, spans = (nb + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
+    i32x4_t* const ring = lds + wave * SMALL_RING * BUF;
+
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    if (t.group < p.n_groups) {
+        const int mine = (spans - wave + SMALL_WAVES - 1) / SMALL_WAVES;  // spans of this wave (none: 0 or less)
+        Side sides[SIDES];
+        sides[0] = side(p.wc, p.ws, (int64_t)t.group * p.n_out + n0, cols, nb);
+        if constexpr (!FUSED) sides[1] = side(p.xc, p.xs, t.row0, t.rows, nb);
+        uint32_t row_at[SIDES][4], scale_at[SIDES][SDW / 4], shift[SIDES];
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
+        for (int s = 0; s < SIDES; ++s) {
+            // load i: row 4 i + lane / 16, slot lane % 16; rows behind the tile re-read its last
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[s][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < 4; ++i) row_at[s][i] = (uint32_t)min(4 * i + (lane >> 4), sides[s].rows - 1) * (nb * 16);
+#pragma unroll
+            for (int i = 0; i < SDW / 4; ++i)
+                scale_at[s][i] = (uint32_t)min(i * (64 / SDW) + lane / SDW, sides[s].rows - 1) * nb + sides[s].lead;
+            shift[s] = ((uint32_t)min(r, sides[s].rows - 1) * nb + sides[s].lead) & 3u;
+        }
+        // The loads of this wave's kth span; behind its last they give zeros.
+        auto ask = [&](int k) {
+            const int sp = k < mine ? wave + k * SMALL_WAVES : spans;
+            i32x4_t* const buf = ring + k % SMALL_RING * BUF;
+#pragma unroll
+            for (int s = 0; s < SIDES; ++s) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int block = (lane & 15) ^ small_swizzle(4 * i + (lane >> 4));
+                    load16_to_lds(sides[s].codes, buf + s * 256 + i * 64, sp * SPAN_BLOCKS + block < nb ? row_at[s][i] + 16 * block : OUTSIDE,
+                                  (uint32_t)sp * 256);
+                }
+#pragma unroll
+                for (int i = 0; i < SDW / 4; ++i)
+                    load4_to_lds(sides[s].scales, reinterpret_cast<uint32_t*>(buf + SIDES * 256 + s * 4 * SDW) + i * 64,
+                                 scale_offset<WHOLE>(scale_at[s][i], lane % SDW, sp, nb), (uint32_t)sp * SPAN_BLOCKS);
+            }
+        };
+        auto scales = [&](int s, int k, int left) {
+            const uint32_t* at = reinterpret_cast<const uint32_t*>(ring + k % SMALL_RING * BUF + SIDES * 256 + s * 4 * SDW);
+            return staged_scales<WHOLE>(at + r * SDW + q, shift[s], left);
+        };
+        auto operand = [&](int s, int k, int j) { return ring[k % SMALL_RING * BUF + s * 256 + r * 16 + ((4 * q + j) ^ small_swizzle(r))]; };
+        i32x4_t* const xq = lds + RING;  // [row][spans * 16], block b of row r at b ^ small_swizzle(r)
+        uint8_t* const xq_scales = reinterpret_cast<uint8_t*>(xq + FUSED_ROW_SPANS * 16);
+#pragma unroll
+        for (int k = 0; k < SMALL_RING; ++k) ask(k);
+        if constexpr (FUSED) {
+            // eight values a thread and round, four threads a block, as quantize_kernel
+            constexpr int THREADS = SMALL_WAVES * 64, ROUNDS = FUSED_ROW_SPANS * 64 / THREADS, NW = 2 * OT::bytes;
+            const int per_row = spans * 64, units = t.rows * per_row;
+            uint32_t w[ROUNDS][NW];
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                const int u = i * THREADS + threadIdx.x, row = u / per_row, at = u - row * per_row;
+#pragma unroll
+                for (int e = 0; e < NW; ++e) w[i][e] = 0;
+                if (u < units && at < nb * 4) {
+                    const u32x4_t* src = reinterpret_cast<const u32x4_t*>(static_cast<const char*>(p.x) + ((int64_t)(t.row0 + row) * p.ldx + 8 * at) * OT::bytes);
+#pragma unroll
+                    for (int c = 0; c < NW / 4; ++c) {
+                        const u32x4_t v = src[c];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[i][4 * c + e] = v[e];
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                const int u = i * THREADS + threadIdx.x, row = u / per_row, at = u - row * per_row;
+                if (u < units) {  // whole quads
+                    uint32_t b;
+                    const uint32_t c = quantize_quad<OT>(w[i], b);
+                    const int slot = row * spans * 16 + ((at >> 2) ^ small_swizzle(row));
+                    reinterpret_cast<uint32_t*>(xq + slot)[at & 3] = c;
+                    if ((at & 3) == 0) xq_scales[row * spans * 16 + (at >> 2)] = (uint8_t)b;
+                }
+            }
+            __syncthreads();
+        }
+        for (int k = 0; k < mine; ++k) {
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(0x0F70 | ((SMALL_RING - 1) * LOADS & 15) | (((SMALL_RING - 1) * LOADS >> 4) << 14));  // vmcnt
+            __builtin_amdgcn_sched_barrier(0);
+            const int sp = wave + k * SMALL_WAVES, left = nb - sp * SPAN_BLOCKS - 4 * q;
+            i32x4_t wv[4], xv[4];
+            uint32_t xsc;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) wv[j] = operand(0, k, j);
+            const uint32_t wsc = scales(0, k, left);
+            if constexpr (FUSED) {
+                const int row = min(r, t.rows - 1);  // rows behind the tile re-read its last
+#pragma unroll
+                for (int j = 0; j < 4; ++j) xv[j] = xq[(row * spans + sp) * 16 + ((4 * q + j) ^ small_swizzle(row))];
+                xsc = reinterpret_cast<const uint32_t*>(xq_scales)[(row * spans + sp) * 4 + q];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) xv[j] = operand(1, k, j);
+                xsc = scales(1, k, left);
+            }
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the buffer is read
+            __builtin_amdgcn_sched_barrier(0);
+            ask(k + SMALL_RING);
+            acc = mfma<0>(wv[0], wsc, xv[0], xsc, acc);
+            acc = mfma<1>(wv[1], wsc, xv[1], xsc, acc);
+            acc = mfma<2>(wv[2], wsc, xv[2], xsc, acc);
+            acc = mfma<3>(wv[3], wsc, xv[3], xsc, acc);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): nothing is on its way into LDS any more
+    }
+    // each wave's sums over its own ring
+    ring[lane] = __builtin_bit_cast(i32x4_t, acc);
+    __syncthreads();
+    if (wave == 0) {
+        f32x4_t v = acc;
+#pragma unroll
+        for (int w = 1; w < SMALL_WAVES; ++w) v += __builtin_bit_cast(f32x4_t, lds[w * SMALL_RING * BUF + lane]);
+        const int o = n0 + 4 * q;
+        if (r < t.rows && o < p.n_out) store4<OT>(p.y, (int64_t)(t.row0 + r) * p.n_out + o, p.n_out - o, (p.n_out & 3) == 0, v);
+    }
+}
+
+// Workgroup b of a launch to tile index: units of 32 consecutive tiles go to the
+// same XCD (workgroups go round the 8 XCDs one by one), so that the tiles that
+// run together on an XCD share rows and weights in its L2.
+constexpr int XCDS = 8, XCD_UNIT = 32;
+__device__ inline int xcd_tile(int b) {
+    const int xcd = b % XCDS, local = b / XCDS;
+    return (local / XCD_UNIT * XCDS + xcd) * XCD_UNIT + local % XCD_UNIT;
+}
+// Tiles of a launch, padded to whole rounds of units.
+inline int64_t xcd_padded(int64_t tiles) { return (tiles + XCDS * XCD_UNIT - 1) / (XCDS * XCD_UNIT) * (XCDS * XCD_UNIT); }
+constexpr int BAND = 8;  // row tiles that share a run of output tiles
+// Row tile and output tile of a tile index: bands of BAND row tiles, an output
+// tile's row tiles after each other.  False behind the last tile.
+__device__ inline bool tile_of(int tile, int row_tiles, int col_tiles, int* row, int* col) {
+    const int band = tile / (BAND * col_tiles), height = min(BAND, row_tiles - band * BAND);
+    if (height <= 0) return false;
+    const int in_band = tile - band * BAND * col_tiles;
+    *col = in_band / height;
+    *row = band * BAND + in_band - *col * height;
+    return *col < col_tiles;
+}
+
+// A wave's results, 32 RT rows from `row0` and 32 CT outputs from `col0`, of which
+// `rows` rows are written.  A lane holds 4 consecutive outputs of a row; 32 rows
+// at a time they go through LDS (`part`, the wave's own), so that a store writes
+// whole pieces of a row, 64 CT bytes and more.
+template <typename OT, int CT> constexpr int store_part_bytes() { return 32 * (32 * CT * OT::bytes + 16); }
+
+template <typename OT, int RT, int CT>
+__device__ inline void store_tile(const f32x16_t (&acc)[RT][CT], char* part, const ProductParams& p, int row0, int rows, int col0) {
+    typedef typename OT::raw raw;
+    constexpr int PITCH = 32 * CT * OT::bytes + 16;
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    const int cols = min(32 * CT, p.n_out - col0);
+    const bool vec = ((int64_t)p.n_out * OT::bytes) % 16 == 0;
+    raw* y = static_cast<raw*>(p.y);
+#pragma unroll
+    for (int m = 0; m < RT; ++m) {
+        const int live = min(32, rows - 32 * m);
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4_t v = {acc[m][c][4 * g], acc[m][c][4 * g + 1], acc[m][c][4 * g + 2], acc[m][c][4 * g + 3]};
+                store4<OT>(part + r * PITCH, 32 * c + 8 * g + 4 * h, 4, true, v);
+            }
+        __builtin_amdgcn_wave_barrier();
+        const int64_t y0 = (int64_t)(row0 + 32 * m) * p.n_out + col0;
+        if (vec) {
+            constexpr int PER = 16 / OT::bytes, LANES = 32 * CT / PER;  // outputs of a lane, lanes of a row
+#pragma unroll
+            for (int i = 0; i < 32; i += 64 / LANES) {
+                const int row = i + lane / LANES, o = lane % LANES * PER;
+                const i32x4_t v = *reinterpret_cast<const i32x4_t*>(part + row * PITCH + o * OT::bytes);
+                if (row < live && o < cols) *reinterpret_cast<i32x4_t*>(y + y0 + (int64_t)row * p.n_out + o) = v;
+            }
+        } else {
+            for (int i = lane; i < live * 32 * CT; i += 64) {
+                const int row = i / (32 * CT), o = i % (32 * CT);
+                const raw v = reinterpret_cast<const raw*>(part + row * PITCH)[o];
+                if (o < cols) y[y0 + (int64_t)row * p.n_out + o] = v;
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// Some rows, or few tiles: a workgroup of four waves owns 64 rows and 64 outputs,
+// each wave a quarter.  Stages of a span (256 bytes of codes a row of both sides)
+// go straight into a ring in LDS, MEDIUM_RING - 1 of them ahead: a stage is
+// little work (8 MFMAs a wave), so it is the bytes in flight that count.  Block b
+// of row r sits in slot b ^ (r & 15) of the row's 256 bytes.
+constexpr int MEDIUM_RING = 4;
+
+template <typename OT, bool WHOLE>
+__global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int row_tiles, int col_tiles) {
+    constexpr int SDW = SCALE_DWORDS<WHOLE>, LOADS = 8 + SDW / 2;
+    constexpr int BUF = 128 * 16 + 128 * SDW / 4;  // slots: codes (64 rows, 64 weight rows), then scales
+    static_assert(store_part_bytes<OT, 1>() * 4 <= MEDIUM_RING * BUF * 16, "the waves' parts fit");
+    __shared__ i32x4_t lds[MEDIUM_RING * BUF];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 31, h = lane >> 5, wy = wave >> 1, wx = wave & 1;
+    int row_tile, col;
+    if (!tile_of(xcd_tile(blockIdx.x), row_tiles, col_tiles, &row_tile, &col)) return;
+    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, row_tile, 64);
+    if (t.rows == 0) return;
+    const int n0 = col * 64, cols = min(64, p.n_out - n0);
+    const int nb = p.n_in / BLOCK, stages = (nb + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
+
+    f32x16_t acc[1][1];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[0][0][i] = 0.f;
 
     if (t.group < p.n_groups) {
-        const uint8_t *wc[NS], *ws[NS];
+        const Side sides[2] = {side(p.xc, p.xs, t.row0, t.rows, nb),
+                               side(p.wc, p.ws, (int64_t)t.group * p.n_out + n0, cols, nb)};
+        // load i of a wave and side: row 16 i + 4 wave + lane / 16, slot lane % 16; rows behind the tile re-read its last
+        const int srow = 4 * wave + (lane >> 4), block = (lane & 15) ^ srow;
+        uint32_t row_at[2][4], scale_at[2][SDW / 4], shift[2];
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            const int64_t o = (int64_t)t.group * p.n_out + min(n0 + 16 * s + r, p.n_out - 1);
-            wc[s] = p.wc + o * (p.n_in / 2) + 64 * q;
-            ws[s] = p.ws + o * nb + 4 * q;
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) row_at[s][i] = (uint32_t)min(16 * i + srow, sides[s].rows - 1) * (nb * 16) + 16 * block;
+#pragma unroll
+            for (int i = 0; i < SDW / 4; ++i)
+                scale_at[s][i] = (uint32_t)min((4 * i + wave) * (64 / SDW) + lane / SDW, sides[s].rows - 1) * nb + sides[s].lead;
+            shift[s] = ((uint32_t)min((s ? wx : wy) * 32 + r, sides[s].rows - 1) * nb + sides[s].lead) & 3u;
         }
-        for (int sp = wave; sp < spans; sp += W) {
-            const int left = nb - sp * SPAN_BLOCKS - 4 * q;
-            i32x4_t wv[NS][4];
-            uint32_t wsc[NS];
+        auto ask = [&](int st) {  // behind the last stage: zeros
+            i32x4_t* const buf = lds + st % MEDIUM_RING * BUF;
 #pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                load_codes(wc[s] + sp * 256, left, wv[s]);
-                wsc[s] = load_scales(ws[s] + sp * 16, left, whole);
+            for (int s = 0; s < 2; ++s) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    load16_to_lds(sides[s].codes, buf + s * 1024 + i * 256 + wave * 64, st * SPAN_BLOCKS + block < nb ? row_at[s][i] : OUTSIDE,
+                                  (uint32_t)st * 256);
+#pragma unroll
+                for (int i = 0; i < SDW / 4; ++i)
+                    load4_to_lds(sides[s].scales, reinterpret_cast<uint32_t*>(buf + 2048 + s * 16 * SDW) + (4 * i + wave) * 64,
+                                 scale_offset<WHOLE>(scale_at[s][i], lane % SDW, st, nb), (uint32_t)st * SPAN_BLOCKS);
             }
+        };
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int row = t.row0 + 16 * m + r;
-                const bool live = 16 * m + r < t.rows;
-                i32x4_t xv[4];
-                uint32_t xsc = UNIT_SCALES;
-                if constexpr (FUSED) {
-                    const char* x = static_cast<const char*>(p.x) + ((int64_t)row * p.ldx + sp * 512 + 128 * q) * OT::bytes;
+        for (int k = 0; k < MEDIUM_RING - 1; ++k) ask(k);
+        for (int st = 0; st < stages; ++st) {
+            // this stage has landed in every wave, and the one before it is read
+            constexpr int PENDING = (MEDIUM_RING - 2) * LOADS;
+            static_assert(PENDING < 64, "a wait counts to 63");
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(0x0070 | (PENDING & 15) | ((PENDING >> 4) << 14));  // lgkmcnt(0), vmcnt(PENDING)
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            ask(st + MEDIUM_RING - 1);
+            const i32x4_t* const buf = lds + st % MEDIUM_RING * BUF;
+            const uint32_t* const xs = reinterpret_cast<const uint32_t*>(buf + 2048) + (wy * 32 + r) * SDW + 2 * h;
+            const uint32_t* const ws = reinterpret_cast<const uint32_t*>(buf + 2048 + 16 * SDW) + (wx * 32 + r) * SDW + 2 * h;
+            const int left = nb - st * SPAN_BLOCKS - 8 * h;
+            uint32_t xsc[2], wsc[2];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        xv[j] = i32x4_t{0, 0, 0, 0};
-                        if (live && j < left) {
-                            uint32_t w[8 * OT::bytes];
-#pragma unroll
-                            for (int c = 0; c < 2 * OT::bytes; ++c) {
-                                const u32x4_t v = reinterpret_cast<const u32x4_t*>(x + j * BLOCK * OT::bytes)[c];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) w[4 * c + e] = v[e];
-                            }
-                            uint32_t b;
-                            xv[j] = quantize_block<OT>(w, b);
-                            xsc = (xsc & ~(0xFFu << (8 * j))) | (b << (8 * j));
-                        }
-                    }
-                } else {
-                    const int xleft = live ? left : 0;
-                    load_codes(p.xc + (int64_t)row * (p.n_in / 2) + sp * 256 + 64 * q, xleft, xv);
-                    xsc = load_scales(p.xs + (int64_t)row * nb + sp * 16 + 4 * q, xleft, whole);
-                }
-#pragma unroll
-                for (int s = 0; s < NS; ++s) {
-                    acc[s][m] = mfma<0>(wv[s][0], wsc[s], xv[0], xsc, acc[s][m]);
-                    acc[s][m] = mfma<1>(wv[s][1], wsc[s], xv[1], xsc, acc[s][m]);
-                    acc[s][m] = mfma<2>(wv[s][2], wsc[s], xv[2], xsc, acc[s][m]);
-                    acc[s][m] = mfma<3>(wv[s][3], wsc[s], xv[3], xsc, acc[s][m]);
-                }
+            for (int e = 0; e < 2; ++e) {
+                xsc[e] = staged_scales<WHOLE>(xs + e, shift[0], left - 4 * e);
+                wsc[e] = staged_scales<WHOLE>(ws + e, shift[1], left - 4 * e);
             }
+            auto step = [&](auto jc) {
+                constexpr int j = decltype(jc)::value;  // block 8 h + j of this half's
+                const int slot = (8 * h + j) ^ (r & 15);
+                const i32x4_t xv = buf[(wy * 32 + r) * 16 + slot], wv = buf[1024 + (wx * 32 + r) * 16 + slot];
+                acc[0][0] = mfma32<j & 3>(wv, wsc[j >> 2], xv, xsc[j >> 2], acc[0][0]);
+            };
+            step(std::integral_constant<int, 0>{});
+            step(std::integral_constant<int, 1>{});
+            step(std::integral_constant<int, 2>{});
+            step(std::integral_constant<int, 3>{});
+            step(std::integral_constant<int, 4>{});
+            step(std::integral_constant<int, 5>{});
+            step(std::integral_constant<int, 6>{});
+            step(std::integral_constant<int, 7>{});
         }
+        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0): nothing is on its way, the ring is read
+        __builtin_amdgcn_s_barrier();
     }
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) red[wave][s * MT + m][lane] = acc[s][m];
-    __syncthreads();
-    for (int i = threadIdx.x; i < NS * MT * 64; i += W * 64) {
-        const int l = i & 63, sm = i >> 6, s = sm / MT, m = sm - s * MT;
-        f32x4_t v = red[0][sm][l];
-#pragma unroll
-        for (int w = 1; w < W; ++w) v += red[w][sm][l];
-        const int row = 16 * m + (l & 15), o = n0 + 16 * s + 4 * (l >> 4);
-        if (row < t.rows && o < p.n_out) store4<OT>(p.y, (int64_t)(t.row0 + row) * p.n_out + o, p.n_out - o, vec, v);
-    }
+    constexpr int PART = store_part_bytes<OT, 1>();
+    store_tile<OT, 1, 1>(acc, reinterpret_cast<char*>(lds) + wave * PART, p, t.row0 + wy * 32, t.rows - wy * 32, n0 + wx * 32);
 }
 
 // Many rows: a workgroup of four waves owns 64 RT rows and 256 outputs, each wave
@@ -293,36 +534,6 @@ __global__ __launch_bounds__(W * 64) void skinny_kernel(const ProductParams p) {
 // Where rows start at any byte (WHOLE false: n_in % 128 != 0) the eight aligned
 // dwords that hold them are staged and two of them meet in an alignbyte.
 
-// Workgroup b of a launch to tile index: units of 32 consecutive tiles go to the
-// same XCD (workgroups go round the 8 XCDs one by one), so that the tiles that
-// run together on an XCD share rows and weights in its L2.
-constexpr int XCDS = 8, XCD_UNIT = 32;
-__device__ inline int xcd_tile(int b) {
-    const int xcd = b % XCDS, local = b / XCDS;
-    return (local / XCD_UNIT * XCDS + xcd) * XCD_UNIT + local % XCD_UNIT;
-}
-// Tiles of a launch, padded to whole rounds of units.
-inline int64_t xcd_padded(int64_t tiles) { return (tiles + XCDS * XCD_UNIT - 1) / (XCDS * XCD_UNIT) * (XCDS * XCD_UNIT); }
-constexpr int BAND = 8;  // row tiles that share a run of output tiles
-
-// Memory from `base` on, read at 32-bit offsets.
-__device__ inline __amdgpu_buffer_rsrc_t buffer(const uint8_t* base, int64_t bytes) {
-    const uint32_t n = bytes > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)bytes;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, n, 0x00020000);
-}
-__device__ inline i32x4_t load16(__amdgpu_buffer_rsrc_t b, uint32_t voff, uint32_t soff) {
-    return __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(b, voff, soff, 0));
-}
-// Straight into LDS: lane l's 16 bytes at dst + 16 l.
-__device__ inline void load16_to_lds(__amdgpu_buffer_rsrc_t b, i32x4_t* dst, uint32_t voff, uint32_t soff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)dst, 16, voff, soff, 0, 0);
-}
-constexpr uint32_t OUTSIDE = 0x7FFFFFF0u;  // an offset past every buffer: the load gives zeros
-
-__device__ inline void load4_to_lds(__amdgpu_buffer_rsrc_t b, uint32_t* dst, uint32_t voff, uint32_t soff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)dst, 4, voff, soff, 0, 0);
-}
-
 constexpr int STAGE_BLOCKS = 8;
 
 template <typename OT, int RT, bool WHOLE>
@@ -336,13 +547,9 @@ __global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int
     uint32_t* const lds_scales = reinterpret_cast<uint32_t*>(lds + 2 * STAGE);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 31, h = lane >> 5, wy = wave >> 1, wx = wave & 1;
-    const int tile = xcd_tile(blockIdx.x);
-    const int band = tile / (BAND * col_tiles), band_rows = min(BAND, row_tiles - band * BAND);
-    if (band_rows <= 0) return;
-    const int in_band = tile - band * BAND * col_tiles;
-    const int col = in_band / band_rows;
-    if (col >= col_tiles) return;
-    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, band * BAND + in_band - col * band_rows, BM);
+    int row_tile, col;
+    if (!tile_of(xcd_tile(blockIdx.x), row_tiles, col_tiles, &row_tile, &col)) return;
+    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, row_tile, BM);
     if (t.rows == 0) return;
     const int n0 = col * BN, cols = min(BN, p.n_out - n0);
     const int nb = p.n_in / BLOCK, stages = (nb + STAGE_BLOCKS - 1) / STAGE_BLOCKS;
@@ -499,46 +706,9 @@ __global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the last stage's second copy is here
         __builtin_amdgcn_s_barrier();        // and the buffers are read
     }
-    // Results: a lane holds 4 consecutive outputs of a row.  32 rows at a time they
-    // go through LDS (this wave's own part), so that a store writes 256 bytes and
-    // more of a row.
-    constexpr int PITCH = 128 * OT::bytes + 16;
-    static_assert(4 * 32 * PITCH <= (int)sizeof(lds), "the waves' parts fit");
-    char* part = reinterpret_cast<char*>(lds) + wave * 32 * PITCH;
-    const int wcols = min(128, cols - wx * 128);
-    const bool vec = (p.n_out * OT::bytes) % 16 == 0;
-#pragma unroll
-    for (int m = 0; m < RT; ++m) {
-        const int mrow = (wy * RT + m) * 32, live = min(32, t.rows - mrow);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const f32x4_t v = {acc[m][c][4 * g], acc[m][c][4 * g + 1], acc[m][c][4 * g + 2], acc[m][c][4 * g + 3]};
-                store4<OT>(part + r * PITCH, 32 * c + 8 * g + 4 * h, 4, true, v);
-            }
-        __builtin_amdgcn_wave_barrier();
-        const int64_t y0 = (int64_t)(t.row0 + mrow) * p.n_out + n0 + wx * 128;
-        typedef typename OT::raw raw;
-        raw* y = static_cast<raw*>(p.y);
-        if (vec) {
-            constexpr int PER = 16 / OT::bytes, LANES = 128 / PER;  // outputs of a lane, lanes of a row
-#pragma unroll
-            for (int i = 0; i < 32; i += 64 / LANES) {
-                const int row = i + lane / LANES, o = lane % LANES * PER;
-                const i32x4_t v = *reinterpret_cast<const i32x4_t*>(part + row * PITCH + o * OT::bytes);
-                if (row < live && o < wcols) *reinterpret_cast<i32x4_t*>(y + y0 + (int64_t)row * p.n_out + o) = v;
-            }
-        } else {
-            for (int row = 0; row < live; ++row)
-#pragma unroll
-                for (int o = 0; o < 128; o += 64) {
-                    const raw v = reinterpret_cast<const raw*>(part + row * PITCH)[o + lane];
-                    if (o + lane < wcols) y[y0 + (int64_t)row * p.n_out + o + lane] = v;
-                }
-        }
-        __builtin_amdgcn_wave_barrier();
-    }
+    constexpr int PART = store_part_bytes<OT, 4>();
+    static_assert(4 * PART <= (int)sizeof(lds), "the waves' parts fit");
+    store_tile<OT, RT, 4>(acc, reinterpret_cast<char*>(lds) + wave * PART, p, t.row0 + wy * RT * 32, t.rows - wy * RT * 32, n0 + wx * 128);
 }
 
 // ---- launches ----
@@ -554,38 +724,51 @@ template <typename T> hipError_t launch_quantize(const void* x, int64_t rows, in
     return hipGetLastError();
 }
 
-// Rows above which the staged product takes over from the few-rows one.
-constexpr int SKINNY_MAX_ROWS = 64;
+// Rows that a group has on average: what a tile's height is chosen by.
+inline int64_t typical_rows(int64_t rows, int n_groups) { return (rows + n_groups - 1) / n_groups; }
 
-template <typename OT, bool FUSED, int MT, int NS> hipError_t launch_skinny(const ProductParams& p, hipStream_t s) {
-    constexpr int W = 8;
-    const dim3 grid((unsigned)((p.n_out + 16 * NS - 1) / (16 * NS)),
-                    (unsigned)max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, 16 * MT));
-    skinny_kernel<OT, FUSED, MT, NS, W><<<grid, W * 64, 0, s>>>(p);
+// Whether a product quantises its rows itself: one tile holds them all, or with
+// groups twice a group's average.
+inline bool fused(int64_t rows, int n_groups, int n_in) {
+    return typical_rows(rows, n_groups) * (n_groups > 1 ? 2 : 1) <= fused_rows(n_in);
+}
+
+template <typename OT, bool FUSED> hipError_t launch_small(const ProductParams& p, hipStream_t s) {
+    const dim3 grid((unsigned)((p.n_out + 15) / 16), (unsigned)max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, FUSED ? fused_rows(p.n_in) : SMALL_MAX_ROWS));
+    if (p.n_in % (4 * BLOCK) == 0) small_kernel<OT, FUSED, true><<<grid, SMALL_WAVES * 64, 0, s>>>(p);
+    else small_kernel<OT, FUSED, false><<<grid, SMALL_WAVES * 64, 0, s>>>(p);
     return hipGetLastError();
 }
 
-// Rows that a group has on average: what a tile's height is chosen by.
-inline int64_t typical_rows(int64_t rows, int n_groups) { return (rows + n_groups - 1) / n_groups; }
-// Whether a product quantises its rows itself.
-inline bool fused(int64_t rows, int n_groups) { return typical_rows(rows, n_groups) <= 16; }
+inline bool tiles_fit(int64_t rows, int64_t cols) { return xcd_padded(rows * cols) <= 0x7FFFFFFF; }
+
+template <typename OT> hipError_t launch_medium(const ProductParams& p, hipStream_t s) {
+    const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, 64), cols = (p.n_out + 63) / 64;
+    if (!tiles_fit(rows, cols)) return hipErrorInvalidConfiguration;
+    const unsigned tiles = (unsigned)xcd_padded(rows * cols);
+    if (p.n_in % (4 * BLOCK) == 0) medium_kernel<OT, true><<<tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
+    else medium_kernel<OT, false><<<tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
+    return hipGetLastError();
+}
 
 template <typename OT, int RT> hipError_t launch_gemm(const ProductParams& p, hipStream_t s) {
     const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, 64 * RT), cols = (p.n_out + 255) / 256;
-    const int64_t tiles = xcd_padded(rows * cols);
-    if (tiles > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    if (p.n_in % (4 * BLOCK) == 0) gemm_kernel<OT, RT, true><<<(unsigned)tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
-    else gemm_kernel<OT, RT, false><<<(unsigned)tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
+    if (!tiles_fit(rows, cols)) return hipErrorInvalidConfiguration;
+    const unsigned tiles = (unsigned)xcd_padded(rows * cols);
+    if (p.n_in % (4 * BLOCK) == 0) gemm_kernel<OT, RT, true><<<tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
+    else gemm_kernel<OT, RT, false><<<tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
     return hipGetLastError();
 }
 
 template <typename OT> hipError_t launch_product(const ProductParams& p, hipStream_t s) {
+    if (p.x) return launch_small<OT, true>(p, s);
     const int64_t m = typical_rows(p.rows, p.n_groups);
-    if (p.x) return launch_skinny<OT, true, 1, 1>(p, s);
-    if (m <= 16) return launch_skinny<OT, false, 1, 1>(p, s);
-    if (m <= 32) return launch_skinny<OT, false, 2, 1>(p, s);
-    if (m <= SKINNY_MAX_ROWS) return launch_skinny<OT, false, 4, 1>(p, s);
-    if (m <= 128) return launch_gemm<OT, 2>(p, s);
+    if (m <= SMALL_MAX_ROWS) return launch_small<OT, false>(p, s);
+    const int64_t cols = (p.n_out + 255) / 256, cus = 256;
+    const int64_t high = ((m + 255) / 256 * p.n_groups * cols + cus - 1) / cus, low = ((m + 127) / 128 * p.n_groups * cols + cus - 1) / cus;
+    const int64_t tiles = (m + 63) / 64 * ((p.n_out + 63) / 64) * p.n_groups;
+    if (tiles <= 2 * cus) return launch_medium<OT>(p, s);
+    if (5 * low < 8 * high) return launch_gemm<OT, 2>(p, s);
     return launch_gemm<OT, 4>(p, s);
 }
 
@@ -665,7 +848,7 @@ int exl3_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t r
 
 int64_t exl3_mxfp4_workspace_bytes(int32_t rows, int32_t n_groups, int32_t n_in) {
     if (rows < 0 || n_groups < 1 || bad_row(n_in)) return EXL3_EINVAL;
-    return fused(rows, n_groups) ? 0 : codes_bytes(rows, n_in) + (((int64_t)rows * (n_in / BLOCK) + 255) & ~int64_t(255));
+    return fused(rows, n_groups, n_in) ? 0 : codes_bytes(rows, n_in) + (((int64_t)rows * (n_in / BLOCK) + 255) & ~int64_t(255));
 }
 
 int exl3_mxfp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, int32_t rows, const int32_t* offsets,

@@ -29,7 +29,6 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int BLOCK = 32;        // values per scale
 constexpr int SPAN_BLOCKS = 16;  // blocks per span
-constexpr uint32_t UNIT_SCALES = 0x7F7F7F7Fu;  // four scales of 1
 
 // Type tags of the 16- and 32-bit tensors.
 struct F16 { typedef uint16_t raw; static constexpr int bytes = 2; };
@@ -43,9 +42,6 @@ __device__ inline float to_f32(F32, uint32_t v) { return __builtin_bit_cast(floa
 __device__ inline uint16_t from_f32(F16, float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
 __device__ inline uint16_t from_f32(BF16, float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 __device__ inline uint32_t from_f32(F32, float v) { return __builtin_bit_cast(uint32_t, v); }
-
-// Two values of a 16-bit type, or one of fp32, as the dwords they load as.
-template <typename T> struct Words {};
 
 // Largest magnitude over dwords of T, as the bits of an fp32 (NaN and infinity
 // keep an all-ones exponent): magnitudes order like their bit patterns.

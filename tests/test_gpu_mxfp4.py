@@ -203,6 +203,17 @@ def test_many_groups(ex):
     check_groups(ex, [0] * 64 + [400] + [0] * 63, 1, 128, 40, "fp16")
 
 
+@pytest.mark.parametrize("n_in", [96, 512, 2048, 4096, 4128, 16384, 16416])
+@pytest.mark.parametrize("m", [1, 2, 4, 5, 8])
+def test_few_rows_of_every_length(ex, m, n_in):
+    check_linear(ex, m, n_in, 40, ("fp16", "bf16", "fp32")[(m + n_in // 32) % 3], pad=16)
+
+
+@pytest.mark.parametrize("m, n_in, n_out", [(70, 4096, 700), (200, 2048, 3000), (200, 2080, 3000), (600, 1056, 2000), (1500, 512, 1500)])
+def test_linear_of_many_tiles(ex, m, n_in, n_out):
+    check_linear(ex, m, n_in, n_out, "bf16")
+
+
 def test_offsets_outside_the_rows_are_taken_as_the_nearer_end(ex):
     rng = np.random.default_rng(8)
     x = R.rows(rng, 6, 64, torch.float32)
