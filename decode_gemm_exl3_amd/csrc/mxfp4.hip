@@ -192,15 +192,16 @@ __device__ inline Side side(const uint8_t* codes, const uint8_t* scales, int64_t
                 buffer(scales + (at & ~int64_t(15)), ((at & 15) + (int64_t)rows * nb + 3) & ~int64_t(3)), (uint32_t)(at & 15), rows};
 }
 
-// Few rows: a workgroup of eight waves owns 16 outputs for up to 16 rows, wave w
-// the spans w, w + 8, ... of the input.  Each wave brings its spans of the weight
-// straight into a ring of its own in LDS, four rows of 256 bytes a load, and
-// waits for nobody (a weight operand read from memory by its lanes would be 64
-// places for 1 KB, 64 cycles of the address unit instead of 16).  The rows come
-// quantised, the same way, or (FUSED) as values, which the workgroup quantises
-// into LDS while the weight is on its way: FUSED_ROW_SPANS spans of them, all rows
-// together, so that two workgroups fit a CU.  The waves' sums meet in LDS and are
-// added in the order of the waves.
+// Few rows: eight waves, `split` of them on each run of 16 outputs (8 / split runs
+// a workgroup), for up to 16 rows; of a run's waves, wave w takes the spans w,
+// w + split, ... of the input.  Each wave brings its spans of the weight straight
+// into a ring of its own in LDS, four rows of 256 bytes a load, and waits for
+// nobody (a weight operand read from memory by its lanes would be 64 places for
+// 1 KB, 64 cycles of the address unit instead of 16).  The rows come quantised,
+// the same way, or (FUSED) as values, which the workgroup quantises into LDS while
+// the weight is on its way: FUSED_ROW_SPANS spans of them, all rows together, so
+// that two workgroups fit a CU.  A run's sums meet in LDS and are added in the
+// order of its waves.
 //
 // Block b of row r sits in 16-byte slot b ^ swizzle(r): the 16 lanes that LDS
 // serves together (rows 0-3 and 12-15 of one quarter, 4-11 of the next) then
@@ -218,7 +219,7 @@ __device__ inline int small_swizzle(int row) {  // rows / 4: 0 1 2 3 -> 0 2 3 1
 }
 
 template <typename OT, bool FUSED, bool WHOLE>
-__global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductParams p) {
+__global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductParams p, int split) {
     constexpr int SDW = SCALE_DWORDS<WHOLE>, SIDES = FUSED ? 1 : 2, LOADS = SIDES * (4 + SDW / 4);
     constexpr int BUF = SIDES * (256 + 4 * SDW);  // slots: codes of each side, then scales
     constexpr int RING = SMALL_WAVES * SMALL_RING * BUF;
@@ -227,15 +228,16 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductPa
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
     const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, blockIdx.y, FUSED ? fused_rows(p.n_in) : SMALL_MAX_ROWS);
     if (t.rows == 0) return;
-    const int n0 = blockIdx.x * 16, cols = min(16, p.n_out - n0);
+    const int first = wave % split;  // of the run's spans
+    const int n0 = (blockIdx.x * (SMALL_WAVES / split) + wave / split) * 16, cols = min(16, p.n_out - n0);
     const int nb = p.n_in / BLOCK, spans = (nb + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
     i32x4_t* const ring = lds + wave * SMALL_RING * BUF;
 
     f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
     if (t.group < p.n_groups) {
-        const int mine = (spans - wave + SMALL_WAVES - 1) / SMALL_WAVES;  // spans of this wave (none: 0 or less)
+        const int mine = cols > 0 ? (spans - first + split - 1) / split : 0;  // spans of this wave
         Side sides[SIDES];
-        sides[0] = side(p.wc, p.ws, (int64_t)t.group * p.n_out + n0, cols, nb);
+        sides[0] = side(p.wc, p.ws, (int64_t)t.group * p.n_out + (cols > 0 ? n0 : 0), max(cols, 1), nb);
         if constexpr (!FUSED) sides[1] = side(p.xc, p.xs, t.row0, t.rows, nb);
         uint32_t row_at[SIDES][4], scale_at[SIDES][SDW / 4], shift[SIDES];
 #pragma unroll
@@ -250,7 +252,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductPa
         }
         // The loads of this wave's kth span; behind its last they give zeros.
         auto ask = [&](int k) {
-            const int sp = k < mine ? wave + k * SMALL_WAVES : spans;
+            const int sp = k < mine ? first + k * split : spans;
             i32x4_t* const buf = ring + k % SMALL_RING * BUF;
 #pragma unroll
             for (int s = 0; s < SIDES; ++s) {
@@ -312,7 +314,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductPa
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(0x0F70 | ((SMALL_RING - 1) * LOADS & 15) | (((SMALL_RING - 1) * LOADS >> 4) << 14));  // vmcnt
             __builtin_amdgcn_sched_barrier(0);
-            const int sp = wave + k * SMALL_WAVES, left = nb - sp * SPAN_BLOCKS - 4 * q;
+            const int sp = first + k * split, left = nb - sp * SPAN_BLOCKS - 4 * q;
             i32x4_t wv[4], xv[4];
             uint32_t xsc;
 #pragma unroll
@@ -341,10 +343,9 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductPa
     // each wave's sums over its own ring
     ring[lane] = __builtin_bit_cast(i32x4_t, acc);
     __syncthreads();
-    if (wave == 0) {
+    if (first == 0) {
         f32x4_t v = acc;
-#pragma unroll
-        for (int w = 1; w < SMALL_WAVES; ++w) v += __builtin_bit_cast(f32x4_t, lds[w * SMALL_RING * BUF + lane]);
+        for (int w = 1; w < split; ++w) v += __builtin_bit_cast(f32x4_t, ring[w * SMALL_RING * BUF + lane]);
         const int o = n0 + 4 * q;
         if (r < t.rows && o < p.n_out) store4<OT>(p.y, (int64_t)(t.row0 + r) * p.n_out + o, p.n_out - o, (p.n_out & 3) == 0, v);
     }
@@ -536,9 +537,9 @@ __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int 
 
 constexpr int STAGE_BLOCKS = 8;
 
-template <typename OT, int RT, bool WHOLE>
-__global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int row_tiles, int col_tiles) {
-    constexpr int BM = 64 * RT, BN = 256;
+template <typename OT, int RT, int CT, bool WHOLE>
+__global__ __launch_bounds__(256, RT * CT > 4 ? 1 : 2) void gemm_kernel(const ProductParams p, int row_tiles, int col_tiles) {
+    constexpr int BM = 64 * RT, BN = 64 * CT;
     constexpr int STAGE = (BM + BN) * 8;  // 16-byte slots: the rows', then the weight's
     constexpr int ROW_LOADS = BM / 32, W_LOADS = BN / 32;  // a wave's loads per stage, 8 rows each
     constexpr int SDW = WHOLE ? 4 : 8;    // dwords of scales a row holds in LDS
@@ -555,11 +556,11 @@ __global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int
     const int nb = p.n_in / BLOCK, stages = (nb + STAGE_BLOCKS - 1) / STAGE_BLOCKS;
     const int half = p.n_in / 2;
 
-    f32x16_t acc[RT][4];
+    f32x16_t acc[RT][CT];
 #pragma unroll
     for (int m = 0; m < RT; ++m)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < CT; ++c)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[m][c][i] = 0.f;
 
@@ -612,11 +613,11 @@ __global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int
             const uint32_t v = __builtin_amdgcn_alignbyte(s[1], s[0], shift);
             return left >= 4 ? v : (left > 0 ? v & ((1u << (8 * left)) - 1u) : 0u);
         };
-        uint32_t xshift[RT], wshift[4];  // bytes from an aligned dword to a row's scales
+        uint32_t xshift[RT], wshift[CT];  // bytes from an aligned dword to a row's scales
 #pragma unroll
         for (int m = 0; m < RT; ++m) xshift[m] = ((uint32_t)min((wy * RT + m) * 32 + r, t.rows - 1) * nb + (uint32_t)(xs0 & 15)) & 3;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) wshift[c] = ((uint32_t)min((wx * 4 + c) * 32 + r, cols - 1) * nb + (uint32_t)(ws0 & 15)) & 3;
+        for (int c = 0; c < CT; ++c) wshift[c] = ((uint32_t)min((wx * CT + c) * 32 + r, cols - 1) * nb + (uint32_t)(ws0 & 15)) & 3;
         // slot of this lane's block of step j in row r of a 32-row tile
         int frag[4];
 #pragma unroll
@@ -629,18 +630,18 @@ __global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int
         // the stage after next; the next stage's first step asks for the other half.
         // The loads go between the MFMAs: a wave that issues them in a row waits for
         // the address unit with the matrix core idle.  Stages behind the last re-read it.
-        constexpr int MFMAS = 4 * RT, READS = 4 + RT, CODES = (ROW_LOADS + W_LOADS) / 2, EACH = (SCALE_LOADS + 1) / 2;
+        constexpr int MFMAS = CT * RT, READS = CT + RT, CODES = (ROW_LOADS + W_LOADS) / 2, EACH = (SCALE_LOADS + 1) / 2;
         const int last = stages - 1;
-        i32x4_t xv[2][RT], wv[2][4];
-        uint32_t wsc[4], xsc[RT], wsn[4], xsn[RT];  // scales of this stage and the next
+        i32x4_t xv[2][RT], wv[2][CT];
+        uint32_t wsc[CT], xsc[RT], wsn[CT], xsn[RT];  // scales of this stage and the next
         auto read_operand = [&](int k, int j, int par, int to) {  // operand k of step j of a stage of this parity
             const i32x4_t* a = lds + par * STAGE + frag[j];
-            if (k < 4) wv[to][k] = a[BM * 8 + (wx * 4 + k) * 256];
-            else xv[to][k - 4] = a[(wy * RT + k - 4) * 256];
+            if (k < CT) wv[to][k] = a[BM * 8 + (wx * CT + k) * 256];
+            else xv[to][k - CT] = a[(wy * RT + k - CT) * 256];
         };
         auto read_scale = [&](int k, int st, int par) {
-            if (k < 4) wsn[k] = scales(BM + (wx * 4 + k) * 32 + r, wshift[k], st, par);
-            else xsn[k - 4] = scales((wy * RT + k - 4) * 32 + r, xshift[k - 4], st, par);
+            if (k < CT) wsn[k] = scales(BM + (wx * CT + k) * 32 + r, wshift[k], st, par);
+            else xsn[k - CT] = scales((wy * RT + k - CT) * 32 + r, xshift[k - CT], st, par);
         };
 #pragma unroll
         for (int k = 0; k < 2 * CODES; ++k) ask_codes(k, 0, 0);
@@ -661,7 +662,7 @@ __global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int
         for (int st = 0; st < stages; ++st) {
             const int par = st & 1;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) wsc[c] = wsn[c];
+            for (int c = 0; c < CT; ++c) wsc[c] = wsn[c];
 #pragma unroll
             for (int m = 0; m < RT; ++m) xsc[m] = xsn[m];
             auto step = [&](auto jc) {
@@ -694,7 +695,7 @@ __global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int
                             ask_scales(par ? k : min(EACH + k, end), par ? so[k] : so[EACH + k < end ? EACH + k : end], ((st + 1) >> 1) + 1);
                         }
                     }
-                    acc[i / 4][i % 4] = mfma32<j>(wv[j & 1][i % 4], wsc[i % 4], xv[j & 1][i / 4], xsc[i / 4], acc[i / 4][i % 4]);
+                    acc[i / CT][i % CT] = mfma32<j>(wv[j & 1][i % CT], wsc[i % CT], xv[j & 1][i / CT], xsc[i / CT], acc[i / CT][i % CT]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             };
@@ -706,9 +707,9 @@ __global__ __launch_bounds__(256, 1) void gemm_kernel(const ProductParams p, int
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the last stage's second copy is here
         __builtin_amdgcn_s_barrier();        // and the buffers are read
     }
-    constexpr int PART = store_part_bytes<OT, 4>();
+    constexpr int PART = store_part_bytes<OT, CT>();
     static_assert(4 * PART <= (int)sizeof(lds), "the waves' parts fit");
-    store_tile<OT, RT, 4>(acc, reinterpret_cast<char*>(lds) + wave * PART, p, t.row0 + wy * RT * 32, t.rows - wy * RT * 32, n0 + wx * 128);
+    store_tile<OT, RT, CT>(acc, reinterpret_cast<char*>(lds) + wave * PART, p, t.row0 + wy * RT * 32, t.rows - wy * RT * 32, n0 + wx * CT * 32);
 }
 
 // ---- launches ----
@@ -727,16 +728,25 @@ template <typename T> hipError_t launch_quantize(const void* x, int64_t rows, in
 // Rows that a group has on average: what a tile's height is chosen by.
 inline int64_t typical_rows(int64_t rows, int n_groups) { return (rows + n_groups - 1) / n_groups; }
 
-// Whether a product quantises its rows itself: one tile holds them all, or with
-// groups twice a group's average.
-inline bool fused(int64_t rows, int n_groups, int n_in) {
-    return typical_rows(rows, n_groups) * (n_groups > 1 ? 2 : 1) <= fused_rows(n_in);
-}
+// Whether a product quantises its rows itself: a tile holds a group's rows.  Saves
+// the launch and the codes' way through memory (us, with the quantisation: one row
+// 4096 -> 4096 5.0 against 7.0, 8192 -> 28672 25.6 against 31; 4 rows of each of
+// 64 groups 2048 -> 2816 32 against 39; equal at 8).
+inline bool fused(int64_t rows, int n_groups, int n_in) { return typical_rows(rows, n_groups) <= fused_rows(n_in); }
 
 template <typename OT, bool FUSED> hipError_t launch_small(const ProductParams& p, hipStream_t s) {
-    const dim3 grid((unsigned)((p.n_out + 15) / 16), (unsigned)max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, FUSED ? fused_rows(p.n_in) : SMALL_MAX_ROWS));
-    if (p.n_in % (4 * BLOCK) == 0) small_kernel<OT, FUSED, true><<<grid, SMALL_WAVES * 64, 0, s>>>(p);
-    else small_kernel<OT, FUSED, false><<<grid, SMALL_WAVES * 64, 0, s>>>(p);
+    const int64_t runs = (p.n_out + 15) / 16, tiles = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, FUSED ? fused_rows(p.n_in) : SMALL_MAX_ROWS);
+    // As many waves a run as the card holds at once (two workgroups a CU when FUSED,
+    // else one), so that one round of workgroups starts up and quantises: one row
+    // 4096 -> 14336 takes 9.0 us at 4 waves a run and 11.2 at 8, 8192 -> 28672
+    // 25.6 at 2, 29.9 at 4 and 30.2 at 1, 14336 -> 4096 9.5 at 8 and 11.1 at 4;
+    // 64 rows in 64 groups 2048 -> 2816 19 at 1 and 63 at 8.
+    const int64_t resident = 256 * SMALL_WAVES * (FUSED ? 2 : 1), spans = (p.n_in / BLOCK + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
+    int split = 1;
+    while (split < SMALL_WAVES && split < spans && runs * tiles * split * 2 <= resident) split *= 2;
+    const dim3 grid((unsigned)((runs * split + SMALL_WAVES - 1) / SMALL_WAVES), (unsigned)tiles);
+    if (p.n_in % (4 * BLOCK) == 0) small_kernel<OT, FUSED, true><<<grid, SMALL_WAVES * 64, 0, s>>>(p, split);
+    else small_kernel<OT, FUSED, false><<<grid, SMALL_WAVES * 64, 0, s>>>(p, split);
     return hipGetLastError();
 }
 
@@ -751,25 +761,44 @@ template <typename OT> hipError_t launch_medium(const ProductParams& p, hipStrea
     return hipGetLastError();
 }
 
-template <typename OT, int RT> hipError_t launch_gemm(const ProductParams& p, hipStream_t s) {
-    const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, 64 * RT), cols = (p.n_out + 255) / 256;
+template <typename OT, int RT, int CT> hipError_t launch_gemm(const ProductParams& p, hipStream_t s) {
+    const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, 64 * RT), cols = (p.n_out + 64 * CT - 1) / (64 * CT);
     if (!tiles_fit(rows, cols)) return hipErrorInvalidConfiguration;
     const unsigned tiles = (unsigned)xcd_padded(rows * cols);
-    if (p.n_in % (4 * BLOCK) == 0) gemm_kernel<OT, RT, true><<<tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
-    else gemm_kernel<OT, RT, false><<<tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
+    if (p.n_in % (4 * BLOCK) == 0) gemm_kernel<OT, RT, CT, true><<<tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
+    else gemm_kernel<OT, RT, CT, false><<<tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
     return hipGetLastError();
+}
+
+// Row tiles of `high` rows that a product is expected to have: with groups, half a
+// tile of each group (or row) is padding.
+inline int64_t expected_tiles(const ProductParams& p, int high) {
+    if (!p.offsets) return (p.rows + high - 1) / high;
+    return p.rows / high + (p.n_groups < p.rows ? p.n_groups : p.rows) / 2 + 1;
 }
 
 template <typename OT> hipError_t launch_product(const ProductParams& p, hipStream_t s) {
     if (p.x) return launch_small<OT, true>(p, s);
+    constexpr int64_t CUS = 256;
+    // Few rows (us, with the quantisation): 16 rows 14336 -> 4096 13.2 in small
+    // tiles and 23.8 in 64 x 64 ones, 4096 -> 14336 12.6 and 12.9; 24 rows 14336 ->
+    // 4096 15.2 and 24.5, but 4096 -> 14336 17 and 13.2; 8 rows of each of 64
+    // groups 2048 -> 2816 50 and 61.
     const int64_t m = typical_rows(p.rows, p.n_groups);
-    if (m <= SMALL_MAX_ROWS) return launch_small<OT, false>(p, s);
-    const int64_t cols = (p.n_out + 255) / 256, cus = 256;
-    const int64_t high = ((m + 255) / 256 * p.n_groups * cols + cus - 1) / cus, low = ((m + 127) / 128 * p.n_groups * cols + cus - 1) / cus;
-    const int64_t tiles = (m + 63) / 64 * ((p.n_out + 63) / 64) * p.n_groups;
-    if (tiles <= 2 * cus) return launch_medium<OT>(p, s);
-    if (5 * low < 8 * high) return launch_gemm<OT, 2>(p, s);
-    return launch_gemm<OT, 4>(p, s);
+    if (p.offsets ? m <= 8 : m <= 16 || (m <= 32 && p.n_out <= 4096)) return launch_small<OT, false>(p, s);
+    // 64 x 64 tiles up to two rounds of them: 512 rows 4096 -> 4096 15.0 us against
+    // 18.5 in 128 x 128, 1024 rows 28.1 against 18.4.
+    if (expected_tiles(p, 64) * ((p.n_out + 63) / 64) <= 2 * CUS) return launch_medium<OT>(p, s);
+    // 128 x 128 tiles (two workgroups a CU) against 256 x 256 (one).  A round of the
+    // former takes 0.7 of the latter's, and with many tiles a CU only whole rounds
+    // of the large ones count, as the small ones end one by one.  2048 rows 4096 ->
+    // 4096 27.8 against 43.1 us (1 : 1 rounds), 4096 rows 50.5 against 43.3 (2 : 1),
+    // 2048 rows 8192 -> 28672 386 against 315 (7 : 4), 2048 rows in 64 groups 2048 ->
+    // 2816 46.5 against 67.5 (2.1 : 2), 1024 rows in 8 groups 4096 -> 14336 100
+    // against 85 (2.8 : 2).
+    const double low = (double)(expected_tiles(p, 128) * ((p.n_out + 127) / 128)) / (2 * CUS);
+    const int64_t high = (expected_tiles(p, 256) * ((p.n_out + 255) / 256) + CUS - 1) / CUS;
+    return 0.72 * (low > 1 ? low : 1) < (double)high ? launch_gemm<OT, 2, 2>(p, s) : launch_gemm<OT, 4, 4>(p, s);
 }
 
 hipError_t product(int dtype, const ProductParams& p, hipStream_t s) {
