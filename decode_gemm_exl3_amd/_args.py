@@ -20,17 +20,18 @@ BYTES = {torch.uint8: None}
 INDEX = {torch.int32: None}
 
 
-def declare(name: str, *argtypes, restype=ctypes.c_int):
-    """The library's function of that name, its types set on the first use."""
-    slot = []
+class Function:
+    """A function of the library, its types set on the first use."""
+    __slots__ = ("name", "argtypes", "restype", "bound")
 
-    def get():
-        if not slot:
-            f = getattr(load(), name)
-            f.argtypes, f.restype = argtypes, restype
-            slot.append(f)
-        return slot[0]
-    return get
+    def __init__(self, name: str, *argtypes, restype=ctypes.c_int):
+        self.name, self.argtypes, self.restype, self.bound = name, argtypes, restype, None
+
+    def load(self):
+        f = getattr(load(), self.name)
+        f.argtypes, f.restype = self.argtypes, self.restype
+        self.bound = f
+        return f
 
 
 def dtype_code(t, name: str) -> int:
@@ -60,6 +61,14 @@ def need(t, name: str, dtypes, shape) -> int:
     return at
 
 
+def result(t, name: str, like, dtype, shape):
+    """A given output, checked, or a new one beside `like`; with its address."""
+    if t is None:
+        t = like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    return t, need(t, name, (dtype,), shape)
+
+
 def need_rows(t, name: str) -> int:
     """A 2-dimensional floating tensor whose rows are contiguous and start at
     multiples of 16 bytes; returns the row stride in elements."""
@@ -78,7 +87,8 @@ def need_rows(t, name: str) -> int:
 
 
 def on_device(dev: int, **tensors) -> None:
-    """Every tensor on GPU `dev`, the device of the first."""
+    """Raises unless every tensor is on GPU `dev`, the device of the first (the
+    callers compare the devices themselves and come here to name the odd one)."""
     for name, t in tensors.items():
         if t is None:
             continue
@@ -89,28 +99,41 @@ def on_device(dev: int, **tensors) -> None:
             raise Exl3Error(f"{name}: on GPU {at}, the first tensor is on GPU {dev}")
 
 
-def call(fn, what: str, dev: int, stream, *args) -> None:
+# The handle of a device's current stream without a Stream object made for it (0.1
+# against 1.1 us, of about 7 for a whole call).
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def call(fn: Function, dev: int, stream, *args) -> None:
     """fn(*args, stream) on GPU `dev`."""
-    if stream is not None and stream.device_index != dev:
-        raise Exl3Error(f"{what}: the stream is of GPU {stream.device_index}, the tensors are on GPU {dev}")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return call(fn, what, dev, stream, *args)
-    handle = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
-    status = fn()(*args, handle)
+            return call(fn, dev, stream, *args)
+    if stream is None:
+        handle = _current(dev)
+    elif stream.device_index != dev:
+        raise Exl3Error(f"{fn.name}: the stream is of GPU {stream.device_index}, the tensors are on GPU {dev}")
+    else:
+        handle = stream.cuda_stream
+    status = (fn.bound or fn.load())(*args, handle)
     if status != 0:
-        _check(status, what)
+        _check(status, fn.name)
 
 
 def scratch(workspace, nbytes: int, like, stream):
-    """`workspace` when given, else scratch of the caching allocator, kept from
-    reuse until `stream` is done with it."""
+    """Address and size of `workspace` when given, else of scratch of the caching
+    allocator, which is kept from reuse until `stream` is done with it; the third
+    value keeps it alive for the call."""
     if workspace is not None:
-        need(workspace, "workspace", BYTES, (workspace.numel(),) if isinstance(workspace, torch.Tensor) else None)
-        return workspace
+        if not isinstance(workspace, torch.Tensor):
+            raise Exl3Error("workspace: expected a torch tensor")
+        at = need(workspace, "workspace", BYTES, workspace.shape)
+        if workspace.get_device() != like.get_device():
+            on_device(like.get_device(), workspace=workspace)
+        return at, workspace.numel(), workspace
     if nbytes == 0:
-        return None
-    buf = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return None, 0, None
+    buf = like.new_empty(nbytes, dtype=torch.uint8)
     if stream is not None:
         buf.record_stream(stream)
-    return buf
+    return buf.data_ptr(), nbytes, buf

@@ -18,39 +18,38 @@ from __future__ import annotations
 import torch
 
 from . import Exl3Error
-from ._args import FLOATS, I32, I64, INDEX, SIZE, VOID, call, declare, dtype_code, need, on_device, scratch
+from ._args import FLOATS, I32, I64, INDEX, SIZE, VOID, Function, call, dtype_code, need, on_device, result, scratch
 
 MAX_EXPERTS = 1024  # EXL3_MOE_MAX_EXPERTS
 _IDS = {torch.int32: 4, torch.int64: 8}
 
-_bytes = declare("exl3_moe_workspace_bytes", I32, I32, restype=I64)
-_sort = declare("exl3_moe_sort", VOID, I32, I32, I32, VOID, VOID, VOID, VOID, SIZE, VOID)
-_gather = declare("exl3_moe_gather", VOID, I32, I32, I32, I32, VOID, VOID, VOID, VOID)
-_combine = declare("exl3_moe_combine", VOID, I32, I32, I32, I32, VOID, VOID, VOID, I32, VOID, VOID)
-_backward = declare("exl3_moe_combine_backward", VOID, VOID, I32, I32, I32, I32, VOID, VOID, VOID, I32, VOID, VOID, VOID)
+_bytes = Function("exl3_moe_workspace_bytes", I32, I32, restype=I64)
+_sort = Function("exl3_moe_sort", VOID, I32, I32, I32, VOID, VOID, VOID, VOID, SIZE, VOID)
+_gather = Function("exl3_moe_gather", VOID, I32, I32, I32, I32, VOID, VOID, VOID, VOID)
+_combine = Function("exl3_moe_combine", VOID, I32, I32, I32, I32, VOID, VOID, VOID, I32, VOID, VOID)
+_backward = Function("exl3_moe_combine_backward", VOID, VOID, I32, I32, I32, I32, VOID, VOID, VOID, I32, VOID, VOID, VOID)
 
 
 def moe_sort(expert_ids, n_experts: int, order=None, position=None, offsets=None, workspace=None, stream=None):
-    """The slots sorted by expert, stable: (order, position, offsets)."""
+    """The slots sorted by expert, stable: (order, position, offsets).
+
+    workspace: a uint8 device tensor of exl3_moe_workspace_bytes; by default new
+    scratch where that is not 0.
+    """
     if not isinstance(expert_ids, torch.Tensor) or expert_ids.dim() != 2:
         raise Exl3Error("expert_ids: expected a torch tensor [tokens, top_k]")
-    ids = need(expert_ids, "expert_ids", _IDS, expert_ids.shape)
+    shape, slots = expert_ids.shape, expert_ids.numel()
+    ids = need(expert_ids, "expert_ids", _IDS, shape)
     if not 1 <= n_experts <= MAX_EXPERTS:
         raise Exl3Error(f"n_experts: {n_experts}, expected 1 to {MAX_EXPERTS}")
-    slots, like = expert_ids.numel(), {"dtype": torch.int32, "device": expert_ids.device}
-    if order is None:
-        order = torch.empty((slots,), **like)
-    if position is None:
-        position = torch.empty(expert_ids.shape, **like)
-    if offsets is None:
-        offsets = torch.empty((n_experts + 1,), **like)
-    o, p = need(order, "order", INDEX, (slots,)), need(position, "position", INDEX, expert_ids.shape)
-    f = need(offsets, "offsets", INDEX, (n_experts + 1,))
+    order, o = result(order, "order", expert_ids, torch.int32, (slots,))
+    position, p = result(position, "position", expert_ids, torch.int32, shape)
+    offsets, f = result(offsets, "offsets", expert_ids, torch.int32, (n_experts + 1,))
     dev = expert_ids.get_device()
-    on_device(dev, expert_ids=expert_ids, order=order, position=position, offsets=offsets, workspace=workspace)
-    ws = scratch(workspace, int(_bytes()(slots, n_experts)) if workspace is None else 0, expert_ids, stream)
-    call(_sort, "exl3_moe_sort", dev, stream, ids, _IDS[expert_ids.dtype], slots, n_experts, o, p, f,
-         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
+    if not dev == order.get_device() == position.get_device() == offsets.get_device() >= 0:
+        on_device(dev, expert_ids=expert_ids, order=order, position=position, offsets=offsets)
+    ws, nbytes, held = scratch(workspace, 0 if workspace is not None else (_bytes.bound or _bytes.load())(slots, n_experts), expert_ids, stream)
+    call(_sort, dev, stream, ids, _IDS[expert_ids.dtype], slots, n_experts, o, p, f, ws, nbytes)
     return order, position, offsets
 
 
@@ -75,12 +74,11 @@ def moe_gather(x, position, offsets, rows=None, stream=None):
     tokens, top_k, at, kept = _places(position, offsets)
     n, code = _width(x, "x"), dtype_code(x, "x")
     src = need(x, "x", FLOATS, (tokens, n))
-    if rows is None:
-        rows = torch.empty((tokens * top_k, n), dtype=x.dtype, device=x.device)
-    dst = need(rows, "rows", (x.dtype,), (tokens * top_k, n))
+    rows, dst = result(rows, "rows", x, x.dtype, (tokens * top_k, n))
     dev = x.get_device()
-    on_device(dev, x=x, position=position, offsets=offsets, rows=rows)
-    call(_gather, "exl3_moe_gather", dev, stream, src, code, tokens, top_k, n, at, kept, dst)
+    if not dev == position.get_device() == offsets.get_device() == rows.get_device() >= 0:
+        on_device(dev, x=x, position=position, offsets=offsets, rows=rows)
+    call(_gather, dev, stream, src, code, tokens, top_k, n, at, kept, dst)
     return rows
 
 
@@ -90,13 +88,12 @@ def moe_combine(rows, position, offsets, weights=None, y=None, stream=None):
     n, code = _width(rows, "rows"), dtype_code(rows, "rows")
     src = need(rows, "rows", FLOATS, (tokens * top_k, n))
     w = None if weights is None else need(weights, "weights", FLOATS, (tokens, top_k))
-    if y is None:
-        y = torch.empty((tokens, n), dtype=rows.dtype, device=rows.device)
-    dst = need(y, "y", (rows.dtype,), (tokens, n))
+    y, dst = result(y, "y", rows, rows.dtype, (tokens, n))
     dev = rows.get_device()
-    on_device(dev, rows=rows, position=position, offsets=offsets, weights=weights, y=y)
-    call(_combine, "exl3_moe_combine", dev, stream, src, code, tokens, top_k, n, at, kept, w,
-         0 if weights is None else FLOATS[weights.dtype], dst)
+    if not (dev == position.get_device() == offsets.get_device() == y.get_device() >= 0
+            and (w is None or weights.get_device() == dev)):
+        on_device(dev, rows=rows, position=position, offsets=offsets, weights=weights, y=y)
+    call(_combine, dev, stream, src, code, tokens, top_k, n, at, kept, w, 0 if w is None else FLOATS[weights.dtype], dst)
     return y
 
 
@@ -111,13 +108,11 @@ def moe_combine_backward(dy, rows, position, offsets, weights, drows=None, dweig
     n, code = _width(rows, "rows"), dtype_code(rows, "rows")
     src, grad = need(rows, "rows", FLOATS, (tokens * top_k, n)), need(dy, "dy", (rows.dtype,), (tokens, n))
     w = need(weights, "weights", FLOATS, (tokens, top_k))
-    if drows is None:
-        drows = torch.empty((tokens * top_k, n), dtype=rows.dtype, device=rows.device)
-    if dweights is None:
-        dweights = torch.empty((tokens, top_k), dtype=weights.dtype, device=rows.device)
-    dst, dw = need(drows, "drows", (rows.dtype,), (tokens * top_k, n)), need(dweights, "dweights", (weights.dtype,), (tokens, top_k))
+    drows, dst = result(drows, "drows", rows, rows.dtype, (tokens * top_k, n))
+    dweights, dw = result(dweights, "dweights", weights, weights.dtype, (tokens, top_k))
     dev = rows.get_device()
-    on_device(dev, rows=rows, dy=dy, position=position, offsets=offsets, weights=weights, drows=drows, dweights=dweights)
-    call(_backward, "exl3_moe_combine_backward", dev, stream, grad, src, code, tokens, top_k, n, at, kept, w,
-         FLOATS[weights.dtype], dst, dw)
+    if not (dev == dy.get_device() == position.get_device() == offsets.get_device() == weights.get_device() == drows.get_device()
+            == dweights.get_device() >= 0):
+        on_device(dev, rows=rows, dy=dy, position=position, offsets=offsets, weights=weights, drows=drows, dweights=dweights)
+    call(_backward, dev, stream, grad, src, code, tokens, top_k, n, at, kept, w, FLOATS[weights.dtype], dst, dw)
     return drows, dweights

@@ -13,15 +13,16 @@ from __future__ import annotations
 import torch
 
 from . import Exl3Error, _check
-from ._args import BYTES, FLOATS, I32, I64, INDEX, SIZE, VOID, call, declare, dtype_code, need, need_rows, on_device, scratch
+from ._args import (BYTES, FLOATS, I32, I64, INDEX, SIZE, VOID, Function, call, dtype_code, need, need_rows, on_device,
+                    result, scratch)
 
 BLOCK = 32  # EXL3_MXFP4_BLOCK
 
-_quantize = declare("exl3_mxfp4_quantize", VOID, I32, I64, I32, I64, VOID, VOID, VOID)
-_dequantize = declare("exl3_mxfp4_dequantize", VOID, VOID, I64, I32, VOID, I32, VOID)
-_bytes = declare("exl3_mxfp4_workspace_bytes", I32, I32, I32, restype=I64)
-_matmul = declare("exl3_mxfp4_matmul", VOID, VOID, I32, VOID, I32, VOID, VOID, I32, I32, VOID, I32, VOID)
-_linear = declare("exl3_mxfp4_linear", VOID, I32, I32, I64, VOID, I32, VOID, VOID, I32, I32, VOID, VOID, SIZE, VOID)
+_quantize = Function("exl3_mxfp4_quantize", VOID, I32, I64, I32, I64, VOID, VOID, VOID)
+_dequantize = Function("exl3_mxfp4_dequantize", VOID, VOID, I64, I32, VOID, I32, VOID)
+_bytes = Function("exl3_mxfp4_workspace_bytes", I32, I32, I32, restype=I64)
+_matmul = Function("exl3_mxfp4_matmul", VOID, VOID, I32, VOID, I32, VOID, VOID, I32, I32, VOID, I32, VOID)
+_linear = Function("exl3_mxfp4_linear", VOID, I32, I32, I64, VOID, I32, VOID, VOID, I32, I32, VOID, VOID, SIZE, VOID)
 
 
 def _blocks(n: int, name: str) -> int:
@@ -35,14 +36,12 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     ld = need_rows(x, "x")
     rows, n = x.shape
     blocks = _blocks(n, "x")
-    if codes is None:
-        codes = torch.empty((rows, n // 2), dtype=torch.uint8, device=x.device)
-    if scales is None:
-        scales = torch.empty((rows, blocks), dtype=torch.uint8, device=x.device)
-    c, s = need(codes, "codes", BYTES, (rows, n // 2)), need(scales, "scales", BYTES, (rows, blocks))
+    codes, c = result(codes, "codes", x, torch.uint8, (rows, n // 2))
+    scales, s = result(scales, "scales", x, torch.uint8, (rows, blocks))
     dev = x.get_device()
-    on_device(dev, x=x, codes=codes, scales=scales)
-    call(_quantize, "exl3_mxfp4_quantize", dev, stream, x.data_ptr(), FLOATS[x.dtype], rows, n, ld, c, s)
+    if not dev == codes.get_device() == scales.get_device() >= 0:
+        on_device(dev, x=x, codes=codes, scales=scales)
+    call(_quantize, dev, stream, x.data_ptr(), FLOATS[x.dtype], rows, n, ld, c, s)
     return codes, scales
 
 
@@ -53,19 +52,18 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None)
         raise Exl3Error("codes: expected a torch tensor of two dimensions")
     rows, n = codes.shape[0], codes.shape[1] * 2
     blocks = _blocks(n, "codes")
-    if out is None:
-        out = torch.empty((rows, n), dtype=dtype, device=codes.device)
     c, s = need(codes, "codes", BYTES, (rows, n // 2)), need(scales, "scales", BYTES, (rows, blocks))
-    o = need(out, "out", (dtype,), (rows, n))
+    out, o = result(out, "out", codes, dtype, (rows, n))
     dev = codes.get_device()
-    on_device(dev, codes=codes, scales=scales, out=out)
-    call(_dequantize, "exl3_mxfp4_dequantize", dev, stream, c, s, rows, n, o, code)
+    if not dev == scales.get_device() == out.get_device() >= 0:
+        on_device(dev, codes=codes, scales=scales, out=out)
+    call(_dequantize, dev, stream, c, s, rows, n, o, code)
     return out
 
 
 def mxfp4_workspace_bytes(rows: int, n_in: int, groups: int = 1) -> int:
     """Bytes of device scratch that mxfp4_linear needs (0: none)."""
-    n = int(_bytes()(rows, groups, n_in))
+    n = (_bytes.bound or _bytes.load())(rows, groups, n_in)
     if n < 0:
         _check(n, "exl3_mxfp4_workspace_bytes")
     return n
@@ -92,27 +90,30 @@ def mxfp4_matmul(x_codes, x_scales, codes, scales, dtype=torch.bfloat16, offsets
     blocks = _blocks(n_in, "x_codes")
     xc, xs = need(x_codes, "x_codes", BYTES, (m, n_in // 2)), need(x_scales, "x_scales", BYTES, (m, blocks))
     c, s, at, groups, n_out = _weight(codes, scales, offsets, n_in, blocks)
-    if y is None:
-        y = torch.empty((m, n_out), dtype=dtype, device=x_codes.device)
-    o = need(y, "y", (dtype,), (m, n_out))
+    y, o = result(y, "y", x_codes, dtype, (m, n_out))
     dev = x_codes.get_device()
-    on_device(dev, x_codes=x_codes, x_scales=x_scales, codes=codes, scales=scales, offsets=offsets, y=y)
-    call(_matmul, "exl3_mxfp4_matmul", dev, stream, xc, xs, m, at, groups, c, s, n_in, n_out, o, code)
+    if not (dev == x_scales.get_device() == codes.get_device() == scales.get_device() == y.get_device() >= 0
+            and (at is None or offsets.get_device() == dev)):
+        on_device(dev, x_codes=x_codes, x_scales=x_scales, codes=codes, scales=scales, offsets=offsets, y=y)
+    call(_matmul, dev, stream, xc, xs, m, at, groups, c, s, n_in, n_out, o, code)
     return y
 
 
 def mxfp4_linear(x, codes, scales, offsets=None, workspace=None, y=None, stream=None):
-    """y [m, n_out] = Q(x) @ W^T in x's type, Q(x) the MXFP4 quantisation of x."""
+    """y [m, n_out] = Q(x) @ W^T in x's type, Q(x) the MXFP4 quantisation of x.
+
+    workspace: a uint8 device tensor of mxfp4_workspace_bytes(m, n_in, groups); by
+    default new scratch where that is not 0.
+    """
     ld = need_rows(x, "x")
     m, n_in = x.shape
-    blocks = _blocks(n_in, "x")
-    c, s, at, groups, n_out = _weight(codes, scales, offsets, n_in, blocks)
-    if y is None:
-        y = torch.empty((m, n_out), dtype=x.dtype, device=x.device)
-    o = need(y, "y", (x.dtype,), (m, n_out))
+    c, s, at, groups, n_out = _weight(codes, scales, offsets, n_in, _blocks(n_in, "x"))
+    dtype = x.dtype
+    y, o = result(y, "y", x, dtype, (m, n_out))
     dev = x.get_device()
-    on_device(dev, x=x, codes=codes, scales=scales, offsets=offsets, y=y, workspace=workspace)
-    ws = scratch(workspace, mxfp4_workspace_bytes(m, n_in, groups) if workspace is None else 0, x, stream)
-    call(_linear, "exl3_mxfp4_linear", dev, stream, x.data_ptr(), FLOATS[x.dtype], m, ld, at, groups, c, s, n_in, n_out,
-         o, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
+    if not (dev == codes.get_device() == scales.get_device() == y.get_device() >= 0
+            and (at is None or offsets.get_device() == dev)):
+        on_device(dev, x=x, codes=codes, scales=scales, offsets=offsets, y=y)
+    ws, nbytes, held = scratch(workspace, 0 if workspace is not None else mxfp4_workspace_bytes(m, n_in, groups), x, stream)
+    call(_linear, dev, stream, x.data_ptr(), FLOATS[dtype], m, ld, at, groups, c, s, n_in, n_out, o, ws, nbytes)
     return y

@@ -19,9 +19,9 @@ F16, BF16, F32 = 0, 1, 2
 @pytest.fixture(scope="module")
 def lib():
     from decode_gemm_exl3_amd import moe, mxfp4
-    for get in (mxfp4._quantize, mxfp4._dequantize, mxfp4._bytes, mxfp4._matmul, mxfp4._linear, moe._bytes, moe._sort,
-                moe._gather, moe._combine, moe._backward):
-        get()
+    for f in (mxfp4._quantize, mxfp4._dequantize, mxfp4._bytes, mxfp4._matmul, mxfp4._linear, moe._bytes, moe._sort,
+              moe._gather, moe._combine, moe._backward):
+        f.load()
     return ex.load()
 
 
