@@ -18,8 +18,8 @@ using namespace mx;  // element types
 // same expert in the chunks before) and places its slots.  One chunk needs no
 // first launch.
 constexpr int SORT_THREADS = 512, SORT_WAVES = SORT_THREADS / 64;
-constexpr int SORT_MAX_CHUNKS = 256;
-constexpr int SORT_ONE_CHUNK = 4096;  // slots one workgroup sorts alone
+constexpr int SORT_MAX_CHUNKS = 256, SORT_MAX_COUNTS = 32768;
+constexpr int SORT_ONE_CHUNK = 1024;  // slots one workgroup sorts alone (2 rounds, 4.9 us; two launches take 6.4)
 
 struct SortParams {
     const void* ids;
@@ -67,15 +67,22 @@ __global__ __launch_bounds__(SORT_THREADS) void place_kernel(const SortParams p)
         count_chunk(p, 0, total);
         for (int e = threadIdx.x; e < bins; e += SORT_THREADS) next[e] = 0;
     } else {
-        for (int e = threadIdx.x; e < bins; e += SORT_THREADS) {
-            int before = 0, all = 0;
-            for (int c = 0; c < p.chunks; ++c) {
-                const int v = p.counts[(int64_t)c * bins + e];
-                before += c < (int)blockIdx.x ? v : 0;
-                all += v;
+        for (int e = threadIdx.x; e < bins; e += SORT_THREADS) total[e] = next[e] = 0;
+        __syncthreads();
+        // the table's entries, row by row, over all threads; integer sums in any order
+        constexpr int U = 8;
+        const int entries = p.chunks * bins;
+        for (int i0 = threadIdx.x; i0 < entries; i0 += U * SORT_THREADS) {
+            int v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = i0 + u * SORT_THREADS < entries ? p.counts[i0 + u * SORT_THREADS] : 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * SORT_THREADS, c = i / bins, e = i - c * bins;
+                if (v[u] == 0) continue;
+                atomicAdd(&total[e], v[u]);
+                if (c < (int)blockIdx.x) atomicAdd(&next[e], v[u]);
             }
-            total[e] = all;
-            next[e] = before;
         }
     }
     __syncthreads();
@@ -152,7 +159,14 @@ struct RowParams {
     int weights_dtype;
     void* out;
     void* dweights;
+    bool stream;  // the results' size asks for STREAM
 };
+
+// STREAM: results from 32 MiB on are stored past the L2s, which hold that much together and
+// would write them back later, in the way of the next kernel (65536 rows of 4 KB
+// gathered, then summed again: 121 us against 143; 4096 tokens of 8 KB combined and
+// differentiated: 45 against 51).  Smaller ones stay there for their reader.
+constexpr int64_t STREAM_BYTES = 32 << 20;
 
 __device__ inline float load_weight(const RowParams& p, int64_t i) {
     if (!p.weights) return 1.f;
@@ -161,81 +175,126 @@ __device__ inline float load_weight(const RowParams& p, int64_t i) {
     return p.weights_dtype == EXL3_F16 ? to_f32(F16{}, v) : to_f32(BF16{}, v);
 }
 
-// 16 bytes of T, as values; VEC: rows are whole 16-byte pieces.  Otherwise one
-// value at a time, `left` of them in the row.
-template <typename T> struct Piece {
-    static constexpr int N = 16 / T::bytes;
-    typename T::raw v[N];
-};
-template <typename T, bool VEC> __device__ inline Piece<T> load_piece(const void* base, int64_t at, int left) {
-    Piece<T> r;
-    const typename T::raw* src = static_cast<const typename T::raw*>(base) + at;
-    if (VEC) {
-        __builtin_memcpy(r.v, __builtin_assume_aligned(src, 16), 16);
-    } else {
+// 16 bytes of T in four registers.  VEC: rows are whole 16-byte pieces.  Otherwise
+// one value at a time, `left` of them in the row, zeros behind.
+template <typename T, bool VEC> __device__ inline u32x4_t load_piece(const void* base, int64_t at, int left) {
+    typedef typename T::raw raw;
+    const raw* src = static_cast<const raw*>(base) + at;
+    if constexpr (VEC) return *reinterpret_cast<const u32x4_t*>(src);
+    u32x4_t r = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < Piece<T>::N; ++i) r.v[i] = i < left ? src[i] : 0;
+    for (int i = 0; i < 16 / T::bytes; ++i) {
+        const uint32_t v = i < left ? src[i] : 0;
+        if constexpr (T::bytes == 2) r[i / 2] |= v << (16 * (i & 1));
+        else r[i] = v;
     }
     return r;
 }
-template <typename T, bool VEC> __device__ inline void store_piece(void* base, int64_t at, int left, const Piece<T>& r) {
-    typename T::raw* dst = static_cast<typename T::raw*>(base) + at;
-    if (VEC) {
-        __builtin_memcpy(__builtin_assume_aligned(dst, 16), r.v, 16);
+template <typename T, bool VEC, bool STREAM> __device__ inline void store_piece(void* base, int64_t at, int left, const u32x4_t r) {
+    typedef typename T::raw raw;
+    raw* dst = static_cast<raw*>(base) + at;
+    if constexpr (VEC) {
+        if constexpr (STREAM) __builtin_nontemporal_store(r, reinterpret_cast<u32x4_t*>(dst));
+        else *reinterpret_cast<u32x4_t*>(dst) = r;
     } else {
 #pragma unroll
-        for (int i = 0; i < Piece<T>::N; ++i)
-            if (i < left) dst[i] = r.v[i];
+        for (int i = 0; i < 16 / T::bytes; ++i)
+            if (i < left) dst[i] = (raw)(T::bytes == 2 ? r[i / 2] >> (16 * (i & 1)) : r[i]);
     }
+}
+// Value i of a piece, and a piece of values rounded to T.
+template <typename T> __device__ inline float piece_value(const u32x4_t r, int i) {
+    if constexpr (T::bytes == 2) return to_f32(T{}, (uint16_t)(r[i / 2] >> (16 * (i & 1))));
+    else return to_f32(T{}, r[i]);
+}
+template <typename T> __device__ inline u32x4_t round_piece(const float (&v)[16 / T::bytes]) {
+    u32x4_t r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (T::bytes == 2) r[i] = (uint32_t)from_f32(T{}, v[2 * i]) | ((uint32_t)from_f32(T{}, v[2 * i + 1]) << 16);
+        else r[i] = from_f32(T{}, v[i]);
+    }
+    return r;
+}
+
+// The places (and weights) of up to 64 slots of a token, one a lane, loaded at
+// once: the loops take them from the lanes, so that a token's rows are asked for
+// without waiting for an index each.
+struct Places {
+    int at;
+    float weight;
+    __device__ inline int place(int j) const { return __builtin_amdgcn_readlane(at, j); }
+    __device__ inline float factor(int j) const { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), j)); }
+};
+__device__ inline Places load_places(const RowParams& p, int64_t first, int count, bool weights) {
+    const int lane = threadIdx.x & 63;
+    Places s = {-1, 0.f};
+    if (lane < count) {
+        s.at = p.position[first + lane];
+        if (weights) s.weight = load_weight(p, first + lane);
+    }
+    return s;
 }
 
 // rows[position[t][j]] = x[t]: a workgroup takes a token and 256 pieces of its
 // row, reads them once and writes them top_k times.
-template <typename T, bool VEC> __global__ __launch_bounds__(256) void gather_kernel(const RowParams p) {
-    constexpr int N = Piece<T>::N;
+template <typename T, bool VEC, bool STREAM> __global__ __launch_bounds__(256) void gather_kernel(const RowParams p) {
+    constexpr int N = 16 / T::bytes;
     const int slots = p.tokens * p.top_k, kept = *p.kept;
     const int t = blockIdx.x, c = (blockIdx.y * 256 + threadIdx.x) * N;
-    if (c >= p.n) return;
-    const Piece<T> x = load_piece<T, VEC>(p.in, (int64_t)t * p.n + c, p.n - c);
-    Piece<T> zero = {};
-    for (int j = 0; j < p.top_k; ++j) {
-        const int at = p.position[(int64_t)t * p.top_k + j];
-        if (at < 0 || at >= slots) continue;
-        store_piece<T, VEC>(p.out, (int64_t)at * p.n + c, p.n - c, at < kept ? x : zero);
+    const u32x4_t zero = {0, 0, 0, 0};
+    const u32x4_t x = c < p.n ? load_piece<T, VEC>(p.in, (int64_t)t * p.n + c, p.n - c) : zero;
+    for (int j0 = 0; j0 < p.top_k; j0 += 64) {
+        const int count = min(64, p.top_k - j0);
+        const Places s = load_places(p, (int64_t)t * p.top_k + j0, count, false);
+        for (int j = 0; j < count; ++j) {
+            const int at = s.place(j);
+            if (at >= 0 && at < slots && c < p.n) store_piece<T, VEC, STREAM>(p.out, (int64_t)at * p.n + c, p.n - c, at < kept ? x : zero);
+        }
     }
 }
 
-// y[t] = sum over j of weights[t][j] * rows[position[t][j]]
-template <typename T, bool VEC> __global__ __launch_bounds__(256) void combine_kernel(const RowParams p) {
-    constexpr int N = Piece<T>::N;
+// y[t] = sum over j of weights[t][j] * rows[position[t][j]], U rows asked for
+// together (a dropped slot's load goes to row 0 and is not used, so that no branch
+// stands between the loads).
+template <typename T, bool VEC, bool STREAM, int U> __global__ __launch_bounds__(256) void combine_kernel(const RowParams p) {
+    constexpr int N = 16 / T::bytes;
     const int slots = p.tokens * p.top_k, kept = min(*p.kept, slots);
     const int t = blockIdx.x, c = (blockIdx.y * 256 + threadIdx.x) * N;
-    if (c >= p.n) return;
+    const bool in = c < p.n;
+    const int col = in ? c : 0;
     float sum[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) sum[i] = 0.f;
-    for (int j = 0; j < p.top_k; ++j) {
-        const int64_t s = (int64_t)t * p.top_k + j;
-        const int at = p.position[s];
-        if (at < 0 || at >= kept) continue;
-        const float w = load_weight(p, s);
-        const Piece<T> r = load_piece<T, VEC>(p.in, (int64_t)at * p.n + c, p.n - c);
+    for (int j0 = 0; j0 < p.top_k; j0 += 64) {
+        const Places s = load_places(p, (int64_t)t * p.top_k + j0, min(64, p.top_k - j0), true);
+        for (int j = 0; j < 64 && j0 + j < p.top_k; j += U) {
+            u32x4_t r[U];
 #pragma unroll
-        for (int i = 0; i < N; ++i) sum[i] += w * to_f32(T{}, r.v[i]);
+            for (int k = 0; k < U; ++k) {
+                const int at = s.place(j + k);  // -1 in lanes without a slot
+                r[k] = load_piece<T, VEC>(p.in, (int64_t)(at >= 0 && at < kept ? at : 0) * p.n + col, p.n - col);
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int at = s.place(j + k);
+                if (at < 0 || at >= kept) continue;
+                const float w = s.factor(j + k);
+#pragma unroll
+                for (int i = 0; i < N; ++i) sum[i] += w * piece_value<T>(r[k], i);
+            }
+        }
     }
-    Piece<T> y;
-#pragma unroll
-    for (int i = 0; i < N; ++i) y.v[i] = from_f32(T{}, sum[i]);
-    store_piece<T, VEC>(p.out, (int64_t)t * p.n + c, p.n - c, y);
+    if (in) store_piece<T, VEC, STREAM>(p.out, (int64_t)t * p.n + c, p.n - c, round_piece<T>(sum));
 }
 
 // drows[position[t][j]] = weights[t][j] * dy[t] and dweights[t][j] = <rows[...], dy[t]>:
 // one wave a slot.
-template <typename T, bool VEC> __global__ __launch_bounds__(256) void combine_backward_kernel(const RowParams p) {
-    constexpr int N = Piece<T>::N;
+template <typename T, bool VEC, bool STREAM> __global__ __launch_bounds__(256) void combine_backward_kernel(const RowParams p) {
+    constexpr int N = 16 / T::bytes;
     const int slots = p.tokens * p.top_k, kept = min(*p.kept, slots);
     const int lane = threadIdx.x & 63;
-    const int64_t s = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t s = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (s >= slots) return;
     const int64_t t = s / p.top_k;
     const int at = p.position[s];
@@ -244,18 +303,20 @@ template <typename T, bool VEC> __global__ __launch_bounds__(256) void combine_b
     float dot = 0.f;
     if (at >= 0 && at < slots) {
         for (int c = lane * N; c < p.n; c += 64 * N) {
-            Piece<T> out = {};
+            u32x4_t out = {0, 0, 0, 0};
             if (live) {
-                const Piece<T> d = load_piece<T, VEC>(p.in, t * p.n + c, p.n - c);
-                const Piece<T> r = load_piece<T, VEC>(p.in2, (int64_t)at * p.n + c, p.n - c);
+                const u32x4_t d = load_piece<T, VEC>(p.in, t * p.n + c, p.n - c);
+                const u32x4_t r = load_piece<T, VEC>(p.in2, (int64_t)at * p.n + c, p.n - c);
+                float g[N];
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const float g = to_f32(T{}, d.v[i]);
-                    dot += g * to_f32(T{}, r.v[i]);
-                    out.v[i] = from_f32(T{}, w * g);
+                    g[i] = piece_value<T>(d, i);
+                    dot += g[i] * piece_value<T>(r, i);
+                    g[i] *= w;
                 }
+                out = round_piece<T>(g);
             }
-            store_piece<T, VEC>(p.out, (int64_t)at * p.n + c, p.n - c, out);
+            store_piece<T, VEC, STREAM>(p.out, (int64_t)at * p.n + c, p.n - c, out);
         }
     }
 #pragma unroll
@@ -268,26 +329,33 @@ template <typename T, bool VEC> __global__ __launch_bounds__(256) void combine_b
 
 enum RowOp { GATHER, COMBINE, COMBINE_BACKWARD };
 
-template <typename T, bool VEC> hipError_t launch_rows(RowOp op, const RowParams& p, hipStream_t s) {
-    const int pieces = (p.n + Piece<T>::N - 1) / Piece<T>::N;
+template <typename T, bool VEC, bool STREAM> hipError_t launch_rows(RowOp op, const RowParams& p, hipStream_t s) {
+    const int pieces = (p.n * T::bytes + 15) / 16;
     const dim3 grid((unsigned)p.tokens, (unsigned)((pieces + 255) / 256));
-    if (op == GATHER) gather_kernel<T, VEC><<<grid, 256, 0, s>>>(p);
-    else if (op == COMBINE) combine_kernel<T, VEC><<<grid, 256, 0, s>>>(p);
-    else combine_backward_kernel<T, VEC><<<(unsigned)(((int64_t)p.tokens * p.top_k + 3) / 4), 256, 0, s>>>(p);
+    if (op == GATHER) gather_kernel<T, VEC, STREAM><<<grid, 256, 0, s>>>(p);
+    else if (op == COMBINE && p.top_k <= 2) combine_kernel<T, VEC, STREAM, 2><<<grid, 256, 0, s>>>(p);
+    else if (op == COMBINE && p.top_k <= 4) combine_kernel<T, VEC, STREAM, 4><<<grid, 256, 0, s>>>(p);
+    else if (op == COMBINE) combine_kernel<T, VEC, STREAM, 8><<<grid, 256, 0, s>>>(p);
+    else combine_backward_kernel<T, VEC, STREAM><<<(unsigned)(((int64_t)p.tokens * p.top_k + 3) / 4), 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
+template <typename T> hipError_t launch_rows(RowOp op, const RowParams& p, hipStream_t s) {
+    if ((int64_t)p.n * T::bytes % 16 != 0) return launch_rows<T, false, false>(op, p, s);
+    return p.stream ? launch_rows<T, true, true>(op, p, s) : launch_rows<T, true, false>(op, p, s);
+}
+
 int rows_op(RowOp op, int dtype, const RowParams& p, hipStream_t s) {
-    const bool vec = (int64_t)p.n * (dtype == EXL3_F32 ? 4 : 2) % 16 == 0;
-    hipError_t e;
-    if (dtype == EXL3_F16) e = vec ? launch_rows<F16, true>(op, p, s) : launch_rows<F16, false>(op, p, s);
-    else if (dtype == EXL3_BF16) e = vec ? launch_rows<BF16, true>(op, p, s) : launch_rows<BF16, false>(op, p, s);
-    else e = vec ? launch_rows<F32, true>(op, p, s) : launch_rows<F32, false>(op, p, s);
+    const hipError_t e = dtype == EXL3_F16 ? launch_rows<F16>(op, p, s) : dtype == EXL3_BF16 ? launch_rows<BF16>(op, p, s) : launch_rows<F32>(op, p, s);
     return e == hipSuccess ? EXL3_OK : EXL3_EHIP;
 }
 
 bool misaligned(const void* ptr, uintptr_t to = 16) { return (reinterpret_cast<uintptr_t>(ptr) & (to - 1)) != 0; }
 bool bad_dtype(int32_t d) { return d < EXL3_F16 || d > EXL3_F32; }
+
+bool streams(int64_t tokens, int64_t rows_each, int64_t n, int dtype) {
+    return tokens * rows_each * n * (dtype == EXL3_F32 ? 4 : 2) >= STREAM_BYTES;
+}
 
 // Checks shared by the three row operators: <= 0 is the call's status.
 int row_checks(const void* in, int32_t dtype, int32_t n_tokens, int32_t top_k, int32_t n, const int32_t* position,
@@ -301,15 +369,17 @@ int row_checks(const void* in, int32_t dtype, int32_t n_tokens, int32_t top_k, i
 }
 
 // One chunk while one workgroup sorts the slots alone, else at most
-// SORT_MAX_CHUNKS chunks of whole rounds of SORT_THREADS slots.
-void plan_sort(int slots, int* chunk, int* chunks) {
+// SORT_MAX_CHUNKS chunks of whole rounds of SORT_THREADS slots; fewer where many
+// experts make the table of counts long, as every chunk reads all of it.
+void plan_sort(int slots, int experts, int* chunk, int* chunks) {
     if (slots <= SORT_ONE_CHUNK) {
         *chunk = SORT_ONE_CHUNK;
         *chunks = 1;
         return;
     }
     const int64_t rounds = ((int64_t)slots + SORT_THREADS - 1) / SORT_THREADS;
-    const int64_t per = (rounds + SORT_MAX_CHUNKS - 1) / SORT_MAX_CHUNKS;
+    const int64_t most = min(SORT_MAX_CHUNKS, SORT_MAX_COUNTS / (experts + 1));
+    const int64_t per = (rounds + most - 1) / most;
     *chunk = (int)(per * SORT_THREADS);
     *chunks = (int)((rounds + per - 1) / per);
 }
@@ -328,7 +398,7 @@ using namespace exl3::moe;
 int64_t exl3_moe_workspace_bytes(int32_t n_slots, int32_t n_experts) {
     if (bad_sort(n_slots, n_experts)) return EXL3_EINVAL;
     int chunk, chunks;
-    plan_sort(n_slots, &chunk, &chunks);
+    plan_sort(n_slots, n_experts, &chunk, &chunks);
     return chunks == 1 ? 0 : (int64_t)chunks * (n_experts + 1) * 4;
 }
 
@@ -343,7 +413,7 @@ int exl3_moe_sort(const void* ids, int32_t id_bytes, int32_t n_slots, int32_t n_
     const int64_t need = exl3_moe_workspace_bytes(n_slots, n_experts);
     if (need > 0 && (!workspace || (int64_t)workspace_bytes < need)) return EXL3_EWORKSPACE;
     SortParams p = {ids, id_bytes, n_slots, n_experts, 0, 0, static_cast<int*>(workspace), order, position, offsets};
-    plan_sort(n_slots, &p.chunk, &p.chunks);
+    plan_sort(n_slots, n_experts, &p.chunk, &p.chunks);
     hipStream_t s = (hipStream_t)stream;
     if (p.chunks > 1) {
         count_kernel<<<p.chunks, SORT_THREADS, 0, s>>>(p);
@@ -357,7 +427,7 @@ int exl3_moe_gather(const void* x, int32_t dtype, int32_t n_tokens, int32_t top_
                     const int32_t* kept, void* rows, void* stream) {
     const int rc = row_checks(x, dtype, n_tokens, top_k, n, position, kept, rows);
     if (rc <= 0) return rc;
-    const RowParams p = {x, nullptr, n_tokens, top_k, n, position, kept, nullptr, EXL3_F32, rows, nullptr};
+    const RowParams p = {x, nullptr, n_tokens, top_k, n, position, kept, nullptr, EXL3_F32, rows, nullptr, streams(n_tokens, top_k, n, dtype)};
     return rows_op(GATHER, dtype, p, (hipStream_t)stream);
 }
 
@@ -368,7 +438,7 @@ int exl3_moe_combine(const void* rows, int32_t dtype, int32_t n_tokens, int32_t 
     const int rc = row_checks(rows, dtype, n_tokens, top_k, n, position, kept, y);
     if (rc <= 0) return rc;
     if (misaligned(weights)) return EXL3_EINVAL;
-    const RowParams p = {rows, nullptr, n_tokens, top_k, n, position, kept, weights, weights_dtype, y, nullptr};
+    const RowParams p = {rows, nullptr, n_tokens, top_k, n, position, kept, weights, weights_dtype, y, nullptr, streams(n_tokens, 1, n, dtype)};
     return rows_op(COMBINE, dtype, p, (hipStream_t)stream);
 }
 
@@ -380,7 +450,7 @@ int exl3_moe_combine_backward(const void* dy, const void* rows, int32_t dtype, i
     if (rc <= 0) return rc;
     if (!rows || !weights || !dweights || misaligned(rows) || misaligned(weights) || misaligned(dweights)) return EXL3_EINVAL;
     if (drows == rows || dweights == weights) return EXL3_EINVAL;
-    const RowParams p = {dy, rows, n_tokens, top_k, n, position, kept, weights, weights_dtype, drows, dweights};
+    const RowParams p = {dy, rows, n_tokens, top_k, n, position, kept, weights, weights_dtype, drows, dweights, streams(n_tokens, top_k, n, dtype)};
     return rows_op(COMBINE_BACKWARD, dtype, p, (hipStream_t)stream);
 }
 

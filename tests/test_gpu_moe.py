@@ -47,7 +47,7 @@ def slack(dtype):
 # ---- sort ----
 
 @pytest.mark.parametrize("id_type", [np.int32, np.int64])
-@pytest.mark.parametrize("tokens, top_k, experts", [(1, 1, 1), (1, 8, 64), (5, 2, 8), (64, 1, 3), (100, 3, 1024), (512, 8, 64), (513, 8, 64),
+@pytest.mark.parametrize("tokens, top_k, experts", [(1, 1, 1), (1, 8, 64), (5, 2, 8), (64, 1, 3), (100, 3, 1024), (128, 8, 64), (129, 8, 64), (512, 8, 64), (513, 8, 64),
                                                     (1365, 3, 200), (1366, 3, 200), (9000, 8, 128), (131072, 2, 7), (40000, 4, 1024)])
 def test_sort(ex, tokens, top_k, experts, id_type):
     ids = random_ids(np.random.default_rng([1, tokens, top_k, experts]), tokens, top_k, experts, dtype=id_type)
@@ -165,6 +165,35 @@ def test_combine_gradients_against_differences(ex):
         step[t, 5] = 1
         diff = ((ex.moe_gather(x + step, pos, at) - ex.moe_gather(x - step, pos, at)).double() * g.double()).sum() / 2
         assert abs(float(diff) - float(dx[t, 5])) < 1e-4
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_results_of_32_mib_and_more(ex, dtype):
+    """Large results are stored another way: checked whole, on the GPU, in float64."""
+    rng = np.random.default_rng(8)
+    tokens, top_k, experts, n = 4100, 2, 9, 4096 if dtype == "fp32" else 8192
+    position, offsets, pos, at = route(rng, tokens, top_k, experts)
+    kept, dt = int(offsets[-1]), DTYPES[dtype]
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.randn((tokens, n), generator=gen, device="cuda").to(dt)
+    weights = torch.rand((tokens, top_k), generator=gen, device="cuda")
+    flat = pos.long().reshape(-1)
+    rows = ex.moe_gather(x, pos, at)
+    ref = torch.zeros_like(rows)
+    ref[flat] = x.repeat_interleave(top_k, 0)
+    ref[kept:] = 0
+    assert torch.equal(rows, ref)
+    w = torch.where(pos < kept, weights, 0.0).double()
+    y = ex.moe_combine(rows, pos, at, weights).double()
+    ref = (w[..., None] * rows.double()[pos.long()]).sum(1)
+    size = (w[..., None] * rows.double()[pos.long()].abs()).sum(1)
+    tol = (top_k + 1) * HALF32 * size
+    assert bool(((y - ref).abs() <= tol + R.half_step(dt) * (ref.abs() + tol) + slack(dt)).all())
+    drows, _ = ex.moe_combine_backward(x, rows, pos, at, weights)
+    ref = torch.zeros(rows.shape, dtype=torch.float64, device="cuda")
+    ref[flat] = (w[..., None] * x.double()[:, None]).flatten(0, 1)
+    tol = HALF32 * ref.abs()
+    assert bool(((drows.double() - ref).abs() <= tol + R.half_step(dt) * (ref.abs() + tol) + slack(dt)).all())
 
 
 def test_positions_outside_the_slots_are_dropped(ex):
