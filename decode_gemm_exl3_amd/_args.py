@@ -49,16 +49,16 @@ def need(t, name: str, dtypes, shape) -> int:
     """Checks all but the device; returns the address."""
     if not isinstance(t, torch.Tensor):
         raise Exl3Error(f"{name}: expected a torch tensor")
+    at = t.data_ptr()
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and not at & 15:
+        return at
     if t.dtype not in dtypes:
         raise Exl3Error(f"{name}: dtype {t.dtype}, expected one of {tuple(str(d) for d in dtypes)}")
     if t.shape != shape:
         raise Exl3Error(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise Exl3Error(f"{name}: must be contiguous")
-    at = t.data_ptr()
-    if at & 15:
-        raise Exl3Error(f"{name}: data must be 16-byte aligned (a view at an offset is not)")
-    return at
+    raise Exl3Error(f"{name}: data must be 16-byte aligned (a view at an offset is not)")
 
 
 def result(t, name: str, like, dtype, shape):
@@ -69,10 +69,10 @@ def result(t, name: str, like, dtype, shape):
     return t, need(t, name, (dtype,), shape)
 
 
-def need_rows(t, name: str) -> int:
+def need_rows(t, name: str):
     """A 2-dimensional floating tensor whose rows are contiguous and start at
-    multiples of 16 bytes; returns the row stride in elements."""
-    dtype_code(t, name)
+    multiples of 16 bytes: (rows, columns, row stride in elements, exl3_dtype, address)."""
+    code = dtype_code(t, name)
     if t.dim() != 2:
         raise Exl3Error(f"{name}: expected two dimensions, got shape {tuple(t.shape)}")
     rows, n = t.shape
@@ -81,9 +81,10 @@ def need_rows(t, name: str) -> int:
         ld = n
     if (inner != 1 and n > 1) or ld < n:
         raise Exl3Error(f"{name}: the values of a row must be contiguous and rows must not overlap")
-    if t.data_ptr() & 15 or ld * t.element_size() & 15:
+    at = t.data_ptr()
+    if (at | ld * (4 if code == 2 else 2)) & 15:
         raise Exl3Error(f"{name}: rows must start at multiples of 16 bytes")
-    return ld
+    return rows, n, ld, code, at
 
 
 def on_device(dev: int, **tensors) -> None:

@@ -10,10 +10,12 @@ offsets[g] .. offsets[g + 1] - 1 go through weight g.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import Exl3Error, _check
-from ._args import (BYTES, FLOATS, I32, I64, INDEX, SIZE, VOID, Function, call, dtype_code, need, need_rows, on_device,
+from ._args import (BYTES, I32, I64, INDEX, SIZE, VOID, Function, call, dtype_code, need, need_rows, on_device,
                     result, scratch)
 
 BLOCK = 32  # EXL3_MXFP4_BLOCK
@@ -33,15 +35,14 @@ def _blocks(n: int, name: str) -> int:
 
 def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     """x [rows, n] to (codes [rows, n / 2], scales [rows, n / 32])."""
-    ld = need_rows(x, "x")
-    rows, n = x.shape
+    rows, n, ld, code, at = need_rows(x, "x")
     blocks = _blocks(n, "x")
     codes, c = result(codes, "codes", x, torch.uint8, (rows, n // 2))
     scales, s = result(scales, "scales", x, torch.uint8, (rows, blocks))
     dev = x.get_device()
     if not dev == codes.get_device() == scales.get_device() >= 0:
         on_device(dev, x=x, codes=codes, scales=scales)
-    call(_quantize, dev, stream, x.data_ptr(), FLOATS[x.dtype], rows, n, ld, c, s)
+    call(_quantize, dev, stream, at, code, rows, n, ld, c, s)
     return codes, scales
 
 
@@ -61,6 +62,7 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None)
     return out
 
 
+@functools.lru_cache(maxsize=1024)  # a size, of sizes alone: 0.6 us of a call otherwise
 def mxfp4_workspace_bytes(rows: int, n_in: int, groups: int = 1) -> int:
     """Bytes of device scratch that mxfp4_linear needs (0: none)."""
     n = (_bytes.bound or _bytes.load())(rows, groups, n_in)
@@ -73,11 +75,12 @@ def _weight(codes, scales, offsets, n_in: int, blocks: int):
     """Addresses of a weight and its offsets, with the group count and n_out."""
     if not isinstance(codes, torch.Tensor) or codes.dim() != (2 if offsets is None else 3):
         raise Exl3Error("codes: expected a torch tensor [n_out, n_in / 2], or [groups, n_out, n_in / 2] with offsets")
-    lead = codes.shape[:-1]
-    c, s = need(codes, "codes", BYTES, (*lead, n_in // 2)), need(scales, "scales", BYTES, (*lead, blocks))
     if offsets is None:
-        return c, s, None, 1, lead[0]
-    return c, s, need(offsets, "offsets", INDEX, (lead[0] + 1,)), lead[0], lead[1]
+        n_out = codes.shape[0]
+        return need(codes, "codes", BYTES, (n_out, n_in // 2)), need(scales, "scales", BYTES, (n_out, blocks)), None, 1, n_out
+    groups, n_out = codes.shape[:2]
+    return (need(codes, "codes", BYTES, (groups, n_out, n_in // 2)), need(scales, "scales", BYTES, (groups, n_out, blocks)),
+            need(offsets, "offsets", INDEX, (groups + 1,)), groups, n_out)
 
 
 def mxfp4_matmul(x_codes, x_scales, codes, scales, dtype=torch.bfloat16, offsets=None, y=None, stream=None):
@@ -105,15 +108,13 @@ def mxfp4_linear(x, codes, scales, offsets=None, workspace=None, y=None, stream=
     workspace: a uint8 device tensor of mxfp4_workspace_bytes(m, n_in, groups); by
     default new scratch where that is not 0.
     """
-    ld = need_rows(x, "x")
-    m, n_in = x.shape
+    m, n_in, ld, code, src = need_rows(x, "x")
     c, s, at, groups, n_out = _weight(codes, scales, offsets, n_in, _blocks(n_in, "x"))
-    dtype = x.dtype
-    y, o = result(y, "y", x, dtype, (m, n_out))
+    y, o = result(y, "y", x, x.dtype, (m, n_out))
     dev = x.get_device()
     if not (dev == codes.get_device() == scales.get_device() == y.get_device() >= 0
             and (at is None or offsets.get_device() == dev)):
         on_device(dev, x=x, codes=codes, scales=scales, offsets=offsets, y=y)
     ws, nbytes, held = scratch(workspace, 0 if workspace is not None else mxfp4_workspace_bytes(m, n_in, groups), x, stream)
-    call(_linear, dev, stream, x.data_ptr(), FLOATS[dtype], m, ld, at, groups, c, s, n_in, n_out, o, ws, nbytes)
+    call(_linear, dev, stream, src, code, m, ld, at, groups, c, s, n_in, n_out, o, ws, nbytes)
     return y
