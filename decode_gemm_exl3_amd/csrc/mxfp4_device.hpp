@@ -128,13 +128,22 @@ struct RowTile {
 };
 __device__ inline int clamp_row(int v, int rows) { return v < 0 ? 0 : (v > rows ? rows : v); }
 
+// Running sum over the lanes of a wave: DPP shifts inside rows of 16 lanes, then
+// each row's last lane to the rows behind it.
+__device__ inline int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);   // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);   // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);   // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+    return v;
+}
+
 __device__ inline RowTile find_tile(const int* offsets, int n_groups, int rows, int tile, int bm) {
-    RowTile t = {0, 0, 0};
     if (!offsets) {
-        t.row0 = tile * bm;
-        t.rows = min(bm, rows - t.row0);
-        if (t.rows < 0) t.rows = 0;
-        return t;
+        const int row0 = tile * bm;
+        return RowTile{0, row0, max(min(bm, rows - row0), 0)};
     }
     const int lane = threadIdx.x & 63;
     int before = 0;
@@ -147,29 +156,16 @@ __device__ inline RowTile find_tile(const int* offsets, int n_groups, int rows, 
         }
         const int count = hi > lo ? hi - lo : 0;
         const int tiles = (count + bm - 1) / bm;
-        int sum = tiles;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int up = __shfl_up(sum, d);
-            if (lane >= d) sum += up;
-        }
-        const uint64_t past = __ballot(before + sum > tile);
+        const int sum = before + wave_scan(tiles);
+        const uint64_t past = __ballot(sum > tile);
         if (past) {
             const int at = __ffsll((unsigned long long)past) - 1;
-            const int first = __shfl(before + sum - tiles, at);
-            const int glo = __shfl(lo, at), gcount = __shfl(count, at);
-            t.group = g0 + at;
-            t.row0 = glo + (tile - first) * bm;
-            t.rows = min(bm, gcount - (tile - first) * bm);
-            break;
+            const int within = (tile - __builtin_amdgcn_readlane(sum - tiles, at)) * bm;
+            return RowTile{g0 + at, __builtin_amdgcn_readlane(lo, at) + within, min(bm, __builtin_amdgcn_readlane(count, at) - within)};
         }
-        before += __shfl(sum, 63);
+        before = __builtin_amdgcn_readlane(sum, 63);
     }
-    // the same in every lane: keep them in scalar registers
-    t.group = __builtin_amdgcn_readfirstlane(t.group);
-    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
-    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
-    return t;
+    return RowTile{0, 0, 0};
 }
 
 // Most row tiles that `rows` rows in n_groups groups and the rows behind them make.
