@@ -2,9 +2,8 @@
 
 The library reads and writes raw device memory, so every tensor is checked for
 element type, shape, contiguity, 16-byte alignment and device before a call
-reaches it.  The calls run on the device of their first tensor: the launch goes
-to `stream` or to that device's current stream, with the device made current for
-the time of the call.
+reaches it.  The calls run on the device of their first tensor, on `stream` or on
+that device's current stream.
 """
 from __future__ import annotations
 
@@ -105,26 +104,28 @@ def on_device(dev: int, **tensors) -> None:
 _current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def call(fn: Function, dev: int, stream, *args) -> None:
-    """fn(*args, stream) on GPU `dev`."""
+def call(fn: Function, dev: int, *args) -> None:
+    """fn(*args, stream) on GPU `dev` and its current stream."""
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return call(fn, dev, stream, *args)
-    if stream is None:
-        handle = _current(dev)
-    elif stream.device_index != dev:
-        raise Exl3Error(f"{fn.name}: the stream is of GPU {stream.device_index}, the tensors are on GPU {dev}")
-    else:
-        handle = stream.cuda_stream
-    status = (fn.bound or fn.load())(*args, handle)
+            return call(fn, dev, *args)
+    status = (fn.bound or fn.load())(*args, _current(dev))
     if status != 0:
         _check(status, fn.name)
 
 
-def scratch(workspace, nbytes: int, like, stream):
+def on_stream(stream, fn, first, *args):
+    """fn(first, *args) with `stream` the current one, so that results and scratch
+    come from its memory as well and nothing of another stream is written early."""
+    if isinstance(first, torch.Tensor) and first.get_device() >= 0 and first.get_device() != stream.device_index:
+        raise Exl3Error(f"{fn.__name__}: the stream is of GPU {stream.device_index}, the tensors are on GPU {first.get_device()}")
+    with torch.cuda.stream(stream):
+        return fn(first, *args)
+
+
+def scratch(workspace, nbytes: int, like):
     """Address and size of `workspace` when given, else of scratch of the caching
-    allocator, which is kept from reuse until `stream` is done with it; the third
-    value keeps it alive for the call."""
+    allocator; the third value keeps it alive for the call."""
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor):
             raise Exl3Error("workspace: expected a torch tensor")
@@ -135,6 +136,4 @@ def scratch(workspace, nbytes: int, like, stream):
     if nbytes == 0:
         return None, 0, None
     buf = like.new_empty(nbytes, dtype=torch.uint8)
-    if stream is not None:
-        buf.record_stream(stream)
     return buf.data_ptr(), nbytes, buf

@@ -364,7 +364,8 @@ int row_checks(const void* in, int32_t dtype, int32_t n_tokens, int32_t top_k, i
     if (n_tokens == 0) return EXL3_OK;
     if (!in || !position || !kept || !out || in == out) return EXL3_EINVAL;
     if (misaligned(in) || misaligned(position) || misaligned(kept, 4) || misaligned(out)) return EXL3_EINVAL;
-    if ((int64_t)n_tokens * top_k > 0x7FFFFFFF || n > (1 << 24)) return EXL3_EUNSUPPORTED;
+    // a launch takes fewer than 2^32 threads: a workgroup a token, a wave a slot
+    if (n_tokens >= (1 << 24) || (int64_t)n_tokens * top_k >= (1 << 26) - 4 || n > (1 << 24)) return EXL3_EUNSUPPORTED;
     return 1;
 }
 

@@ -418,26 +418,31 @@ __device__ inline void store_tile(const f32x16_t (&acc)[RT][CT], char* part, con
     }
 }
 
-// Some rows, or few tiles: a workgroup of four waves owns 64 rows and 64 outputs,
-// each wave a quarter.  Stages of a span (256 bytes of codes a row of both sides)
-// go straight into a ring in LDS, MEDIUM_RING - 1 of them ahead: a stage is
-// little work (8 MFMAs a wave), so it is the bytes in flight that count.  Block b
-// of row r sits in slot b ^ (r & 15) of the row's 256 bytes.
-constexpr int MEDIUM_RING = 4;
+// Some rows, or few tiles: a workgroup of four waves owns T rows and T outputs.
+// Stages of a span (256 bytes of codes a row of both sides) go straight into a
+// ring in LDS, all but one of it ahead: a stage is little work, so it is the bytes
+// in flight that count.  T = 64: each wave a quarter of the tile, 8 MFMAs a stage.
+// T = 32: each wave the whole tile over a quarter of the stage's inputs, and the
+// waves' sums meet in LDS at the end; four times the workgroups where 64 x 64
+// tiles would leave most of the card idle.  Block b of row r sits in slot
+// b ^ (r & 15) of the row's 256 bytes.
+template <int T> constexpr int MEDIUM_RING = T == 64 ? 4 : 8;
 
-template <typename OT, bool WHOLE>
+template <typename OT, int T, bool WHOLE>
 __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int row_tiles, int col_tiles) {
-    constexpr int SDW = SCALE_DWORDS<WHOLE>, LOADS = 8 + SDW / 2;
-    constexpr int BUF = 128 * 16 + 128 * SDW / 4;  // slots: codes (64 rows, 64 weight rows), then scales
-    static_assert(store_part_bytes<OT, 1>() * 4 <= MEDIUM_RING * BUF * 16, "the waves' parts fit");
-    __shared__ i32x4_t lds[MEDIUM_RING * BUF];
+    constexpr int SDW = SCALE_DWORDS<WHOLE>, RING = MEDIUM_RING<T>;
+    constexpr int CODE_LOADS = T / 8, SCALE_LOADS = T * SDW / 128, LOADS = CODE_LOADS + SCALE_LOADS;  // of a wave and stage
+    constexpr int BUF = 2 * T * 16 + 2 * T * SDW / 4;  // slots: codes (rows, then weight rows), then scales
+    constexpr int STEPS = T == 64 ? 8 : 2;             // MFMAs of a wave and stage
+    static_assert(store_part_bytes<OT, 1>() * 4 <= RING * BUF * 16, "the waves' parts fit");
+    __shared__ i32x4_t lds[RING * BUF];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 31, h = lane >> 5, wy = wave >> 1, wx = wave & 1;
+    const int r = lane & 31, h = lane >> 5, wy = T == 64 ? wave >> 1 : 0, wx = T == 64 ? wave & 1 : 0;
     int row_tile, col;
     if (!tile_of(xcd_tile(blockIdx.x), row_tiles, col_tiles, &row_tile, &col)) return;
-    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, row_tile, 64);
+    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, row_tile, T);
     if (t.rows == 0) return;
-    const int n0 = col * 64, cols = min(64, p.n_out - n0);
+    const int n0 = col * T, cols = min(T, p.n_out - n0);
     const int nb = p.n_in / BLOCK, stages = (nb + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
 
     f32x16_t acc[1][1];
@@ -445,72 +450,90 @@ __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int 
     for (int i = 0; i < 16; ++i) acc[0][0][i] = 0.f;
 
     if (t.group < p.n_groups) {
-        const Side sides[2] = {side(p.xc, p.xs, t.row0, t.rows, nb),
-                               side(p.wc, p.ws, (int64_t)t.group * p.n_out + n0, cols, nb)};
-        // load i of a wave and side: row 16 i + 4 wave + lane / 16, slot lane % 16; rows behind the tile re-read its last
+        const Side x = side(p.xc, p.xs, t.row0, t.rows, nb), w = side(p.wc, p.ws, (int64_t)t.group * p.n_out + n0, cols, nb);
+        // Rows of both sides together, the weight's from T on.  Load i of a wave: row
+        // 16 i + 4 wave + lane / 16, slot lane % 16; rows behind a side's end re-read its last.
         const int srow = 4 * wave + (lane >> 4), block = (lane & 15) ^ srow;
-        uint32_t row_at[2][4], scale_at[2][SDW / 4], shift[2];
+        uint32_t row_at[CODE_LOADS], scale_at[SCALE_LOADS];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) row_at[s][i] = (uint32_t)min(16 * i + srow, sides[s].rows - 1) * (nb * 16) + 16 * block;
-#pragma unroll
-            for (int i = 0; i < SDW / 4; ++i)
-                scale_at[s][i] = (uint32_t)min((4 * i + wave) * (64 / SDW) + lane / SDW, sides[s].rows - 1) * nb + sides[s].lead;
-            shift[s] = ((uint32_t)min((s ? wx : wy) * 32 + r, sides[s].rows - 1) * nb + sides[s].lead) & 3u;
+        for (int i = 0; i < CODE_LOADS; ++i) {
+            const int row = 16 * i + srow;
+            row_at[i] = (uint32_t)(16 * i < T ? min(row, x.rows - 1) : min(row - T, w.rows - 1)) * (nb * 16) + 16 * block;
         }
+#pragma unroll
+        for (int i = 0; i < SCALE_LOADS; ++i) {
+            const int row = (4 * i + wave) * (64 / SDW) + lane / SDW;
+            scale_at[i] = row < T ? (uint32_t)min(row, x.rows - 1) * nb + x.lead : (uint32_t)min(row - T, w.rows - 1) * nb + w.lead;
+        }
+        const uint32_t xshift = ((uint32_t)min(wy * 32 + r, x.rows - 1) * nb + x.lead) & 3u;
+        const uint32_t wshift = ((uint32_t)min(wx * 32 + r, w.rows - 1) * nb + w.lead) & 3u;
         auto ask = [&](int st) {  // behind the last stage: zeros
-            i32x4_t* const buf = lds + st % MEDIUM_RING * BUF;
+            i32x4_t* const buf = lds + st % RING * BUF;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
+            for (int i = 0; i < CODE_LOADS; ++i)
+                load16_to_lds(16 * i < T ? x.codes : w.codes, buf + i * 256 + wave * 64, st * SPAN_BLOCKS + block < nb ? row_at[i] : OUTSIDE,
+                              (uint32_t)st * 256);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    load16_to_lds(sides[s].codes, buf + s * 1024 + i * 256 + wave * 64, st * SPAN_BLOCKS + block < nb ? row_at[s][i] : OUTSIDE,
-                                  (uint32_t)st * 256);
-#pragma unroll
-                for (int i = 0; i < SDW / 4; ++i)
-                    load4_to_lds(sides[s].scales, reinterpret_cast<uint32_t*>(buf + 2048 + s * 16 * SDW) + (4 * i + wave) * 64,
-                                 scale_offset<WHOLE>(scale_at[s][i], lane % SDW, st, nb), (uint32_t)st * SPAN_BLOCKS);
-            }
+            for (int i = 0; i < SCALE_LOADS; ++i)
+                load4_to_lds((4 * i + wave) * (64 / SDW) < T ? x.scales : w.scales, reinterpret_cast<uint32_t*>(buf + 2 * T * 16) + (4 * i + wave) * 64,
+                             scale_offset<WHOLE>(scale_at[i], lane % SDW, st, nb), (uint32_t)st * SPAN_BLOCKS);
         };
 #pragma unroll
-        for (int k = 0; k < MEDIUM_RING - 1; ++k) ask(k);
+        for (int k = 0; k < RING - 1; ++k) ask(k);
         for (int st = 0; st < stages; ++st) {
             // this stage has landed in every wave, and the one before it is read
-            constexpr int PENDING = (MEDIUM_RING - 2) * LOADS;
+            constexpr int PENDING = (RING - 2) * LOADS;
             static_assert(PENDING < 64, "a wait counts to 63");
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(0x0070 | (PENDING & 15) | ((PENDING >> 4) << 14));  // lgkmcnt(0), vmcnt(PENDING)
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
-            ask(st + MEDIUM_RING - 1);
-            const i32x4_t* const buf = lds + st % MEDIUM_RING * BUF;
-            const uint32_t* const xs = reinterpret_cast<const uint32_t*>(buf + 2048) + (wy * 32 + r) * SDW + 2 * h;
-            const uint32_t* const ws = reinterpret_cast<const uint32_t*>(buf + 2048 + 16 * SDW) + (wx * 32 + r) * SDW + 2 * h;
-            const int left = nb - st * SPAN_BLOCKS - 8 * h;
-            uint32_t xsc[2], wsc[2];
+            ask(st + RING - 1);
+            // This lane's blocks: T = 64, the 8 of its half, two dwords of scales; T = 32,
+            // two of the wave's four, h and h + 2, so that one dword holds the scales.
+            const i32x4_t* const buf = lds + st % RING * BUF;
+            const int first = T == 64 ? 8 * h : 4 * wave, left = nb - st * SPAN_BLOCKS - first;
+            const uint32_t* const xs = reinterpret_cast<const uint32_t*>(buf + 2 * T * 16) + (wy * 32 + r) * SDW + first / 4;
+            const uint32_t* const ws = reinterpret_cast<const uint32_t*>(buf + 2 * T * 16) + (T + wx * 32 + r) * SDW + first / 4;
+            uint32_t xsc[T / 32], wsc[T / 32];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                xsc[e] = staged_scales<WHOLE>(xs + e, shift[0], left - 4 * e);
-                wsc[e] = staged_scales<WHOLE>(ws + e, shift[1], left - 4 * e);
+            for (int e = 0; e < T / 32; ++e) {
+                xsc[e] = staged_scales<WHOLE>(xs + e, xshift, left - 4 * e);
+                wsc[e] = staged_scales<WHOLE>(ws + e, wshift, left - 4 * e);
+            }
+            if constexpr (T == 32) {  // bytes h and h + 2 to 0 and 2
+                xsc[0] >>= 8 * h;
+                wsc[0] >>= 8 * h;
             }
             auto step = [&](auto jc) {
-                constexpr int j = decltype(jc)::value;  // block 8 h + j of this half's
-                const int slot = (8 * h + j) ^ (r & 15);
-                const i32x4_t xv = buf[(wy * 32 + r) * 16 + slot], wv = buf[1024 + (wx * 32 + r) * 16 + slot];
-                acc[0][0] = mfma32<j & 3>(wv, wsc[j >> 2], xv, xsc[j >> 2], acc[0][0]);
+                constexpr int j = decltype(jc)::value;
+                const int slot = (T == 64 ? 8 * h + j : first + h + 2 * j) ^ (r & 15);
+                const i32x4_t xv = buf[(wy * 32 + r) * 16 + slot], wv = buf[(T + wx * 32 + r) * 16 + slot];
+                acc[0][0] = mfma32<T == 64 ? j & 3 : 2 * j>(wv, wsc[T == 64 ? j >> 2 : 0], xv, xsc[T == 64 ? j >> 2 : 0], acc[0][0]);
             };
             step(std::integral_constant<int, 0>{});
             step(std::integral_constant<int, 1>{});
-            step(std::integral_constant<int, 2>{});
-            step(std::integral_constant<int, 3>{});
-            step(std::integral_constant<int, 4>{});
-            step(std::integral_constant<int, 5>{});
-            step(std::integral_constant<int, 6>{});
-            step(std::integral_constant<int, 7>{});
+            if constexpr (STEPS == 8) {
+                step(std::integral_constant<int, 2>{});
+                step(std::integral_constant<int, 3>{});
+                step(std::integral_constant<int, 4>{});
+                step(std::integral_constant<int, 5>{});
+                step(std::integral_constant<int, 6>{});
+                step(std::integral_constant<int, 7>{});
+            }
         }
         __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0): nothing is on its way, the ring is read
         __builtin_amdgcn_s_barrier();
+    }
+    if constexpr (T == 32) {
+        // the four waves' sums, added in order by wave 0
+        f32x16_t* const sums = reinterpret_cast<f32x16_t*>(lds);
+        if (wave > 0) sums[(wave - 1) * 64 + lane] = acc[0][0];
+        __syncthreads();
+        if (wave > 0) return;
+#pragma unroll
+        for (int v = 0; v < 3; ++v) acc[0][0] += sums[v * 64 + lane];
+        __builtin_amdgcn_wave_barrier();
     }
     constexpr int PART = store_part_bytes<OT, 1>();
     store_tile<OT, 1, 1>(acc, reinterpret_cast<char*>(lds) + wave * PART, p, t.row0 + wy * 32, t.rows - wy * 32, n0 + wx * 32);
@@ -750,20 +773,16 @@ template <typename OT, bool FUSED> hipError_t launch_small(const ProductParams& 
     return hipGetLastError();
 }
 
-inline bool tiles_fit(int64_t rows, int64_t cols) { return xcd_padded(rows * cols) <= 0x7FFFFFFF; }
-
-template <typename OT> hipError_t launch_medium(const ProductParams& p, hipStream_t s) {
-    const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, 64), cols = (p.n_out + 63) / 64;
-    if (!tiles_fit(rows, cols)) return hipErrorInvalidConfiguration;
+template <typename OT, int T> hipError_t launch_medium(const ProductParams& p, hipStream_t s) {
+    const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, T), cols = (p.n_out + T - 1) / T;
     const unsigned tiles = (unsigned)xcd_padded(rows * cols);
-    if (p.n_in % (4 * BLOCK) == 0) medium_kernel<OT, true><<<tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
-    else medium_kernel<OT, false><<<tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
+    if (p.n_in % (4 * BLOCK) == 0) medium_kernel<OT, T, true><<<tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
+    else medium_kernel<OT, T, false><<<tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
     return hipGetLastError();
 }
 
 template <typename OT, int RT, int CT> hipError_t launch_gemm(const ProductParams& p, hipStream_t s) {
     const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, 64 * RT), cols = (p.n_out + 64 * CT - 1) / (64 * CT);
-    if (!tiles_fit(rows, cols)) return hipErrorInvalidConfiguration;
     const unsigned tiles = (unsigned)xcd_padded(rows * cols);
     if (p.n_in % (4 * BLOCK) == 0) gemm_kernel<OT, RT, CT, true><<<tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
     else gemm_kernel<OT, RT, CT, false><<<tiles, 256, 0, s>>>(p, (int)rows, (int)cols);
@@ -786,9 +805,13 @@ template <typename OT> hipError_t launch_product(const ProductParams& p, hipStre
     // groups 2048 -> 2816 50 and 61.
     const int64_t m = typical_rows(p.rows, p.n_groups);
     if (p.offsets ? m <= 8 : m <= 16 || (m <= 32 && p.n_out <= 4096)) return launch_small<OT, false>(p, s);
-    // 64 x 64 tiles up to two rounds of them: 512 rows 4096 -> 4096 15.0 us against
-    // 18.5 in 128 x 128, 1024 rows 28.1 against 18.4.
-    if (expected_tiles(p, 64) * ((p.n_out + 63) / 64) <= 2 * CUS) return launch_medium<OT>(p, s);
+    // 32 x 32 tiles in one round: 64 rows 14336 -> 4096 (256 of them) 15.0 us against
+    // 25.4 in 64 x 64, 256 rows 4096 -> 1024 6.2 against 8.7; two rounds lose (128
+    // rows 14336 -> 4096 26.1 against 24.4, 1024 -> 4096 7.3 against 5.1).
+    if (expected_tiles(p, 32) * ((p.n_out + 31) / 32) <= CUS) return launch_medium<OT, 32>(p, s);
+    // 64 x 64 tiles up to two rounds: 512 rows 4096 -> 4096 15.0 us against 18.5 in
+    // 128 x 128, 1024 rows 28.1 against 18.4.
+    if (expected_tiles(p, 64) * ((p.n_out + 63) / 64) <= 2 * CUS) return launch_medium<OT, 64>(p, s);
     // 128 x 128 tiles (two workgroups a CU) against 256 x 256 (one).  A round of the
     // former takes 0.7 of the latter's, and with many tiles a CU only whole rounds
     // of the large ones count, as the small ones end one by one.  2048 rows 4096 ->
@@ -827,9 +850,9 @@ bool bad_ld(int64_t ldx, int32_t n, int32_t dtype) { return ldx < n || ldx * dty
 
 int64_t codes_bytes(int64_t rows, int32_t n) { return (rows * (n / 2) + 255) & ~int64_t(255); }
 
-// Workgroups that one launch takes of quantise and dequantise: 2^31 - 1.
+// More than one launch of quantise or dequantise takes: 2^24 - 1 workgroups (fewer than 2^32 threads).
 bool too_many_units(int64_t rows, int32_t n) {
-    return rows > ((int64_t)1 << 40) || rows * (n / 8) > (int64_t)0x7FFFFFFF * 256 * QUANT_UNROLL;
+    return rows > ((int64_t)1 << 40) || rows * (n / 8) > (int64_t)0xFFFFFF * 256 * QUANT_UNROLL;
 }
 
 int product_checks(int32_t rows, const int32_t* offsets, int32_t n_groups, const uint8_t* codes, const uint8_t* scales,
@@ -840,6 +863,8 @@ int product_checks(int32_t rows, const int32_t* offsets, int32_t n_groups, const
     if (!codes || !scales || !y) return EXL3_EINVAL;
     if (misaligned(codes) || misaligned(scales) || misaligned(y) || (reinterpret_cast<uintptr_t>(offsets) & 3)) return EXL3_EINVAL;
     if (n_in > (1 << 20) || n_groups > 4096 || rows > (1 << 23) || n_out > (1 << 24)) return EXL3_EUNSUPPORTED;
+    // a launch takes fewer than 2^32 threads: 2^24 workgroups of the smallest tile that many outputs come in
+    if ((((int64_t)rows >> 6) + n_groups + 2) * (((int64_t)n_out >> 6) + 1) >= (1 << 24) - XCDS * XCD_UNIT) return EXL3_EUNSUPPORTED;
     return 1;  // proceed
 }
 

@@ -18,7 +18,7 @@ from __future__ import annotations
 import torch
 
 from . import Exl3Error
-from ._args import FLOATS, I32, I64, INDEX, SIZE, VOID, Function, call, dtype_code, need, on_device, result, scratch
+from ._args import FLOATS, I32, I64, INDEX, SIZE, VOID, Function, call, dtype_code, need, on_device, on_stream, result, scratch
 
 MAX_EXPERTS = 1024  # EXL3_MOE_MAX_EXPERTS
 _IDS = {torch.int32: 4, torch.int64: 8}
@@ -36,6 +36,8 @@ def moe_sort(expert_ids, n_experts: int, order=None, position=None, offsets=None
     workspace: a uint8 device tensor of exl3_moe_workspace_bytes; by default new
     scratch where that is not 0.
     """
+    if stream is not None:
+        return on_stream(stream, moe_sort, expert_ids, n_experts, order, position, offsets, workspace)
     if not isinstance(expert_ids, torch.Tensor) or expert_ids.dim() != 2:
         raise Exl3Error("expert_ids: expected a torch tensor [tokens, top_k]")
     shape, slots = expert_ids.shape, expert_ids.numel()
@@ -48,8 +50,8 @@ def moe_sort(expert_ids, n_experts: int, order=None, position=None, offsets=None
     dev = expert_ids.get_device()
     if not dev == order.get_device() == position.get_device() == offsets.get_device() >= 0:
         on_device(dev, expert_ids=expert_ids, order=order, position=position, offsets=offsets)
-    ws, nbytes, held = scratch(workspace, 0 if workspace is not None else (_bytes.bound or _bytes.load())(slots, n_experts), expert_ids, stream)
-    call(_sort, dev, stream, ids, _IDS[expert_ids.dtype], slots, n_experts, o, p, f, ws, nbytes)
+    ws, nbytes, held = scratch(workspace, 0 if workspace is not None else (_bytes.bound or _bytes.load())(slots, n_experts), expert_ids)
+    call(_sort, dev, ids, _IDS[expert_ids.dtype], slots, n_experts, o, p, f, ws, nbytes)
     return order, position, offsets
 
 
@@ -71,6 +73,8 @@ def _width(t, name: str) -> int:
 
 def moe_gather(x, position, offsets, rows=None, stream=None):
     """rows[position[t, j]] = x[t]; the rows of dropped slots are zero."""
+    if stream is not None:
+        return on_stream(stream, moe_gather, x, position, offsets, rows)
     tokens, top_k, at, kept = _places(position, offsets)
     n, code = _width(x, "x"), dtype_code(x, "x")
     src = need(x, "x", FLOATS, (tokens, n))
@@ -78,12 +82,14 @@ def moe_gather(x, position, offsets, rows=None, stream=None):
     dev = x.get_device()
     if not dev == position.get_device() == offsets.get_device() == rows.get_device() >= 0:
         on_device(dev, x=x, position=position, offsets=offsets, rows=rows)
-    call(_gather, dev, stream, src, code, tokens, top_k, n, at, kept, dst)
+    call(_gather, dev, src, code, tokens, top_k, n, at, kept, dst)
     return rows
 
 
 def moe_combine(rows, position, offsets, weights=None, y=None, stream=None):
     """y[t] = sum over j of weights[t, j] * rows[position[t, j]] (no weights: ones)."""
+    if stream is not None:
+        return on_stream(stream, moe_combine, rows, position, offsets, weights, y)
     tokens, top_k, at, kept = _places(position, offsets)
     n, code = _width(rows, "rows"), dtype_code(rows, "rows")
     src = need(rows, "rows", FLOATS, (tokens * top_k, n))
@@ -93,7 +99,7 @@ def moe_combine(rows, position, offsets, weights=None, y=None, stream=None):
     if not (dev == position.get_device() == offsets.get_device() == y.get_device() >= 0
             and (w is None or weights.get_device() == dev)):
         on_device(dev, rows=rows, position=position, offsets=offsets, weights=weights, y=y)
-    call(_combine, dev, stream, src, code, tokens, top_k, n, at, kept, w, 0 if w is None else FLOATS[weights.dtype], dst)
+    call(_combine, dev, src, code, tokens, top_k, n, at, kept, w, 0 if w is None else FLOATS[weights.dtype], dst)
     return y
 
 
@@ -104,6 +110,8 @@ def moe_gather_backward(drows, position, offsets, dx=None, stream=None):
 
 def moe_combine_backward(dy, rows, position, offsets, weights, drows=None, dweights=None, stream=None):
     """The gradients of moe_combine: (drows, dweights)."""
+    if stream is not None:
+        return on_stream(stream, moe_combine_backward, dy, rows, position, offsets, weights, drows, dweights)
     tokens, top_k, at, kept = _places(position, offsets)
     n, code = _width(rows, "rows"), dtype_code(rows, "rows")
     src, grad = need(rows, "rows", FLOATS, (tokens * top_k, n)), need(dy, "dy", (rows.dtype,), (tokens, n))
@@ -114,5 +122,5 @@ def moe_combine_backward(dy, rows, position, offsets, weights, drows=None, dweig
     if not (dev == dy.get_device() == position.get_device() == offsets.get_device() == weights.get_device() == drows.get_device()
             == dweights.get_device() >= 0):
         on_device(dev, rows=rows, dy=dy, position=position, offsets=offsets, weights=weights, drows=drows, dweights=dweights)
-    call(_backward, dev, stream, grad, src, code, tokens, top_k, n, at, kept, w, FLOATS[weights.dtype], dst, dw)
+    call(_backward, dev, grad, src, code, tokens, top_k, n, at, kept, w, FLOATS[weights.dtype], dst, dw)
     return drows, dweights

@@ -16,7 +16,7 @@ import torch
 
 from . import Exl3Error, _check
 from ._args import (BYTES, I32, I64, INDEX, SIZE, VOID, Function, call, dtype_code, need, need_rows, on_device,
-                    result, scratch)
+                    on_stream, result, scratch)
 
 BLOCK = 32  # EXL3_MXFP4_BLOCK
 
@@ -35,6 +35,8 @@ def _blocks(n: int, name: str) -> int:
 
 def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     """x [rows, n] to (codes [rows, n / 2], scales [rows, n / 32])."""
+    if stream is not None:
+        return on_stream(stream, mxfp4_quantize, x, codes, scales)
     rows, n, ld, code, at = need_rows(x, "x")
     blocks = _blocks(n, "x")
     codes, c = result(codes, "codes", x, torch.uint8, (rows, n // 2))
@@ -42,12 +44,14 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     dev = x.get_device()
     if not dev == codes.get_device() == scales.get_device() >= 0:
         on_device(dev, x=x, codes=codes, scales=scales)
-    call(_quantize, dev, stream, at, code, rows, n, ld, c, s)
+    call(_quantize, dev, at, code, rows, n, ld, c, s)
     return codes, scales
 
 
 def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
     """The values of codes [rows, n / 2] and scales [rows, n / 32], as dtype [rows, n]."""
+    if stream is not None:
+        return on_stream(stream, mxfp4_dequantize, codes, scales, dtype, out)
     code = dtype_code(dtype, "dtype")
     if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
         raise Exl3Error("codes: expected a torch tensor of two dimensions")
@@ -58,7 +62,7 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None)
     dev = codes.get_device()
     if not dev == scales.get_device() == out.get_device() >= 0:
         on_device(dev, codes=codes, scales=scales, out=out)
-    call(_dequantize, dev, stream, c, s, rows, n, o, code)
+    call(_dequantize, dev, c, s, rows, n, o, code)
     return out
 
 
@@ -86,6 +90,8 @@ def _weight(codes, scales, offsets, n_in: int, blocks: int):
 def mxfp4_matmul(x_codes, x_scales, codes, scales, dtype=torch.bfloat16, offsets=None, y=None, stream=None):
     """y [m, n_out] = X @ W^T for quantised rows X (x_codes [m, n_in / 2], x_scales
     [m, n_in / 32]): several projections of one input quantise it once."""
+    if stream is not None:
+        return on_stream(stream, mxfp4_matmul, x_codes, x_scales, codes, scales, dtype, offsets, y)
     code = dtype_code(dtype, "dtype")
     if not isinstance(x_codes, torch.Tensor) or x_codes.dim() != 2:
         raise Exl3Error("x_codes: expected a torch tensor of two dimensions")
@@ -98,7 +104,7 @@ def mxfp4_matmul(x_codes, x_scales, codes, scales, dtype=torch.bfloat16, offsets
     if not (dev == x_scales.get_device() == codes.get_device() == scales.get_device() == y.get_device() >= 0
             and (at is None or offsets.get_device() == dev)):
         on_device(dev, x_codes=x_codes, x_scales=x_scales, codes=codes, scales=scales, offsets=offsets, y=y)
-    call(_matmul, dev, stream, xc, xs, m, at, groups, c, s, n_in, n_out, o, code)
+    call(_matmul, dev, xc, xs, m, at, groups, c, s, n_in, n_out, o, code)
     return y
 
 
@@ -108,6 +114,8 @@ def mxfp4_linear(x, codes, scales, offsets=None, workspace=None, y=None, stream=
     workspace: a uint8 device tensor of mxfp4_workspace_bytes(m, n_in, groups); by
     default new scratch where that is not 0.
     """
+    if stream is not None:
+        return on_stream(stream, mxfp4_linear, x, codes, scales, offsets, workspace, y)
     m, n_in, ld, code, src = need_rows(x, "x")
     c, s, at, groups, n_out = _weight(codes, scales, offsets, n_in, _blocks(n_in, "x"))
     y, o = result(y, "y", x, x.dtype, (m, n_out))
@@ -115,6 +123,6 @@ def mxfp4_linear(x, codes, scales, offsets=None, workspace=None, y=None, stream=
     if not (dev == codes.get_device() == scales.get_device() == y.get_device() >= 0
             and (at is None or offsets.get_device() == dev)):
         on_device(dev, x=x, codes=codes, scales=scales, offsets=offsets, y=y)
-    ws, nbytes, held = scratch(workspace, 0 if workspace is not None else mxfp4_workspace_bytes(m, n_in, groups), x, stream)
-    call(_linear, dev, stream, src, code, m, ld, at, groups, c, s, n_in, n_out, o, ws, nbytes)
+    ws, nbytes, held = scratch(workspace, 0 if workspace is not None else mxfp4_workspace_bytes(m, n_in, groups), x)
+    call(_linear, dev, src, code, m, ld, at, groups, c, s, n_in, n_out, o, ws, nbytes)
     return y

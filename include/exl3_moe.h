@@ -18,7 +18,11 @@
  * where a call writes them and are not read otherwise.
  *
  * Conventions: as in exl3.h and exl3_mxfp4.h (dtype is exl3_dtype).  position
- * entries outside 0 .. slots - 1 are treated as dropped.  Sums are fp32, in the
+ * entries outside 0 .. slots - 1 are treated as dropped; an entry that comes
+ * twice gives its row to one of the two.  EXL3_EINVAL for null or misaligned
+ * pointers (kept: 4 bytes), bad types and sizes below 1 (no tokens or slots are a
+ * no-op); EXL3_EUNSUPPORTED for 2^24 tokens, 2^26 - 4 slots (sort: more than
+ * 2^30) or n > 2^24.  Sums are fp32, in the
  * order of j, rounded once; results do not depend on timing.
  */
 #ifndef EXL3_MOE_H

@@ -48,7 +48,8 @@ enum exl3_dtype {
  *   codes  : uint8 [rows][n / 2], overwritten
  *   scales : uint8 [rows][n / 32], overwritten
  * rows == 0 is a no-op.  EXL3_EINVAL for a null or misaligned pointer, a bad
- * dtype, n < 32 or n % 32 != 0, rows < 0 or a bad ldx.
+ * dtype, n < 32 or n % 32 != 0, rows < 0 or a bad ldx; EXL3_EUNSUPPORTED for
+ * more than 2^37 values.
  */
 int exl3_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int32_t n, int64_t ldx, uint8_t* codes,
                         uint8_t* scales, void* stream);
@@ -86,7 +87,7 @@ int64_t exl3_mxfp4_workspace_bytes(int32_t rows, int32_t n_groups, int32_t n_in)
  * rows == 0 is a no-op.  EXL3_EINVAL for a null or misaligned pointer, a bad
  * dtype, n_in < 32 or n_in % 32 != 0, n_out < 1, rows < 0, n_groups < 1, more
  * than one group without offsets; EXL3_EUNSUPPORTED for n_in > 2^20,
- * n_groups > 4096, rows > 2^23, n_out > 2^24.
+ * n_groups > 4096, rows > 2^23, n_out > 2^24, or about 2^36 outputs and more.
  */
 int exl3_mxfp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, int32_t rows, const int32_t* offsets,
                       int32_t n_groups, const uint8_t* codes, const uint8_t* scales, int32_t n_in, int32_t n_out,

@@ -195,6 +195,11 @@ def test_groups(ex, counts, behind, dtype):
     check_groups(ex, counts, behind, 352, 80, dtype)
 
 
+@pytest.mark.parametrize("n_in, n_out", [(160, 2500), (160, 10000), (256, 10001)])
+def test_large_groups(ex, n_in, n_out):
+    check_groups(ex, [700, 0, 900, 450], 30, n_in, n_out, "bf16")
+
+
 def test_many_groups(ex):
     rng = np.random.default_rng(7)
     check_groups(ex, [int(c) for c in rng.integers(0, 4, 150)], 9, 64, 33, "bf16")
@@ -207,6 +212,14 @@ def test_many_groups(ex):
 @pytest.mark.parametrize("m", [1, 2, 4, 5, 8])
 def test_few_rows_of_every_length(ex, m, n_in):
     check_linear(ex, m, n_in, 40, ("fp16", "bf16", "fp32")[(m + n_in // 32) % 3], pad=16)
+
+
+# the tile sizes: 128 x 128 and 256 x 256, every number of stages of 256 inputs from 1 to 5, and rows of scales that start at any byte
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n_in", [96, 256, 288, 640, 1024, 1056])
+@pytest.mark.parametrize("m, n_out", [(1100, 2100), (2050, 6001)])
+def test_linear_large_tiles(ex, m, n_in, n_out, dtype):
+    check_linear(ex, m, n_in, n_out, dtype)
 
 
 @pytest.mark.parametrize("m, n_in, n_out", [(70, 4096, 700), (200, 2048, 3000), (200, 2080, 3000), (600, 1056, 2000), (1500, 512, 1500)])

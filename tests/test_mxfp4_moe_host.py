@@ -76,7 +76,7 @@ def test_quantize_argument_errors(lib):
     assert q(x=None) == -1 and q(codes=None) == -1 and q(scales=None) == -1
     assert q(x=A + 8) == -1 and q(codes=A + 4) == -1 and q(scales=A + 1) == -1
     assert q(rows=0, x=None, codes=None, scales=None) == 0
-    assert q(rows=1 << 41) == -2
+    assert q(rows=1 << 41) == -2 and q(rows=1 << 32) == -2
 
     def d(codes=A, scales=2 * A, rows=4, n=64, out=3 * A, dtype=F16):
         return lib.exl3_mxfp4_dequantize(codes, scales, rows, n, out, dtype, None)
@@ -98,6 +98,7 @@ def test_product_argument_errors(lib):
         assert g(c=None) == -1 and g(s=None) == -1 and g(y=None) == -1
         assert g(c=A + 8) == -1 and g(s=A + 8) == -1 and g(y=A + 8) == -1 and g(at=A + 2) == -1
         assert g(groups=4097, at=7 * A) == -2 and g(rows=(1 << 23) + 1) == -2 and g(n_out=(1 << 24) + 1) == -2
+        assert g(rows=1 << 23, n_out=1 << 14) == -2                      # 2^37 outputs
         assert g(rows=0, c=None, s=None, y=None) == 0
     assert m(n_in=(1 << 20) + 32) == -2 and f(n_in=(1 << 20) + 32, ld=(1 << 20) + 32) == -2
     assert m(xc=None) == -1 and m(xs=None) == -1 and m(xc=A + 1) == -1 and m(xs=A + 1) == -1 and m(xc=5 * A) == -1
@@ -129,7 +130,7 @@ def test_moe_argument_errors(lib):
         assert f(dtype=3) == -1 and f(tokens=-1) == -1 and f(k=0) == -1 and f(n=0) == -1
         assert f(x=None) == -1 and f(pos=None) == -1 and f(kept=None) == -1 and f(rows=None) == -1 and f(rows=A) == -1
         assert f(x=A + 8) == -1 and f(pos=A + 8) == -1 and f(kept=A + 2) == -1 and f(rows=A + 8) == -1
-        assert f(tokens=1 << 30, k=2) == -2 and f(n=(1 << 24) + 1) == -2
+        assert f(tokens=1 << 24) == -2 and f(tokens=1 << 20, k=64) == -2 and f(n=(1 << 24) + 1) == -2
         assert f(tokens=0, x=None) == 0
     for f in (c, b):
         assert f(wd=4) == -1 and f(w=A + 8) == -1
