@@ -15,10 +15,12 @@ Tensors:
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import Exl3Error
-from ._args import FLOATS, I32, I64, INDEX, SIZE, VOID, Function, call, dtype_code, need, on_device, on_stream, result, scratch
+from ._args import FLOATS, I32, I64, INDEX, SIZE, VOID, Function, call, need, on_device, on_stream, result, scratch
 
 MAX_EXPERTS = 1024  # EXL3_MOE_MAX_EXPERTS
 _IDS = {torch.int32: 4, torch.int64: 8}
@@ -28,6 +30,11 @@ _sort = Function("exl3_moe_sort", VOID, I32, I32, I32, VOID, VOID, VOID, VOID, S
 _gather = Function("exl3_moe_gather", VOID, I32, I32, I32, I32, VOID, VOID, VOID, VOID)
 _combine = Function("exl3_moe_combine", VOID, I32, I32, I32, I32, VOID, VOID, VOID, I32, VOID, VOID)
 _backward = Function("exl3_moe_combine_backward", VOID, VOID, I32, I32, I32, I32, VOID, VOID, VOID, I32, VOID, VOID, VOID)
+
+
+@functools.lru_cache(maxsize=1024)  # a size, of sizes alone
+def _workspace_bytes(slots: int, n_experts: int) -> int:
+    return (_bytes.bound or _bytes.load())(slots, n_experts)
 
 
 def moe_sort(expert_ids, n_experts: int, order=None, position=None, offsets=None, workspace=None, stream=None):
@@ -50,7 +57,7 @@ def moe_sort(expert_ids, n_experts: int, order=None, position=None, offsets=None
     dev = expert_ids.get_device()
     if not dev == order.get_device() == position.get_device() == offsets.get_device() >= 0:
         on_device(dev, expert_ids=expert_ids, order=order, position=position, offsets=offsets)
-    ws, nbytes, held = scratch(workspace, 0 if workspace is not None else (_bytes.bound or _bytes.load())(slots, n_experts), expert_ids)
+    ws, nbytes, held = scratch(workspace, 0 if workspace is not None else _workspace_bytes(slots, n_experts), expert_ids)
     call(_sort, dev, ids, _IDS[expert_ids.dtype], slots, n_experts, o, p, f, ws, nbytes)
     return order, position, offsets
 
@@ -61,14 +68,21 @@ def _places(position, offsets):
         raise Exl3Error("position: expected a torch tensor [tokens, top_k]")
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
         raise Exl3Error("offsets: expected a torch tensor [n_experts + 1]")
-    at, kept = need(position, "position", INDEX, position.shape), need(offsets, "offsets", INDEX, offsets.shape)
-    return (*position.shape, at, kept + 4 * (offsets.shape[0] - 1))
+    tokens, top_k = position.shape
+    at, kept = position.data_ptr(), offsets.data_ptr()
+    if not (position.dtype is offsets.dtype is torch.int32 and position.is_contiguous() and offsets.is_contiguous()) or (at | kept) & 15:
+        need(position, "position", INDEX, position.shape)
+        need(offsets, "offsets", INDEX, offsets.shape)
+    return tokens, top_k, at, kept + 4 * (offsets.shape[0] - 1)
 
 
-def _width(t, name: str) -> int:
+def _matrix(t, name: str, rows: int):
+    """A floating tensor of `rows` rows: columns, exl3_dtype and address."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[1] < 1:
         raise Exl3Error(f"{name}: expected a torch tensor of two dimensions")
-    return t.shape[1]
+    n = t.shape[1]
+    at = need(t, name, FLOATS, (rows, n))
+    return n, FLOATS[t.dtype], at
 
 
 def moe_gather(x, position, offsets, rows=None, stream=None):
@@ -76,8 +90,7 @@ def moe_gather(x, position, offsets, rows=None, stream=None):
     if stream is not None:
         return on_stream(stream, moe_gather, x, position, offsets, rows)
     tokens, top_k, at, kept = _places(position, offsets)
-    n, code = _width(x, "x"), dtype_code(x, "x")
-    src = need(x, "x", FLOATS, (tokens, n))
+    n, code, src = _matrix(x, "x", tokens)
     rows, dst = result(rows, "rows", x, x.dtype, (tokens * top_k, n))
     dev = x.get_device()
     if not dev == position.get_device() == offsets.get_device() == rows.get_device() >= 0:
@@ -91,8 +104,7 @@ def moe_combine(rows, position, offsets, weights=None, y=None, stream=None):
     if stream is not None:
         return on_stream(stream, moe_combine, rows, position, offsets, weights, y)
     tokens, top_k, at, kept = _places(position, offsets)
-    n, code = _width(rows, "rows"), dtype_code(rows, "rows")
-    src = need(rows, "rows", FLOATS, (tokens * top_k, n))
+    n, code, src = _matrix(rows, "rows", tokens * top_k)
     w = None if weights is None else need(weights, "weights", FLOATS, (tokens, top_k))
     y, dst = result(y, "y", rows, rows.dtype, (tokens, n))
     dev = rows.get_device()
@@ -113,8 +125,8 @@ def moe_combine_backward(dy, rows, position, offsets, weights, drows=None, dweig
     if stream is not None:
         return on_stream(stream, moe_combine_backward, dy, rows, position, offsets, weights, drows, dweights)
     tokens, top_k, at, kept = _places(position, offsets)
-    n, code = _width(rows, "rows"), dtype_code(rows, "rows")
-    src, grad = need(rows, "rows", FLOATS, (tokens * top_k, n)), need(dy, "dy", (rows.dtype,), (tokens, n))
+    n, code, src = _matrix(rows, "rows", tokens * top_k)
+    grad = need(dy, "dy", (rows.dtype,), (tokens, n))
     w = need(weights, "weights", FLOATS, (tokens, top_k))
     drows, dst = result(drows, "drows", rows, rows.dtype, (tokens * top_k, n))
     dweights, dw = result(dweights, "dweights", weights, weights.dtype, (tokens, top_k))
