@@ -126,6 +126,7 @@ struct ProductParams {
     const uint8_t* ws;
     int n_in, n_out;
     void* y;
+    int ldy;  // outputs from a row of y to the next: n_out, or more where this launch makes some of the columns
 };
 
 // Memory from `base` on, read at 32-bit offsets.
@@ -347,7 +348,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductPa
         f32x4_t v = acc;
         for (int w = 1; w < split; ++w) v += __builtin_bit_cast(f32x4_t, ring[w * SMALL_RING * BUF + lane]);
         const int o = n0 + 4 * q;
-        if (r < t.rows && o < p.n_out) store4<OT>(p.y, (int64_t)(t.row0 + r) * p.n_out + o, p.n_out - o, (p.n_out & 3) == 0, v);
+        if (r < t.rows && o < p.n_out) store4<OT>(p.y, (int64_t)(t.row0 + r) * p.ldy + o, p.n_out - o, (p.ldy & 3) == 0, v);
     }
 }
 
@@ -385,7 +386,7 @@ __device__ inline void store_tile(const f32x16_t (&acc)[RT][CT], char* part, con
     constexpr int PITCH = 32 * CT * OT::bytes + 16;
     const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
     const int cols = min(32 * CT, p.n_out - col0);
-    const bool vec = ((int64_t)p.n_out * OT::bytes) % 16 == 0;
+    const bool vec = ((int64_t)p.ldy * OT::bytes) % 16 == 0 && p.n_out % (16 / OT::bytes) == 0;
     raw* y = static_cast<raw*>(p.y);
 #pragma unroll
     for (int m = 0; m < RT; ++m) {
@@ -398,20 +399,20 @@ __device__ inline void store_tile(const f32x16_t (&acc)[RT][CT], char* part, con
                 store4<OT>(part + r * PITCH, 32 * c + 8 * g + 4 * h, 4, true, v);
             }
         __builtin_amdgcn_wave_barrier();
-        const int64_t y0 = (int64_t)(row0 + 32 * m) * p.n_out + col0;
+        const int64_t y0 = (int64_t)(row0 + 32 * m) * p.ldy + col0;
         if (vec) {
             constexpr int PER = 16 / OT::bytes, LANES = 32 * CT / PER;  // outputs of a lane, lanes of a row
 #pragma unroll
             for (int i = 0; i < 32; i += 64 / LANES) {
                 const int row = i + lane / LANES, o = lane % LANES * PER;
                 const i32x4_t v = *reinterpret_cast<const i32x4_t*>(part + row * PITCH + o * OT::bytes);
-                if (row < live && o < cols) *reinterpret_cast<i32x4_t*>(y + y0 + (int64_t)row * p.n_out + o) = v;
+                if (row < live && o < cols) *reinterpret_cast<i32x4_t*>(y + y0 + (int64_t)row * p.ldy + o) = v;
             }
         } else {
             for (int i = lane; i < live * 32 * CT; i += 64) {
                 const int row = i / (32 * CT), o = i % (32 * CT);
                 const raw v = reinterpret_cast<const raw*>(part + row * PITCH)[o];
-                if (o < cols) y[y0 + (int64_t)row * p.n_out + o] = v;
+                if (o < cols) y[y0 + (int64_t)row * p.ldy + o] = v;
             }
         }
         __builtin_amdgcn_wave_barrier();
@@ -796,6 +797,12 @@ inline int64_t expected_tiles(const ProductParams& p, int high) {
     return p.rows / high + (p.n_groups < p.rows ? p.n_groups : p.rows) / 2 + 1;
 }
 
+// Rounds of 128 x 128 tiles, two workgroups a CU; at least one.
+inline double rounds128(const ProductParams& p) {
+    const double rounds = (double)(expected_tiles(p, 128) * ((p.n_out + 127) / 128)) / 512;
+    return rounds > 1 ? rounds : 1;
+}
+
 template <typename OT> hipError_t launch_product(const ProductParams& p, hipStream_t s) {
     if (p.x) return launch_small<OT, true>(p, s);
     constexpr int64_t CUS = 256;
@@ -819,9 +826,26 @@ template <typename OT> hipError_t launch_product(const ProductParams& p, hipStre
     // 2048 rows 8192 -> 28672 386 against 315 (7 : 4), 2048 rows in 64 groups 2048 ->
     // 2816 46.5 against 67.5 (2.1 : 2), 1024 rows in 8 groups 4096 -> 14336 100
     // against 85 (2.8 : 2).
-    const double low = (double)(expected_tiles(p, 128) * ((p.n_out + 127) / 128)) / (2 * CUS);
-    const int64_t high = (expected_tiles(p, 256) * ((p.n_out + 255) / 256) + CUS - 1) / CUS;
-    return 0.72 * (low > 1 ? low : 1) < (double)high ? launch_gemm<OT, 2, 2>(p, s) : launch_gemm<OT, 4, 4>(p, s);
+    const double low = 0.72 * rounds128(p);
+    const int64_t row_tiles = expected_tiles(p, 256), tiles = row_tiles * ((p.n_out + 255) / 256), high = (tiles + CUS - 1) / CUS;
+    // Whole rounds of large tiles, and small ones for the columns left over: 2048
+    // rows 8192 -> 28672 (3 + 0.72 rounds against 4) 261 us against 270, 8192 ->
+    // 10240 (1.72 : 2) 101 against 112.
+    const int64_t whole = tiles / CUS, cols = row_tiles > 0 ? whole * CUS / row_tiles * 256 : 0;
+    if (!p.offsets && cols > 0 && cols < p.n_out) {
+        ProductParams left = p, right = p;
+        left.n_out = (int)cols;
+        right.n_out = (int)(p.n_out - cols);
+        right.wc += cols * (p.n_in / 2);
+        right.ws += cols * (p.n_in / BLOCK);
+        right.y = static_cast<char*>(p.y) + cols * OT::bytes;
+        const double both = (double)whole + 0.72 * rounds128(right) + 0.05;
+        if (both < low && both < (double)high) {
+            const hipError_t e = launch_gemm<OT, 4, 4>(left, s);
+            return e == hipSuccess ? launch_gemm<OT, 2, 2>(right, s) : e;
+        }
+    }
+    return low < (double)high ? launch_gemm<OT, 2, 2>(p, s) : launch_gemm<OT, 4, 4>(p, s);
 }
 
 hipError_t product(int dtype, const ProductParams& p, hipStream_t s) {
@@ -912,7 +936,7 @@ int exl3_mxfp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, int32_t r
     if (rc <= 0) return rc;
     if (!x_codes || !x_scales || misaligned(x_codes) || misaligned(x_scales) || y == x_codes || y == x_scales)
         return EXL3_EINVAL;
-    const ProductParams p = {nullptr, 0, x_codes, x_scales, offsets, n_groups, rows, codes, scales, n_in, n_out, y};
+    const ProductParams p = {nullptr, 0, x_codes, x_scales, offsets, n_groups, rows, codes, scales, n_in, n_out, y, n_out};
     return product(dtype, p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_EHIP;
 }
 
@@ -926,7 +950,7 @@ int exl3_mxfp4_linear(const void* x, int32_t dtype, int32_t rows, int64_t ldx, c
     if (!x || misaligned(x) || misaligned(workspace) || x == y) return EXL3_EINVAL;
     const int64_t need = exl3_mxfp4_workspace_bytes(rows, n_groups, n_in);
     if (need > 0 && (!workspace || (int64_t)workspace_bytes < need)) return EXL3_EWORKSPACE;
-    ProductParams p = {x, ldx, nullptr, nullptr, offsets, n_groups, rows, codes, scales, n_in, n_out, y};
+    ProductParams p = {x, ldx, nullptr, nullptr, offsets, n_groups, rows, codes, scales, n_in, n_out, y, n_out};
     if (need > 0) {
         uint8_t* xc = static_cast<uint8_t*>(workspace);
         uint8_t* xs = xc + codes_bytes(rows, n_in);

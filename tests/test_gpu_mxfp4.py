@@ -222,6 +222,11 @@ def test_linear_large_tiles(ex, m, n_in, n_out, dtype):
     check_linear(ex, m, n_in, n_out, dtype)
 
 
+@pytest.mark.parametrize("n_in, n_out, dtype", [(288, 10200, "bf16"), (544, 10203, "fp32"), (256, 10201, "fp16")])
+def test_linear_of_both_large_tiles(ex, n_in, n_out, dtype):
+    check_linear(ex, 2040, n_in, n_out, dtype)
+
+
 @pytest.mark.parametrize("m, n_in, n_out", [(70, 4096, 700), (200, 2048, 3000), (200, 2080, 3000), (600, 1056, 2000), (1500, 512, 1500)])
 def test_linear_of_many_tiles(ex, m, n_in, n_out):
     check_linear(ex, m, n_in, n_out, "bf16")
