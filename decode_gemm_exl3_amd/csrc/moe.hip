@@ -117,6 +117,7 @@ __global__ __launch_bounds__(SORT_THREADS) void place_kernel(const SortParams p)
     while ((1 << bits) < bins) ++bits;
     const int64_t begin = (int64_t)blockIdx.x * p.chunk, end = min((int64_t)p.slots, begin + p.chunk);
     for (int64_t i0 = begin; i0 < end; i0 += SORT_THREADS) {
+        __syncthreads();  // the round before has read in_wave and moved next on
         for (int k = threadIdx.x; k < SORT_WAVES * bins; k += SORT_THREADS) in_wave[k / bins][k % bins] = 0;
         __syncthreads();
         const int64_t i = i0 + threadIdx.x;
@@ -143,7 +144,6 @@ __global__ __launch_bounds__(SORT_THREADS) void place_kernel(const SortParams p)
             for (int w = 0; w < SORT_WAVES; ++w) n += in_wave[w][k];
             next[k] += n;
         }
-        // the next round's first barrier orders these writes before their use
     }
 }
 
