@@ -667,17 +667,21 @@ __global__ __launch_bounds__(256, RT * CT > 4 ? 1 : 2) void gemm_kernel(const Pr
             if (k < CT) wsn[k] = scales(BM + (wx * CT + k) * 32 + r, wshift[k], st, par);
             else xsn[k - CT] = scales((wy * RT + k - CT) * 32 + r, xshift[k - CT], st, par);
         };
+        // both buffers are asked for before the first is waited for
 #pragma unroll
         for (int k = 0; k < 2 * CODES; ++k) ask_codes(k, 0, 0);
 #pragma unroll
         for (int k = 0; k < SCALE_LOADS; ++k) ask_scales(k, so[k], 0);
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int k = 0; k < CODES; ++k) ask_codes(k, min(1, last), 1);
+        for (int k = 0; k < 2 * CODES; ++k) ask_codes(k, min(1, last), 1);
 #pragma unroll
         for (int k = 0; k < EACH; ++k) ask_scales(k, so[k], 1);
+        constexpr int YOUNGER = 2 * CODES + EACH;
+        static_assert(YOUNGER < 64, "a wait counts to 63");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (YOUNGER & 15) | ((YOUNGER >> 4) << 14));  // vmcnt(YOUNGER)
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int k = 0; k < READS; ++k) {
             read_operand(k, 0, 0, 0);
@@ -708,7 +712,7 @@ __global__ __launch_bounds__(256, RT * CT > 4 ? 1 : 2) void gemm_kernel(const Pr
 #pragma unroll
                         for (int k = i * CODES / MFMAS; k < (i + 1) * CODES / MFMAS; ++k) {
                             if (j == 3) ask_codes(k, min(st + 2, last), par);
-                            else ask_codes(CODES + k, min(st + 1, last), par ^ 1);
+                            else if (st > 0) ask_codes(CODES + k, min(st + 1, last), par ^ 1);
                         }
                     }
                     if constexpr (j == 3) {
