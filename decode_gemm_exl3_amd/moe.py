@@ -64,25 +64,25 @@ def moe_sort(expert_ids, n_experts: int, order=None, position=None, offsets=None
 
 def _places(position, offsets):
     """Tokens, top_k, the address of position and that of the number of kept slots."""
-    if not isinstance(position, torch.Tensor) or position.dim() != 2 or position.shape[1] < 1:
+    if not isinstance(position, torch.Tensor) or len(shape := position.shape) != 2 or shape[1] < 1:
         raise Exl3Error("position: expected a torch tensor [tokens, top_k]")
-    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+    if not isinstance(offsets, torch.Tensor) or len(ends := offsets.shape) != 1 or ends[0] < 2:
         raise Exl3Error("offsets: expected a torch tensor [n_experts + 1]")
-    tokens, top_k = position.shape
     at, kept = position.data_ptr(), offsets.data_ptr()
     if not (position.dtype is offsets.dtype is torch.int32 and position.is_contiguous() and offsets.is_contiguous()) or (at | kept) & 15:
-        need(position, "position", INDEX, position.shape)
-        need(offsets, "offsets", INDEX, offsets.shape)
-    return tokens, top_k, at, kept + 4 * (offsets.shape[0] - 1)
+        need(position, "position", INDEX, shape)
+        need(offsets, "offsets", INDEX, ends)
+    return shape[0], shape[1], at, kept + 4 * (ends[0] - 1)
 
 
 def _matrix(t, name: str, rows: int):
     """A floating tensor of `rows` rows: columns, exl3_dtype and address."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[1] < 1:
+    if not isinstance(t, torch.Tensor) or len(shape := t.shape) != 2 or shape[1] < 1:
         raise Exl3Error(f"{name}: expected a torch tensor of two dimensions")
-    n = t.shape[1]
-    at = need(t, name, FLOATS, (rows, n))
-    return n, FLOATS[t.dtype], at
+    n, code, at = shape[1], FLOATS.get(t.dtype), t.data_ptr()
+    if code is None or shape[0] != rows or not t.is_contiguous() or at & 15:
+        need(t, name, FLOATS, (rows, n))
+    return n, code, at
 
 
 def moe_gather(x, position, offsets, rows=None, stream=None):
