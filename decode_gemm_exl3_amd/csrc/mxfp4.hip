@@ -583,7 +583,7 @@ __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int 
 // matrix cores are busy 53 % of the cycles at 1.57 GHz, and zeros instead of random codes
 // run 20 to 30 % faster.  128 x 128 tiles (two a CU): the address unit (64 bytes a
 // cycle) and the first touch of each line; 16384 rows in 64 groups 2048 -> 2816 in
-// 107 to 125 us, waiting for data half of the time.
+// 107 to 125 us, waiting for data half of the time (131 without a pause between calls).
 
 constexpr int STAGE_BLOCKS = 8;
 
