@@ -44,6 +44,11 @@ def dtype_code(t, name: str) -> int:
     return code
 
 
+def too_large(name: str, shape):
+    """The library takes its sizes as 32-bit numbers, and ctypes would cut longer ones."""
+    raise Exl3Error(f"{name}: shape {tuple(shape)}, sizes must be below 2^31")
+
+
 def need(t, name: str, dtypes, shape) -> int:
     """Checks all but the device; returns the address."""
     if not isinstance(t, torch.Tensor):
@@ -76,6 +81,8 @@ def need_rows(t, name: str):
     if t.dim() != 2:
         raise Exl3Error(f"{name}: expected two dimensions, got shape {tuple(t.shape)}")
     rows, n = t.shape
+    if n >> 31:
+        too_large(name, t.shape)
     ld, inner = t.stride()
     if rows <= 1:
         ld = n

@@ -20,7 +20,7 @@ import functools
 import torch
 
 from . import Exl3Error
-from ._args import FLOATS, I32, I64, INDEX, SIZE, VOID, Function, call, need, on_device, on_stream, result, scratch
+from ._args import FLOATS, I32, I64, INDEX, SIZE, VOID, Function, call, need, on_device, on_stream, result, scratch, too_large
 
 MAX_EXPERTS = 1024  # EXL3_MOE_MAX_EXPERTS
 _IDS = {torch.int32: 4, torch.int64: 8}
@@ -48,6 +48,8 @@ def moe_sort(expert_ids, n_experts: int, order=None, position=None, offsets=None
     if not isinstance(expert_ids, torch.Tensor) or expert_ids.dim() != 2:
         raise Exl3Error("expert_ids: expected a torch tensor [tokens, top_k]")
     shape, slots = expert_ids.shape, expert_ids.numel()
+    if slots >> 31:
+        too_large("expert_ids", shape)
     ids = need(expert_ids, "expert_ids", _IDS, shape)
     if not 1 <= n_experts <= MAX_EXPERTS:
         raise Exl3Error(f"n_experts: {n_experts}, expected 1 to {MAX_EXPERTS}")
@@ -68,6 +70,8 @@ def _places(position, offsets):
         raise Exl3Error("position: expected a torch tensor [tokens, top_k]")
     if not isinstance(offsets, torch.Tensor) or len(ends := offsets.shape) != 1 or ends[0] < 2:
         raise Exl3Error("offsets: expected a torch tensor [n_experts + 1]")
+    if shape[0] * shape[1] >> 31:
+        too_large("position", shape)
     at, kept = position.data_ptr(), offsets.data_ptr()
     if not (position.dtype is offsets.dtype is torch.int32 and position.is_contiguous() and offsets.is_contiguous()) or (at | kept) & 15:
         need(position, "position", INDEX, shape)
@@ -80,6 +84,8 @@ def _matrix(t, name: str, rows: int):
     if not isinstance(t, torch.Tensor) or len(shape := t.shape) != 2 or shape[1] < 1:
         raise Exl3Error(f"{name}: expected a torch tensor of two dimensions")
     n, code, at = shape[1], FLOATS.get(t.dtype), t.data_ptr()
+    if n >> 31:
+        too_large(name, shape)
     if code is None or shape[0] != rows or not t.is_contiguous() or at & 15:
         need(t, name, FLOATS, (rows, n))
     return n, code, at

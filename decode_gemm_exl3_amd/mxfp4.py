@@ -16,7 +16,7 @@ import torch
 
 from . import Exl3Error, _check
 from ._args import (BYTES, I32, I64, INDEX, SIZE, VOID, Function, call, dtype_code, need, need_rows, on_device,
-                    on_stream, result, scratch)
+                    on_stream, result, scratch, too_large)
 
 BLOCK = 32  # EXL3_MXFP4_BLOCK
 
@@ -56,6 +56,8 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None)
     if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
         raise Exl3Error("codes: expected a torch tensor of two dimensions")
     rows, n = codes.shape[0], codes.shape[1] * 2
+    if n >> 31:
+        too_large("codes", codes.shape)
     blocks = _blocks(n, "codes")
     c, s = need(codes, "codes", BYTES, (rows, n // 2)), need(scales, "scales", BYTES, (rows, blocks))
     out, o = result(out, "out", codes, dtype, (rows, n))
@@ -69,6 +71,8 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None)
 @functools.lru_cache(maxsize=1024)  # a size, of sizes alone: 0.6 us of a call otherwise
 def mxfp4_workspace_bytes(rows: int, n_in: int, groups: int = 1) -> int:
     """Bytes of device scratch that mxfp4_linear needs (0: none)."""
+    if max(rows, n_in, groups) >> 31:
+        too_large("mxfp4_workspace_bytes", (rows, n_in, groups))
     n = (_bytes.bound or _bytes.load())(rows, groups, n_in)
     if n < 0:
         _check(n, "exl3_mxfp4_workspace_bytes")
@@ -79,6 +83,8 @@ def _weight(codes, scales, offsets, n_in: int, blocks: int):
     """Addresses of a weight and its offsets, with the group count and n_out."""
     if not isinstance(codes, torch.Tensor) or codes.dim() != (2 if offsets is None else 3):
         raise Exl3Error("codes: expected a torch tensor [n_out, n_in / 2], or [groups, n_out, n_in / 2] with offsets")
+    if codes.shape[-2] >> 31 or codes.shape[0] >> 31:
+        too_large("codes", codes.shape)
     if offsets is None:
         n_out = codes.shape[0]
         return need(codes, "codes", BYTES, (n_out, n_in // 2)), need(scales, "scales", BYTES, (n_out, blocks)), None, 1, n_out
@@ -96,6 +102,8 @@ def mxfp4_matmul(x_codes, x_scales, codes, scales, dtype=torch.bfloat16, offsets
     if not isinstance(x_codes, torch.Tensor) or x_codes.dim() != 2:
         raise Exl3Error("x_codes: expected a torch tensor of two dimensions")
     m, n_in = x_codes.shape[0], x_codes.shape[1] * 2
+    if (m | n_in) >> 31:
+        too_large("x_codes", x_codes.shape)
     blocks = _blocks(n_in, "x_codes")
     xc, xs = need(x_codes, "x_codes", BYTES, (m, n_in // 2)), need(x_scales, "x_scales", BYTES, (m, blocks))
     c, s, at, groups, n_out = _weight(codes, scales, offsets, n_in, blocks)
@@ -117,6 +125,8 @@ def mxfp4_linear(x, codes, scales, offsets=None, workspace=None, y=None, stream=
     if stream is not None:
         return on_stream(stream, mxfp4_linear, x, codes, scales, offsets, workspace, y)
     m, n_in, ld, code, src = need_rows(x, "x")
+    if m >> 31:
+        too_large("x", x.shape)
     c, s, at, groups, n_out = _weight(codes, scales, offsets, n_in, _blocks(n_in, "x"))
     y, o = result(y, "y", x, x.dtype, (m, n_out))
     dev = x.get_device()

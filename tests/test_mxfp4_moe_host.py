@@ -197,3 +197,34 @@ def test_moe_binding_rejects_bad_tensors():
     for f, match in bad:
         with pytest.raises(ex.Exl3Error, match=match):
             f()
+
+
+def test_binding_rejects_sizes_beyond_32_bits():
+    # ctypes cuts a size to 32 bits without an error; meta tensors stand for ones too large to allocate
+    def t(*shape, dtype=torch.uint8):
+        return torch.empty(shape, dtype=dtype, device="meta")
+    big, f16, i32 = 2 ** 32 + 32, torch.float16, torch.int32
+    ids, at = t(3, 2, dtype=i32), t(5, dtype=i32)
+    bad = [
+        lambda: ex.mxfp4_quantize(t(1, big, dtype=f16)),
+        lambda: ex.mxfp4_dequantize(t(1, big // 2), t(1, big // 32)),
+        lambda: ex.mxfp4_linear(t(big, 64, dtype=f16), t(5, 32), t(5, 2)),
+        lambda: ex.mxfp4_linear(t(3, big, dtype=f16), t(5, big // 2), t(5, big // 32)),
+        lambda: ex.mxfp4_linear(t(3, 64, dtype=f16), t(big, 32), t(big, 2)),
+        lambda: ex.mxfp4_linear(t(3, 64, dtype=f16), t(big, 5, 32), t(big, 5, 2), offsets=t(big + 1, dtype=i32)),
+        lambda: ex.mxfp4_linear(t(3, 64, dtype=f16), t(2, big, 32), t(2, big, 2), offsets=t(3, dtype=i32)),
+        lambda: ex.mxfp4_matmul(t(big, 32), t(big, 2), t(5, 32), t(5, 2)),
+        lambda: ex.mxfp4_matmul(t(3, big // 2), t(3, big // 32), t(5, big // 2), t(5, big // 32)),
+        lambda: ex.mxfp4_matmul(t(3, 32), t(3, 2), t(big, 32), t(big, 2)),
+        lambda: ex.mxfp4_workspace_bytes(big, 64),
+        lambda: ex.mxfp4_workspace_bytes(64, big),
+        lambda: ex.mxfp4_workspace_bytes(64, 64, big),
+        lambda: ex.moe_sort(t(big // 2, 2, dtype=i32), 4),
+        lambda: ex.moe_gather(t(big // 2, 1, dtype=f16), t(big // 2, 2, dtype=i32), at),
+        lambda: ex.moe_gather(t(3, big, dtype=f16), ids, at),
+        lambda: ex.moe_combine(t(6, big, dtype=f16), ids, at),
+        lambda: ex.moe_combine_backward(t(3, big, dtype=f16), t(6, big, dtype=f16), ids, at, t(3, 2, dtype=f16)),
+    ]
+    for f in bad:
+        with pytest.raises(ex.Exl3Error, match="below 2.31"):
+            f()
