@@ -365,7 +365,7 @@ int row_checks(const void* in, int32_t dtype, int32_t n_tokens, int32_t top_k, i
                const int32_t* kept, const void* out) {
     if (bad_dtype(dtype) || n_tokens < 0 || top_k < 1 || n < 1) return EXL3_EINVAL;
     if (n_tokens == 0) return EXL3_OK;
-    if (!in || !position || !kept || !out || in == out) return EXL3_EINVAL;
+    if (!in || !position || !kept || !out || out == in || out == position || out == kept) return EXL3_EINVAL;
     if (misaligned(in) || misaligned(position) || misaligned(kept, 4) || misaligned(out)) return EXL3_EINVAL;
     // a launch takes fewer than 2^32 threads: a workgroup a token, a wave a slot
     if (n_tokens >= (1 << 24) || (int64_t)n_tokens * top_k >= (1 << 26) - 4 || n > (1 << 24)) return EXL3_EUNSUPPORTED;
@@ -413,6 +413,8 @@ int exl3_moe_sort(const void* ids, int32_t id_bytes, int32_t n_slots, int32_t n_
     if (n_slots > 0 && (!ids || !order || !position || misaligned(ids) || misaligned(order) || misaligned(position)))
         return EXL3_EINVAL;
     if (misaligned(workspace)) return EXL3_EINVAL;
+    if (n_slots > 0 && (order == ids || position == ids || order == position || offsets == ids || offsets == order || offsets == position))
+        return EXL3_EINVAL;
     if (n_slots > (1 << 30)) return EXL3_EUNSUPPORTED;
     const int64_t need = exl3_moe_workspace_bytes(n_slots, n_experts);
     if (need > 0 && (!workspace || (int64_t)workspace_bytes < need)) return EXL3_EWORKSPACE;
@@ -453,7 +455,9 @@ int exl3_moe_combine_backward(const void* dy, const void* rows, int32_t dtype, i
     const int rc = row_checks(dy, dtype, n_tokens, top_k, n, position, kept, drows);
     if (rc <= 0) return rc;
     if (!rows || !weights || !dweights || misaligned(rows) || misaligned(weights) || misaligned(dweights)) return EXL3_EINVAL;
-    if (drows == rows || dweights == weights) return EXL3_EINVAL;
+    if (drows == rows || drows == weights || drows == dweights || dweights == weights || dweights == rows || dweights == dy ||
+        dweights == position)
+        return EXL3_EINVAL;
     const RowParams p = {dy, rows, n_tokens, top_k, n, position, kept, weights, weights_dtype, drows, dweights, streams(n_tokens, top_k, n, dtype)};
     return rows_op(COMBINE_BACKWARD, dtype, p, (hipStream_t)stream);
 }

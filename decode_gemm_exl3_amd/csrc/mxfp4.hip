@@ -920,6 +920,7 @@ int product_checks(int32_t rows, const int32_t* offsets, int32_t n_groups, const
     if (rows == 0) return EXL3_OK;
     if (!codes || !scales || !y) return EXL3_EINVAL;
     if (misaligned(codes) || misaligned(scales) || misaligned(y) || (reinterpret_cast<uintptr_t>(offsets) & 3)) return EXL3_EINVAL;
+    if (y == codes || y == scales || y == offsets) return EXL3_EINVAL;
     if (n_in > (1 << 20) || n_groups > 4096 || rows > (1 << 23) || n_out > (1 << 24)) return EXL3_EUNSUPPORTED;
     // a launch takes fewer than 2^32 threads: 2^24 workgroups of the smallest tile that many outputs come in
     if ((((int64_t)rows >> 6) + n_groups + 2) * (((int64_t)n_out >> 6) + 1) >= (1 << 24) - XCDS * XCD_UNIT) return EXL3_EUNSUPPORTED;
@@ -938,6 +939,7 @@ int exl3_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int32_t n, i
     if (bad_dtype(dtype) || bad_row(n) || rows < 0 || bad_ld(ldx, n, dtype)) return EXL3_EINVAL;
     if (rows == 0) return EXL3_OK;
     if (!x || !codes || !scales || misaligned(x) || misaligned(codes) || misaligned(scales)) return EXL3_EINVAL;
+    if (x == codes || x == scales || codes == scales) return EXL3_EINVAL;
     if (too_many_units(rows, n)) return EXL3_EUNSUPPORTED;
     return quantize(dtype, x, rows, n, ldx, codes, scales, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_EHIP;
 }
@@ -947,6 +949,7 @@ int exl3_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t r
     if (bad_dtype(dtype) || bad_row(n) || rows < 0) return EXL3_EINVAL;
     if (rows == 0) return EXL3_OK;
     if (!out || !codes || !scales || misaligned(out) || misaligned(codes) || misaligned(scales)) return EXL3_EINVAL;
+    if (out == codes || out == scales) return EXL3_EINVAL;
     if (too_many_units(rows, n)) return EXL3_EUNSUPPORTED;
     const int64_t units = rows * (n / 8);
     const dim3 grid((unsigned)((units + 256 * QUANT_UNROLL - 1) / (256 * QUANT_UNROLL)));
@@ -981,7 +984,7 @@ int exl3_mxfp4_linear(const void* x, int32_t dtype, int32_t rows, int64_t ldx, c
     if (rc < 0) return rc;
     if (bad_ld(ldx, n_in, dtype)) return EXL3_EINVAL;
     if (rc == 0) return rc;
-    if (!x || misaligned(x) || misaligned(workspace) || x == y) return EXL3_EINVAL;
+    if (!x || misaligned(x) || misaligned(workspace) || x == y || (workspace && (workspace == x || workspace == y))) return EXL3_EINVAL;
     const int64_t need = exl3_mxfp4_workspace_bytes(rows, n_groups, n_in);
     if (need > 0 && (!workspace || (int64_t)workspace_bytes < need)) return EXL3_EWORKSPACE;
     ProductParams p = {x, ldx, nullptr, nullptr, offsets, n_groups, rows, codes, scales, n_in, n_out, y, n_out};

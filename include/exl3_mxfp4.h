@@ -18,7 +18,7 @@
  *     NaN or an infinity has b = 255 and codes 0: it dequantises to NaN.
  *
  * Conventions: as in exl3.h (device pointers owned by the caller, 16-byte
- * aligned, no allocation, `stream` a hipStream_t of the current device,
+ * aligned, results apart from the arguments, no allocation, `stream` a hipStream_t of the current device,
  * argument errors returned before any launch, no exception crosses).  Status
  * codes are exl3_status.
  */
@@ -101,7 +101,8 @@ int exl3_mxfp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, int32_t r
  *   x         : dtype [rows][n_in], row stride ldx as in exl3_mxfp4_quantize
  *   workspace : device scratch of exl3_mxfp4_workspace_bytes(rows, n_groups,
  *               n_in) bytes (NULL where that is 0); its contents need no
- *               initialisation and are meaningless after the call.  Calls that may run at the same time need separate ones.
+ *               initialisation and are meaningless after the call.  Calls that
+ *               may run at the same time need separate ones.
  * Errors as exl3_mxfp4_matmul, and EXL3_EWORKSPACE.
  */
 int exl3_mxfp4_linear(const void* x, int32_t dtype, int32_t rows, int64_t ldx, const int32_t* offsets,

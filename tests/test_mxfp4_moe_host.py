@@ -137,6 +137,25 @@ def test_moe_argument_errors(lib):
     assert b(w=None) == -1 and b(src=None) == -1 and b(dw=None) == -1 and b(src=4 * A) == -1 and b(dw=5 * A) == -1
 
 
+def test_results_over_arguments_are_refused(lib):
+    # every workgroup reads what others write: the same pointer twice is an error, not a race
+    q = lambda x, c, s: lib.exl3_mxfp4_quantize(x, F16, 4, 64, 64, c, s, None)  # noqa: E731
+    assert q(A, A, 2 * A) == -1 and q(A, 2 * A, A) == -1 and q(A, 2 * A, 2 * A) == -1
+    d = lambda c, s, o: lib.exl3_mxfp4_dequantize(c, s, 4, 64, o, F16, None)  # noqa: E731
+    assert d(A, 2 * A, A) == -1 and d(A, 2 * A, 2 * A) == -1
+    m = lambda y, at=None: lib.exl3_mxfp4_matmul(A, 2 * A, 4, at, 1, 3 * A, 4 * A, 64, 5, y, BF16, None)  # noqa: E731
+    assert [m(k * A) for k in (1, 2, 3, 4)] == [-1] * 4 and m(5 * A, 5 * A) == -1
+    f = lambda y, ws: lib.exl3_mxfp4_linear(A, BF16, 100, 64, None, 1, 3 * A, 4 * A, 64, 5, y, ws, 1 << 40, None)  # noqa: E731
+    assert [f(k * A, 6 * A) for k in (1, 3, 4)] == [-1] * 3 and f(5 * A, 5 * A) == -1 and f(5 * A, A) == -1
+    s = lambda i, o, p, f: lib.exl3_moe_sort(i, 4, 8, 4, o, p, f, None, 0, None)  # noqa: E731
+    for args in ((1, 1, 3, 4), (1, 2, 1, 4), (1, 2, 2, 4), (1, 2, 3, 1), (1, 2, 3, 2), (1, 2, 3, 3)):
+        assert s(*(k * A for k in args)) == -1
+    b = lambda dr, dw: lib.exl3_moe_combine_backward(A, 2 * A, F32, 4, 2, 8, 3 * A, 4 * A, 5 * A, F32, dr, dw, None)  # noqa: E731
+    assert [b(k * A, 7 * A) for k in (1, 2, 3, 4, 5, 7)] == [-1] * 6 and [b(6 * A, k * A) for k in (1, 2, 3, 5)] == [-1] * 4
+    g = lambda rows: lib.exl3_moe_gather(A, F32, 4, 2, 8, 2 * A, 3 * A, rows, None)  # noqa: E731
+    assert [g(k * A) for k in (1, 2, 3)] == [-1] * 3
+
+
 def test_mxfp4_binding_rejects_bad_tensors():
     x = torch.zeros((3, 64), dtype=torch.bfloat16)
     c, s = torch.zeros((5, 32), dtype=torch.uint8), torch.zeros((5, 2), dtype=torch.uint8)
