@@ -204,11 +204,12 @@ __device__ inline Side side(const uint8_t* codes, const uint8_t* scales, int64_t
 // w + split, ... of the input.  Each wave brings its spans of the weight straight
 // into a ring of its own in LDS, four rows of 256 bytes a load, and waits for
 // nobody (a weight operand read from memory by its lanes would be 64 places for
-// 1 KB, 64 cycles of the address unit instead of 16).  The rows come quantised,
-// the same way, or (FUSED) as values, which the workgroup quantises into LDS while
-// the weight is on its way: FUSED_ROW_SPANS spans of them, all rows together, so
-// that two workgroups fit a CU.  A run's sums meet in LDS and are added in the
-// order of its waves.
+// 1 KB, 64 cycles of the address unit instead of 16).  The rows come quantised, the
+// same way (STREAMED), or, HELD_ROW_SPANS spans of them, all rows together, the
+// workgroup brings them into LDS first, while the weight is on its way: quantised
+// ones (STAGED), or values that it quantises (QUANTISED).  Then two workgroups fit
+// a CU: 2048 rows in 256 groups 1024 -> 1024 35 us staged against 57 streamed.  A run's sums meet
+// in LDS and are added in the order of its waves.
 //
 // Block b of row r sits in 16-byte slot b ^ swizzle(r): the 16 lanes that LDS
 // serves together (rows 0-3 and 12-15 of one quarter, 4-11 of the next) then
@@ -219,10 +220,11 @@ __device__ inline Side side(const uint8_t* codes, const uint8_t* scales, int64_t
 // A short launch is its start, the rows' and the weight's latency and the sums:
 // one row 4096 -> 4096 in 4.7 us, of which 1.7 are the weight's at the copy rate.
 constexpr int SMALL_WAVES = 8, SMALL_RING = 2, SMALL_MAX_ROWS = 16;
-constexpr int FUSED_ROW_SPANS = 32;
-// Rows of a tile that quantises them itself (0: none fits).
-__host__ __device__ inline int fused_rows(int n_in) {
-    const int rows = FUSED_ROW_SPANS / ((n_in + SPAN_BLOCKS * BLOCK - 1) / (SPAN_BLOCKS * BLOCK));
+enum Rows { STREAMED, STAGED, QUANTISED };
+constexpr int HELD_ROW_SPANS = 32;
+// Rows of a tile that holds them (0: none fits).
+__host__ __device__ inline int held_rows(int n_in) {
+    const int rows = HELD_ROW_SPANS / ((n_in + SPAN_BLOCKS * BLOCK - 1) / (SPAN_BLOCKS * BLOCK));
     return rows < SMALL_MAX_ROWS ? rows : SMALL_MAX_ROWS;
 }
 
@@ -230,15 +232,16 @@ __device__ inline int small_swizzle(int row) {  // rows / 4: 0 1 2 3 -> 0 2 3 1
     return (row & 3) | (((0x78 >> (row >> 2 << 1)) & 3) << 2);
 }
 
-template <typename OT, bool FUSED, bool WHOLE>
+template <typename OT, Rows ROWS, bool WHOLE>
 __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductParams p, int split) {
-    constexpr int SDW = SCALE_DWORDS<WHOLE>, SIDES = FUSED ? 1 : 2, LOADS = SIDES * (4 + SDW / 4);
+    constexpr bool HELD = ROWS != STREAMED;
+    constexpr int SDW = SCALE_DWORDS<WHOLE>, SIDES = HELD ? 1 : 2, LOADS = SIDES * (4 + SDW / 4);
     constexpr int BUF = SIDES * (256 + 4 * SDW);  // slots: codes of each side, then scales
     constexpr int RING = SMALL_WAVES * SMALL_RING * BUF;
-    __shared__ i32x4_t lds[RING + (FUSED ? FUSED_ROW_SPANS * 17 : 0)];  // and the quantised rows: codes, scales
+    __shared__ i32x4_t lds[RING + (HELD ? HELD_ROW_SPANS * 17 : 0)];  // and the held rows: codes, scales
     static_assert(SMALL_RING * BUF >= 64, "the sums of a wave fit its ring");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
-    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, blockIdx.y, FUSED ? fused_rows(p.n_in) : SMALL_MAX_ROWS);
+    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, blockIdx.y, HELD ? held_rows(p.n_in) : SMALL_MAX_ROWS);
     if (t.rows == 0) return;
     const int first = wave % split;  // of the run's spans
     const int n0 = (blockIdx.x * (SMALL_WAVES / split) + wave / split) * 16, cols = min(16, p.n_out - n0);
@@ -250,7 +253,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductPa
         const int mine = cols > 0 ? (spans - first + split - 1) / split : 0;  // spans of this wave
         Side sides[SIDES];
         sides[0] = side(p.wc, p.ws, (int64_t)t.group * p.n_out + (cols > 0 ? n0 : 0), max(cols, 1), nb);
-        if constexpr (!FUSED) sides[1] = side(p.xc, p.xs, t.row0, t.rows, nb);
+        if constexpr (!HELD) sides[1] = side(p.xc, p.xs, t.row0, t.rows, nb);
         uint32_t row_at[SIDES][4], scale_at[SIDES][SDW / 4], shift[SIDES];
 #pragma unroll
         for (int s = 0; s < SIDES; ++s) {
@@ -286,12 +289,29 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductPa
         };
         auto operand = [&](int s, int k, int j) { return ring[k % SMALL_RING * BUF + s * 256 + r * 16 + ((4 * q + j) ^ small_swizzle(r))]; };
         i32x4_t* const xq = lds + RING;  // [row][spans * 16], block b of row r at b ^ small_swizzle(r)
-        uint8_t* const xq_scales = reinterpret_cast<uint8_t*>(xq + FUSED_ROW_SPANS * 16);
+        uint8_t* const xq_scales = reinterpret_cast<uint8_t*>(xq + HELD_ROW_SPANS * 16);
 #pragma unroll
         for (int k = 0; k < SMALL_RING; ++k) ask(k);
-        if constexpr (FUSED) {
+        if constexpr (ROWS == STAGED) {
+            // a block a thread; zeros behind a row's end
+            static_assert(HELD_ROW_SPANS * SPAN_BLOCKS <= SMALL_WAVES * 64, "a thread for each");
+            const int row = threadIdx.x / (spans * SPAN_BLOCKS), block = threadIdx.x - row * spans * SPAN_BLOCKS;
+            if (row < t.rows) {
+                const int64_t at = (int64_t)(t.row0 + row) * nb + block;
+                i32x4_t c = {0, 0, 0, 0};
+                uint8_t b = 0;
+                if (block < nb) {
+                    c = *reinterpret_cast<const i32x4_t*>(p.xc + at * 16);
+                    b = p.xs[at];
+                }
+                xq[row * spans * 16 + (block ^ small_swizzle(row))] = c;
+                xq_scales[row * spans * 16 + block] = b;
+            }
+            __syncthreads();
+        }
+        if constexpr (ROWS == QUANTISED) {
             // eight values a thread and round, four threads a block, as quantize_kernel
-            constexpr int THREADS = SMALL_WAVES * 64, ROUNDS = FUSED_ROW_SPANS * 64 / THREADS, NW = 2 * OT::bytes;
+            constexpr int THREADS = SMALL_WAVES * 64, ROUNDS = HELD_ROW_SPANS * 64 / THREADS, NW = 2 * OT::bytes;
             const int per_row = spans * 64, units = t.rows * per_row;
             uint32_t w[ROUNDS][NW];
 #pragma unroll
@@ -332,7 +352,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductPa
 #pragma unroll
             for (int j = 0; j < 4; ++j) wv[j] = operand(0, k, j);
             const uint32_t wsc = scales(0, k, left);
-            if constexpr (FUSED) {
+            if constexpr (HELD) {
                 const int row = min(r, t.rows - 1);  // rows behind the tile re-read its last
 #pragma unroll
                 for (int j = 0; j < 4; ++j) xv[j] = xq[(row * spans + sp) * 16 + ((4 * q + j) ^ small_swizzle(row))];
@@ -789,22 +809,26 @@ inline int64_t typical_rows(int64_t rows, int n_groups) { return (rows + n_group
 // Whether a product quantises its rows itself: a tile holds a group's rows.  Saves
 // the launch and the codes' way through memory (us, with the quantisation: one row
 // 4096 -> 4096 5.0 against 7.0, 8192 -> 28672 25.6 against 31; 4 rows of each of
-// 64 groups 2048 -> 2816 32 against 39; equal at 8).
-inline bool fused(int64_t rows, int n_groups, int n_in) { return typical_rows(rows, n_groups) <= fused_rows(n_in); }
+// 64 groups 2048 -> 2816 32 against 39; equal at 8, and 16 rows of each of 512
+// groups 1024 -> 1024 115 against 93).
+inline bool fused(int64_t rows, int n_groups, int n_in) {
+    const int most = n_groups > 1 ? 8 : SMALL_MAX_ROWS, held = held_rows(n_in);
+    return typical_rows(rows, n_groups) <= (held < most ? held : most);
+}
 
-template <typename OT, bool FUSED> hipError_t launch_small(const ProductParams& p, hipStream_t s) {
-    const int64_t runs = (p.n_out + 15) / 16, tiles = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, FUSED ? fused_rows(p.n_in) : SMALL_MAX_ROWS);
-    // As many waves a run as the card holds at once (two workgroups a CU when FUSED,
+template <typename OT, Rows ROWS> hipError_t launch_small(const ProductParams& p, hipStream_t s) {
+    const int64_t runs = (p.n_out + 15) / 16, tiles = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, ROWS != STREAMED ? held_rows(p.n_in) : SMALL_MAX_ROWS);
+    // As many waves a run as the card holds at once (two workgroups a CU with HELD rows,
     // else one), so that one round of workgroups starts up and quantises: one row
     // 4096 -> 14336 takes 9.0 us at 4 waves a run and 11.2 at 8, 8192 -> 28672
     // 25.6 at 2, 29.9 at 4 and 30.2 at 1, 14336 -> 4096 9.5 at 8 and 11.1 at 4;
     // 64 rows in 64 groups 2048 -> 2816 19 at 1 and 63 at 8.
-    const int64_t resident = 256 * SMALL_WAVES * (FUSED ? 2 : 1), spans = (p.n_in / BLOCK + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
+    const int64_t resident = 256 * SMALL_WAVES * (ROWS != STREAMED ? 2 : 1), spans = (p.n_in / BLOCK + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
     int split = 1;
     while (split < SMALL_WAVES && split < spans && runs * tiles * split * 2 <= resident) split *= 2;
     const dim3 grid((unsigned)((runs * split + SMALL_WAVES - 1) / SMALL_WAVES), (unsigned)tiles);
-    if (p.n_in % (4 * BLOCK) == 0) small_kernel<OT, FUSED, true><<<grid, SMALL_WAVES * 64, 0, s>>>(p, split);
-    else small_kernel<OT, FUSED, false><<<grid, SMALL_WAVES * 64, 0, s>>>(p, split);
+    if (p.n_in % (4 * BLOCK) == 0) small_kernel<OT, ROWS, true><<<grid, SMALL_WAVES * 64, 0, s>>>(p, split);
+    else small_kernel<OT, ROWS, false><<<grid, SMALL_WAVES * 64, 0, s>>>(p, split);
     return hipGetLastError();
 }
 
@@ -838,14 +862,15 @@ inline double rounds128(const ProductParams& p) {
 }
 
 template <typename OT> hipError_t launch_product(const ProductParams& p, hipStream_t s) {
-    if (p.x) return launch_small<OT, true>(p, s);
+    if (p.x) return launch_small<OT, QUANTISED>(p, s);
+    if (fused(p.rows, p.n_groups, p.n_in)) return launch_small<OT, STAGED>(p, s);
     constexpr int64_t CUS = 256;
     // Few rows (us, with the quantisation): 16 rows 14336 -> 4096 13.2 in small
     // tiles and 23.8 in 64 x 64 ones, 4096 -> 14336 12.6 and 12.9; 24 rows 14336 ->
     // 4096 15.2 and 24.5, but 4096 -> 14336 17 and 13.2; 8 rows of each of 64
     // groups 2048 -> 2816 50 and 61.
     const int64_t m = typical_rows(p.rows, p.n_groups);
-    if (p.offsets ? m <= 8 : m <= 16 || (m <= 32 && p.n_out <= 4096)) return launch_small<OT, false>(p, s);
+    if (p.offsets ? m <= 8 : m <= 16 || (m <= 32 && p.n_out <= 4096)) return launch_small<OT, STREAMED>(p, s);
     // 32 x 32 tiles in one round: 64 rows 14336 -> 4096 (256 of them) 15.0 us against
     // 25.4 in 64 x 64, 256 rows 4096 -> 1024 6.2 against 8.7; two rounds lose (128
     // rows 14336 -> 4096 26.1 against 24.4, 1024 -> 4096 7.3 against 5.1).

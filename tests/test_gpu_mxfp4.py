@@ -208,6 +208,15 @@ def test_many_groups(ex):
     check_groups(ex, [0] * 64 + [400] + [0] * 63, 1, 128, 40, "fp16")
 
 
+@pytest.mark.parametrize("groups", [191, 192, 255, 256, 257, 511, 1030])
+def test_more_groups_than_one_batch_of_offsets(ex, groups):
+    # a tile is looked for 64 groups at a time, 256 of them loaded together
+    rng = np.random.default_rng([8, groups])
+    check_groups(ex, [int(c) for c in rng.integers(0, 3, groups)], 2, 64, 17, "fp16")
+    check_groups(ex, [0] * (groups - 1) + [3], 0, 64, 17, "bf16")
+    check_groups(ex, [0] * (groups - 70) + [150] + [0] * 69, 5, 64, 17, "fp32")
+
+
 @pytest.mark.parametrize("n_in", [96, 512, 2048, 4096, 4128, 16384, 16416])
 @pytest.mark.parametrize("m", [1, 2, 4, 5, 8])
 def test_few_rows_of_every_length(ex, m, n_in):
