@@ -205,11 +205,11 @@ __device__ inline Side side(const uint8_t* codes, const uint8_t* scales, int64_t
 // into a ring of its own in LDS, four rows of 256 bytes a load, and waits for
 // nobody (a weight operand read from memory by its lanes would be 64 places for
 // 1 KB, 64 cycles of the address unit instead of 16).  The rows come quantised, the
-// same way (STREAMED), or, HELD_ROW_SPANS spans of them, all rows together, the
+// same way (STREAMED), or, up to HELD spans of them, all rows together, the
 // workgroup brings them into LDS first, while the weight is on its way: quantised
-// ones (STAGED), or values that it quantises (QUANTISED).  Then two workgroups fit
-// a CU: 2048 rows in 256 groups 1024 -> 1024 35 us staged against 57 streamed.  A run's sums meet
-// in LDS and are added in the order of its waves.
+// ones (STAGED), or values that it quantises (QUANTISED).  With HELD_SPANS two
+// workgroups fit a CU: 2048 rows in 256 groups 1024 -> 1024 35 us staged against 57
+// streamed.  A run's sums meet in LDS and are added in the order of its waves.
 //
 // Block b of row r sits in 16-byte slot b ^ swizzle(r): the 16 lanes that LDS
 // serves together (rows 0-3 and 12-15 of one quarter, 4-11 of the next) then
@@ -221,10 +221,10 @@ __device__ inline Side side(const uint8_t* codes, const uint8_t* scales, int64_t
 // one row 4096 -> 4096 in 4.7 us, of which 1.7 are the weight's at the copy rate.
 constexpr int SMALL_WAVES = 8, SMALL_RING = 2, SMALL_MAX_ROWS = 16;
 enum Rows { STREAMED, STAGED, QUANTISED };
-constexpr int HELD_ROW_SPANS = 32;
-// Rows of a tile that holds them (0: none fits).
-__host__ __device__ inline int held_rows(int n_in) {
-    const int rows = HELD_ROW_SPANS / ((n_in + SPAN_BLOCKS * BLOCK - 1) / (SPAN_BLOCKS * BLOCK));
+constexpr int HELD_SPANS = 32, MORE_HELD_SPANS = 64;
+// Rows of a tile that holds `spans` spans of them (0: none fits).
+__host__ __device__ inline int held_rows(int n_in, int spans) {
+    const int rows = spans / ((n_in + SPAN_BLOCKS * BLOCK - 1) / (SPAN_BLOCKS * BLOCK));
     return rows < SMALL_MAX_ROWS ? rows : SMALL_MAX_ROWS;
 }
 
@@ -232,16 +232,15 @@ __device__ inline int small_swizzle(int row) {  // rows / 4: 0 1 2 3 -> 0 2 3 1
     return (row & 3) | (((0x78 >> (row >> 2 << 1)) & 3) << 2);
 }
 
-template <typename OT, Rows ROWS, bool WHOLE>
+template <typename OT, Rows ROWS, int HELD, bool WHOLE>
 __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductParams p, int split) {
-    constexpr bool HELD = ROWS != STREAMED;
     constexpr int SDW = SCALE_DWORDS<WHOLE>, SIDES = HELD ? 1 : 2, LOADS = SIDES * (4 + SDW / 4);
     constexpr int BUF = SIDES * (256 + 4 * SDW);  // slots: codes of each side, then scales
     constexpr int RING = SMALL_WAVES * SMALL_RING * BUF;
-    __shared__ i32x4_t lds[RING + (HELD ? HELD_ROW_SPANS * 17 : 0)];  // and the held rows: codes, scales
+    __shared__ i32x4_t lds[RING + (HELD * 17)];  // and the held rows: codes, scales
     static_assert(SMALL_RING * BUF >= 64, "the sums of a wave fit its ring");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
-    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, blockIdx.y, HELD ? held_rows(p.n_in) : SMALL_MAX_ROWS);
+    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, blockIdx.y, HELD ? held_rows(p.n_in, HELD) : SMALL_MAX_ROWS);
     if (t.rows == 0) return;
     const int first = wave % split;  // of the run's spans
     const int n0 = (blockIdx.x * (SMALL_WAVES / split) + wave / split) * 16, cols = min(16, p.n_out - n0);
@@ -289,12 +288,12 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductPa
         };
         auto operand = [&](int s, int k, int j) { return ring[k % SMALL_RING * BUF + s * 256 + r * 16 + ((4 * q + j) ^ small_swizzle(r))]; };
         i32x4_t* const xq = lds + RING;  // [row][spans * 16], block b of row r at b ^ small_swizzle(r)
-        uint8_t* const xq_scales = reinterpret_cast<uint8_t*>(xq + HELD_ROW_SPANS * 16);
+        uint8_t* const xq_scales = reinterpret_cast<uint8_t*>(xq + HELD * 16);
 #pragma unroll
         for (int k = 0; k < SMALL_RING; ++k) ask(k);
         if constexpr (ROWS == STAGED) {
             // a block a thread; zeros behind a row's end
-            static_assert(HELD_ROW_SPANS * SPAN_BLOCKS <= SMALL_WAVES * 64, "a thread for each");
+            static_assert(HELD * SPAN_BLOCKS <= SMALL_WAVES * 64, "a thread for each");
             const int row = threadIdx.x / (spans * SPAN_BLOCKS), block = threadIdx.x - row * spans * SPAN_BLOCKS;
             if (row < t.rows) {
                 const int64_t at = (int64_t)(t.row0 + row) * nb + block;
@@ -311,33 +310,36 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductPa
         }
         if constexpr (ROWS == QUANTISED) {
             // eight values a thread and round, four threads a block, as quantize_kernel
-            constexpr int THREADS = SMALL_WAVES * 64, ROUNDS = HELD_ROW_SPANS * 64 / THREADS, NW = 2 * OT::bytes;
+            constexpr int THREADS = SMALL_WAVES * 64, ROUNDS = 4, NW = 2 * OT::bytes;
             const int per_row = spans * 64, units = t.rows * per_row;
-            uint32_t w[ROUNDS][NW];
+            for (int u0 = threadIdx.x; u0 < units; u0 += ROUNDS * THREADS) {
+                uint32_t w[ROUNDS][NW];
 #pragma unroll
-            for (int i = 0; i < ROUNDS; ++i) {
-                const int u = i * THREADS + threadIdx.x, row = u / per_row, at = u - row * per_row;
+                for (int i = 0; i < ROUNDS; ++i) {
+                    const int u = u0 + i * THREADS, row = u / per_row, at = u - row * per_row;
 #pragma unroll
-                for (int e = 0; e < NW; ++e) w[i][e] = 0;
-                if (u < units && at < nb * 4) {
-                    const u32x4_t* src = reinterpret_cast<const u32x4_t*>(static_cast<const char*>(p.x) + ((int64_t)(t.row0 + row) * p.ldx + 8 * at) * OT::bytes);
+                    for (int e = 0; e < NW; ++e) w[i][e] = 0;
+                    if (u < units && at < nb * 4) {
+                        const int64_t from = (int64_t)(t.row0 + row) * p.ldx + 8 * at;
+                        const u32x4_t* src = reinterpret_cast<const u32x4_t*>(static_cast<const char*>(p.x) + from * OT::bytes);
 #pragma unroll
-                    for (int c = 0; c < NW / 4; ++c) {
-                        const u32x4_t v = src[c];
+                        for (int c = 0; c < NW / 4; ++c) {
+                            const u32x4_t v = src[c];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) w[i][4 * c + e] = v[e];
+                            for (int e = 0; e < 4; ++e) w[i][4 * c + e] = v[e];
+                        }
                     }
                 }
-            }
 #pragma unroll
-            for (int i = 0; i < ROUNDS; ++i) {
-                const int u = i * THREADS + threadIdx.x, row = u / per_row, at = u - row * per_row;
-                if (u < units) {  // whole quads
-                    uint32_t b;
-                    const uint32_t c = quantize_quad<OT>(w[i], b);
-                    const int slot = row * spans * 16 + ((at >> 2) ^ small_swizzle(row));
-                    reinterpret_cast<uint32_t*>(xq + slot)[at & 3] = c;
-                    if ((at & 3) == 0) xq_scales[row * spans * 16 + (at >> 2)] = (uint8_t)b;
+                for (int i = 0; i < ROUNDS; ++i) {
+                    const int u = u0 + i * THREADS, row = u / per_row, at = u - row * per_row;
+                    if (u < units) {  // whole quads
+                        uint32_t b;
+                        const uint32_t c = quantize_quad<OT>(w[i], b);
+                        const int slot = row * spans * 16 + ((at >> 2) ^ small_swizzle(row));
+                        reinterpret_cast<uint32_t*>(xq + slot)[at & 3] = c;
+                        if ((at & 3) == 0) xq_scales[row * spans * 16 + (at >> 2)] = (uint8_t)b;
+                    }
                 }
             }
             __syncthreads();
@@ -806,29 +808,36 @@ template <typename T> hipError_t launch_quantize(const void* x, int64_t rows, in
 // Rows that a group has on average: what a tile's height is chosen by.
 inline int64_t typical_rows(int64_t rows, int n_groups) { return (rows + n_groups - 1) / n_groups; }
 
-// Whether a product quantises its rows itself: a tile holds a group's rows.  Saves
-// the launch and the codes' way through memory (us, with the quantisation: one row
-// 4096 -> 4096 5.0 against 7.0, 8192 -> 28672 25.6 against 31; 4 rows of each of
-// 64 groups 2048 -> 2816 32 against 39; equal at 8, and 16 rows of each of 512
-// groups 1024 -> 1024 115 against 93).
-inline bool fused(int64_t rows, int n_groups, int n_in) {
-    const int most = n_groups > 1 ? 8 : SMALL_MAX_ROWS, held = held_rows(n_in);
-    return typical_rows(rows, n_groups) <= (held < most ? held : most);
+// The spans that a product's workgroups hold in LDS, where a tile of them holds a
+// group's rows; 0 where it holds none.  A product of values then quantises them
+// itself, without a launch and the codes' way through memory (us, with the
+// quantisation: one row 4096 -> 4096 5.0 against 7.0, 8192 -> 28672 25.6 against 31;
+// 4 rows of each of 64 groups 2048 -> 2816 32 against 39; equal at 8, and 16 rows of
+// each of 512 groups 1024 -> 1024 115 against 93).  More than HELD_SPANS: 5 rows
+// 4096 -> 14336 9.1 against 11.0, 8 rows 9.9 against 10.9, but 12 rows (96 spans)
+// 11.4 against 11.1, 8192 -> 4096 4 rows 8.6 against 9.2 and 6 rows (96) 9.9; not for
+// groups, where the larger ones take more tiles (512 rows in 64 4096 -> 2816 110
+// against 89).
+inline int held_spans(int64_t rows, int n_groups, int n_in) {
+    const int64_t m = typical_rows(rows, n_groups);
+    if (n_groups > 1 && m > 8) return 0;
+    if (m <= held_rows(n_in, HELD_SPANS)) return HELD_SPANS;
+    return n_groups == 1 && m <= held_rows(n_in, MORE_HELD_SPANS) ? MORE_HELD_SPANS : 0;
 }
 
-template <typename OT, Rows ROWS> hipError_t launch_small(const ProductParams& p, hipStream_t s) {
-    const int64_t runs = (p.n_out + 15) / 16, tiles = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, ROWS != STREAMED ? held_rows(p.n_in) : SMALL_MAX_ROWS);
-    // As many waves a run as the card holds at once (two workgroups a CU with HELD rows,
-    // else one), so that one round of workgroups starts up and quantises: one row
+template <typename OT, Rows ROWS, int HELD> hipError_t launch_small(const ProductParams& p, hipStream_t s) {
+    const int64_t runs = (p.n_out + 15) / 16, tiles = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, HELD ? held_rows(p.n_in, HELD) : SMALL_MAX_ROWS);
+    // As many waves a run as the card holds at once (two workgroups a CU with
+    // HELD_SPANS, else one), so that one round of workgroups starts up and quantises: one row
     // 4096 -> 14336 takes 9.0 us at 4 waves a run and 11.2 at 8, 8192 -> 28672
     // 25.6 at 2, 29.9 at 4 and 30.2 at 1, 14336 -> 4096 9.5 at 8 and 11.1 at 4;
     // 64 rows in 64 groups 2048 -> 2816 19 at 1 and 63 at 8.
-    const int64_t resident = 256 * SMALL_WAVES * (ROWS != STREAMED ? 2 : 1), spans = (p.n_in / BLOCK + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
+    const int64_t resident = 256 * SMALL_WAVES * (HELD == HELD_SPANS ? 2 : 1), spans = (p.n_in / BLOCK + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
     int split = 1;
     while (split < SMALL_WAVES && split < spans && runs * tiles * split * 2 <= resident) split *= 2;
     const dim3 grid((unsigned)((runs * split + SMALL_WAVES - 1) / SMALL_WAVES), (unsigned)tiles);
-    if (p.n_in % (4 * BLOCK) == 0) small_kernel<OT, ROWS, true><<<grid, SMALL_WAVES * 64, 0, s>>>(p, split);
-    else small_kernel<OT, ROWS, false><<<grid, SMALL_WAVES * 64, 0, s>>>(p, split);
+    if (p.n_in % (4 * BLOCK) == 0) small_kernel<OT, ROWS, HELD, true><<<grid, SMALL_WAVES * 64, 0, s>>>(p, split);
+    else small_kernel<OT, ROWS, HELD, false><<<grid, SMALL_WAVES * 64, 0, s>>>(p, split);
     return hipGetLastError();
 }
 
@@ -862,15 +871,16 @@ inline double rounds128(const ProductParams& p) {
 }
 
 template <typename OT> hipError_t launch_product(const ProductParams& p, hipStream_t s) {
-    if (p.x) return launch_small<OT, QUANTISED>(p, s);
-    if (fused(p.rows, p.n_groups, p.n_in)) return launch_small<OT, STAGED>(p, s);
+    const int held = held_spans(p.rows, p.n_groups, p.n_in);
+    if (p.x) return held == HELD_SPANS ? launch_small<OT, QUANTISED, HELD_SPANS>(p, s) : launch_small<OT, QUANTISED, MORE_HELD_SPANS>(p, s);
+    if (held == HELD_SPANS) return launch_small<OT, STAGED, HELD_SPANS>(p, s);
     constexpr int64_t CUS = 256;
     // Few rows (us, with the quantisation): 16 rows 14336 -> 4096 13.2 in small
     // tiles and 23.8 in 64 x 64 ones, 4096 -> 14336 12.6 and 12.9; 24 rows 14336 ->
     // 4096 15.2 and 24.5, but 4096 -> 14336 17 and 13.2; 8 rows of each of 64
     // groups 2048 -> 2816 50 and 61.
     const int64_t m = typical_rows(p.rows, p.n_groups);
-    if (p.offsets ? m <= 8 : m <= 16 || (m <= 32 && p.n_out <= 4096)) return launch_small<OT, STREAMED>(p, s);
+    if (p.offsets ? m <= 8 : m <= 16 || (m <= 32 && p.n_out <= 4096)) return launch_small<OT, STREAMED, 0>(p, s);
     // 32 x 32 tiles in one round: 64 rows 14336 -> 4096 (256 of them) 15.0 us against
     // 25.4 in 64 x 64, 256 rows 4096 -> 1024 6.2 against 8.7; two rounds lose (128
     // rows 14336 -> 4096 26.1 against 24.4, 1024 -> 4096 7.3 against 5.1).
@@ -988,7 +998,7 @@ int exl3_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t r
 
 int64_t exl3_mxfp4_workspace_bytes(int32_t rows, int32_t n_groups, int32_t n_in) {
     if (rows < 0 || n_groups < 1 || bad_row(n_in)) return EXL3_EINVAL;
-    return fused(rows, n_groups, n_in) ? 0 : codes_bytes(rows, n_in) + (((int64_t)rows * (n_in / BLOCK) + 255) & ~int64_t(255));
+    return held_spans(rows, n_groups, n_in) ? 0 : codes_bytes(rows, n_in) + (((int64_t)rows * (n_in / BLOCK) + 255) & ~int64_t(255));
 }
 
 int exl3_mxfp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, int32_t rows, const int32_t* offsets,
