@@ -77,12 +77,15 @@ def result(t, name: str, like, dtype, shape):
 def need_rows(t, name: str):
     """A 2-dimensional floating tensor whose rows are contiguous and start at
     multiples of 16 bytes: (rows, columns, row stride in elements, exl3_dtype, address)."""
-    code = dtype_code(t, name)
-    if t.dim() != 2:
-        raise Exl3Error(f"{name}: expected two dimensions, got shape {tuple(t.shape)}")
-    rows, n = t.shape
+    code = FLOATS.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None:
+        dtype_code(t, name)
+    shape = t.shape
+    if len(shape) != 2:
+        raise Exl3Error(f"{name}: expected two dimensions, got shape {tuple(shape)}")
+    rows, n = shape
     if n >> 31:
-        too_large(name, t.shape)
+        too_large(name, shape)
     ld, inner = t.stride()
     if rows <= 1:
         ld = n
@@ -136,6 +139,8 @@ def on_stream(stream, fn, first, *args):
 def scratch(workspace, nbytes: int, like):
     """Address and size of `workspace` when given, else of scratch of the caching
     allocator; the third value keeps it alive for the call."""
+    if workspace is None and nbytes == 0:
+        return None, 0, None
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor):
             raise Exl3Error("workspace: expected a torch tensor")
@@ -143,7 +148,5 @@ def scratch(workspace, nbytes: int, like):
         if workspace.get_device() != like.get_device():
             on_device(like.get_device(), workspace=workspace)
         return at, workspace.numel(), workspace
-    if nbytes == 0:
-        return None, 0, None
     buf = like.new_empty(nbytes, dtype=torch.uint8)
     return buf.data_ptr(), nbytes, buf

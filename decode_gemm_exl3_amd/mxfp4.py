@@ -81,14 +81,14 @@ def mxfp4_workspace_bytes(rows: int, n_in: int, groups: int = 1) -> int:
 
 def _weight(codes, scales, offsets, n_in: int, blocks: int):
     """Addresses of a weight and its offsets, with the group count and n_out."""
-    if not isinstance(codes, torch.Tensor) or codes.dim() != (2 if offsets is None else 3):
+    shape = codes.shape if isinstance(codes, torch.Tensor) else ()
+    if len(shape) != (2 if offsets is None else 3):
         raise Exl3Error("codes: expected a torch tensor [n_out, n_in / 2], or [groups, n_out, n_in / 2] with offsets")
-    if codes.shape[-2] >> 31 or codes.shape[0] >> 31:
-        too_large("codes", codes.shape)
+    n_out, groups = shape[-2], 1 if offsets is None else shape[0]
+    if (n_out | groups) >> 31:
+        too_large("codes", shape)
     if offsets is None:
-        n_out = codes.shape[0]
         return need(codes, "codes", BYTES, (n_out, n_in // 2)), need(scales, "scales", BYTES, (n_out, blocks)), None, 1, n_out
-    groups, n_out = codes.shape[:2]
     return (need(codes, "codes", BYTES, (groups, n_out, n_in // 2)), need(scales, "scales", BYTES, (groups, n_out, blocks)),
             need(offsets, "offsets", INDEX, (groups + 1,)), groups, n_out)
 
