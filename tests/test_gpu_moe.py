@@ -300,3 +300,39 @@ def test_captured_layer_with_changing_routes(ex):
             assert torch.equal(a, b)
         for a, b in zip(eager, refs[(i + 1) % 4]):
             assert torch.equal(a, b)
+
+
+def test_more_than_32_bits_of_values(ex):
+    tokens, top_k, n, dropped = 1 << 19, 2, 4160, 6
+    slots = tokens * top_k
+    x = torch.randn((1024, n), generator=torch.Generator(device="cuda").manual_seed(4), device="cuda").half().repeat(tokens // 1024, 1)
+    pos = torch.arange(slots - 1, -1, -1, dtype=torch.int32, device="cuda").reshape(tokens, top_k)  # the first slots come last
+    at = torch.tensor([0, slots - dropped], dtype=torch.int32, device="cuda")
+    rows = ex.moe_gather(x, pos, at)
+    assert rows.numel() > 1 << 32
+    none = dropped // top_k  # tokens without a place
+    for t in (none, 1, 1000, tokens // 2 - 1, tokens // 2, tokens - 1):
+        for j in range(top_k):
+            assert torch.equal(rows[slots - 1 - t * top_k - j], x[t] if t >= none else torch.zeros_like(x[t])), (t, j)
+    # two equal rows add up without a rounding
+    y = ex.moe_combine(rows, pos, at)
+    assert torch.equal(y[none:], x[none:] * 2) and not y[:none].any()
+    del y
+    weights = torch.full((tokens, top_k), 0.5, device="cuda")
+    drows, dweights = ex.moe_combine_backward(x, rows, pos, at, weights)
+    for a in range(0, slots, 1 << 17):
+        assert torch.equal(drows[a:a + (1 << 17)], rows[a:a + (1 << 17)] * 0.5), a
+    assert not dweights[:none].any() and bool((dweights[none:] > 0).all())
+
+
+def test_sort_of_many_slots(ex):
+    slots, experts = (1 << 26) + 5, 100
+    ids = torch.randint(-3, experts + 3, (slots, 1), generator=torch.Generator(device="cuda").manual_seed(5), device="cuda", dtype=torch.int32)
+    order, position, offsets = ex.moe_sort(ids, experts)
+    bins = torch.where((ids < 0) | (ids >= experts), experts, ids).reshape(-1)
+    counts = torch.bincount(bins, minlength=experts + 1)
+    assert torch.equal(offsets[1:].long(), counts.cumsum(0)[:experts]) and int(offsets[0]) == 0
+    sorted_bins = bins[order.long()]
+    assert bool((sorted_bins[1:] >= sorted_bins[:-1]).all())
+    assert bool(((order[1:] > order[:-1]) | (sorted_bins[1:] > sorted_bins[:-1])).all())  # stable, and each slot once
+    assert torch.equal(position.reshape(-1)[order.long()], torch.arange(slots, device="cuda", dtype=torch.int32))

@@ -305,3 +305,58 @@ def test_given_workspace(ex):
     assert torch.equal(y, ex.mxfp4_linear(x, codes, scales)) and (ws[need:] == 0xCD).all()
     with pytest.raises(ex.Exl3Error, match="workspace"):
         ex.mxfp4_linear(x, codes, scales, workspace=ws[:need - 16])
+
+
+# ---- more than 2^32 elements ----
+#
+# Large tensors repeat 1024 rows, so that every part of a result has to equal the
+# first.  Codes under a scale of 1 have products that are multiples of 1/4, at most
+# 36, and up to 16384 of them sum to less than 2^24 / 4: fp32 sums are exact.
+
+def test_quantize_more_than_32_bits_of_values(ex):
+    rows, n = 1 << 20, 4128
+    base = torch.randn((1024, n), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").bfloat16()
+    x = base.repeat(rows // 1024, 1)
+    assert x.numel() > 1 << 32
+    codes, scales = ex.mxfp4_quantize(x)
+    ref = ex.mxfp4_quantize(base)
+    del x
+    out = ex.mxfp4_dequantize(codes, scales, torch.bfloat16)
+    ref += (ex.mxfp4_dequantize(*ref, torch.bfloat16),)
+    for i in (0, 1, 507, 508, 1016, 1022, 1023):
+        for got, want in zip((codes, scales, out), ref):
+            assert torch.equal(got[1024 * i:1024 * (i + 1)], want), i
+
+
+def test_product_of_more_than_32_bits_of_outputs(ex):
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    m, n_in, n_out = 1 << 20, 64, 4160
+    base = torch.randint(0, 256, (1024, n_in // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    w = torch.randint(0, 256, (n_out, n_in // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    one = lambda rows: torch.full((rows, n_in // 32), 127, dtype=torch.uint8, device="cuda")  # noqa: E731
+    y = ex.mxfp4_matmul(base.repeat(m // 1024, 1), one(m), w, one(n_out))
+    assert y.numel() > 1 << 32
+    ref = (ex.mxfp4_dequantize(base, one(1024), torch.float32).double().cpu()
+           @ ex.mxfp4_dequantize(w, one(n_out), torch.float32).double().cpu().T).bfloat16().cuda()
+    for i in (0, 1, 503, 504, 1007, 1022, 1023):
+        assert torch.equal(y[1024 * i:1024 * (i + 1)], ref), i
+
+
+@pytest.mark.parametrize("rows", [3, 20, 200, 1500])
+def test_weights_of_more_than_32_bits(ex, rows):
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    groups, n_out, n_in = 72, 8192, 16384
+    w = torch.randint(0, 256, (n_out, n_in // 2), generator=gen, device="cuda", dtype=torch.uint8).repeat(groups, 1, 1)
+    assert w.numel() > 1 << 32
+    w[-1] ^= 0x5A
+    scales = torch.full((groups, n_out, n_in // 32), 127, dtype=torch.uint8, device="cuda")
+    xc = torch.randint(0, 256, (rows, n_in // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    xs = torch.full((rows, n_in // 32), 127, dtype=torch.uint8, device="cuda")
+    at = torch.zeros(groups + 1, dtype=torch.int32, device="cuda")
+    at[-1], at[-2] = rows, 1  # one row of the last group but one, the others of the last
+    y = ex.mxfp4_matmul(xc, xs, w, scales, torch.float32, offsets=at)
+    for g, a, b in ((-2, 0, 1), (-1, 1, rows)):
+        assert torch.equal(y[a:b], ex.mxfp4_matmul(xc[a:b].clone(), xs[a:b].clone(), w[g], scales[g], torch.float32)), g
+    ref = ex.mxfp4_dequantize(xc[1:3], xs[1:3].contiguous(), torch.float32).double().cpu() \
+        @ ex.mxfp4_dequantize(w[-1], scales[-1], torch.float32).double().cpu().T
+    assert torch.equal(y[1:3].double().cpu(), ref)
