@@ -5,6 +5,7 @@
 
 #include "../../include/exl3_mxfp4.h"
 #include "mxfp4_device.hpp"
+#include "spans.hpp"
 
 namespace exl3 {
 namespace mx {
@@ -941,6 +942,12 @@ int dtype_bytes(int32_t d) { return d == EXL3_F32 ? 4 : 2; }
 bool bad_row(int32_t n) { return n < BLOCK || n % BLOCK != 0; }
 bool bad_ld(int64_t ldx, int32_t n, int32_t dtype) { return ldx < n || ldx * dtype_bytes(dtype) % 16 != 0; }
 
+// `rows` rows of n values of dtype.
+Span values(const void* at, int32_t dtype, int64_t rows, int64_t n, int64_t ld) {
+    const int64_t size = dtype_bytes(dtype);
+    return Span{at, n * size, rows, (rows > 1 ? ld : n) * size};
+}
+
 int64_t codes_bytes(int64_t rows, int32_t n) { return (rows * (n / 2) + 255) & ~int64_t(255); }
 
 // More than one launch of quantise or dequantise takes: 2^24 - 1 workgroups (fewer than 2^32 threads).
@@ -955,7 +962,6 @@ int product_checks(int32_t rows, const int32_t* offsets, int32_t n_groups, const
     if (rows == 0) return EXL3_OK;
     if (!codes || !scales || !y) return EXL3_EINVAL;
     if (misaligned(codes) || misaligned(scales) || misaligned(y) || (reinterpret_cast<uintptr_t>(offsets) & 3)) return EXL3_EINVAL;
-    if (y == codes || y == scales || y == offsets) return EXL3_EINVAL;
     if (n_in > (1 << 20) || n_groups > 4096 || rows > (1 << 23) || n_out > (1 << 24)) return EXL3_EUNSUPPORTED;
     // a launch takes fewer than 2^32 threads: 2^24 workgroups of the smallest tile that many outputs come in
     if ((((int64_t)rows >> 6) + n_groups + 2) * (((int64_t)n_out >> 6) + 1) >= (1 << 24) - XCDS * XCD_UNIT) return EXL3_EUNSUPPORTED;
@@ -967,6 +973,7 @@ int product_checks(int32_t rows, const int32_t* offsets, int32_t n_groups, const
 
 extern "C" {
 
+using exl3::apart;
 using namespace exl3::mx;
 
 int exl3_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int32_t n, int64_t ldx, uint8_t* codes,
@@ -974,8 +981,8 @@ int exl3_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int32_t n, i
     if (bad_dtype(dtype) || bad_row(n) || rows < 0 || bad_ld(ldx, n, dtype)) return EXL3_EINVAL;
     if (rows == 0) return EXL3_OK;
     if (!x || !codes || !scales || misaligned(x) || misaligned(codes) || misaligned(scales)) return EXL3_EINVAL;
-    if (x == codes || x == scales || codes == scales) return EXL3_EINVAL;
     if (too_many_units(rows, n)) return EXL3_EUNSUPPORTED;
+    if (!apart({{codes, rows * (n / 2)}, {scales, rows * (n / BLOCK)}}, {values(x, dtype, rows, n, ldx)})) return EXL3_EINVAL;
     return quantize(dtype, x, rows, n, ldx, codes, scales, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_EHIP;
 }
 
@@ -984,8 +991,8 @@ int exl3_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t r
     if (bad_dtype(dtype) || bad_row(n) || rows < 0) return EXL3_EINVAL;
     if (rows == 0) return EXL3_OK;
     if (!out || !codes || !scales || misaligned(out) || misaligned(codes) || misaligned(scales)) return EXL3_EINVAL;
-    if (out == codes || out == scales) return EXL3_EINVAL;
     if (too_many_units(rows, n)) return EXL3_EUNSUPPORTED;
+    if (!apart({values(out, dtype, 1, rows * n, rows * n)}, {{codes, rows * (n / 2)}, {scales, rows * (n / BLOCK)}})) return EXL3_EINVAL;
     const int64_t units = rows * (n / 8);
     const dim3 grid((unsigned)((units + 256 * QUANT_UNROLL - 1) / (256 * QUANT_UNROLL)));
     const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
@@ -1006,7 +1013,10 @@ int exl3_mxfp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, int32_t r
                       void* y, int32_t dtype, void* stream) {
     const int rc = product_checks(rows, offsets, n_groups, codes, scales, n_in, n_out, y, dtype);
     if (rc <= 0) return rc;
-    if (!x_codes || !x_scales || misaligned(x_codes) || misaligned(x_scales) || y == x_codes || y == x_scales)
+    if (!x_codes || !x_scales || misaligned(x_codes) || misaligned(x_scales)) return EXL3_EINVAL;
+    const int64_t in = rows, w = (int64_t)n_groups * n_out, size = (int64_t)rows * n_out;
+    if (!apart({values(y, dtype, 1, size, size)}, {{x_codes, in * (n_in / 2)}, {x_scales, in * (n_in / BLOCK)}, {codes, w * (n_in / 2)},
+               {scales, w * (n_in / BLOCK)}, {offsets, 4 * ((int64_t)n_groups + 1)}}))
         return EXL3_EINVAL;
     const ProductParams p = {nullptr, 0, x_codes, x_scales, offsets, n_groups, rows, codes, scales, n_in, n_out, y, n_out};
     return product(dtype, p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_EHIP;
@@ -1019,9 +1029,13 @@ int exl3_mxfp4_linear(const void* x, int32_t dtype, int32_t rows, int64_t ldx, c
     if (rc < 0) return rc;
     if (bad_ld(ldx, n_in, dtype)) return EXL3_EINVAL;
     if (rc == 0) return rc;
-    if (!x || misaligned(x) || misaligned(workspace) || x == y || (workspace && (workspace == x || workspace == y))) return EXL3_EINVAL;
+    if (!x || misaligned(x) || misaligned(workspace)) return EXL3_EINVAL;
     const int64_t need = exl3_mxfp4_workspace_bytes(rows, n_groups, n_in);
     if (need > 0 && (!workspace || (int64_t)workspace_bytes < need)) return EXL3_EWORKSPACE;
+    const int64_t w = (int64_t)n_groups * n_out, size = (int64_t)rows * n_out;
+    if (!apart({values(y, dtype, 1, size, size), {workspace, need}}, {values(x, dtype, rows, n_in, ldx), {codes, w * (n_in / 2)},
+               {scales, w * (n_in / BLOCK)}, {offsets, 4 * ((int64_t)n_groups + 1)}}))
+        return EXL3_EINVAL;
     ProductParams p = {x, ldx, nullptr, nullptr, offsets, n_groups, rows, codes, scales, n_in, n_out, y, n_out};
     if (need > 0) {
         uint8_t* xc = static_cast<uint8_t*>(workspace);

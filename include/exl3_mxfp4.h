@@ -18,9 +18,11 @@
  *     NaN or an infinity has b = 255 and codes 0: it dequantises to NaN.
  *
  * Conventions: as in exl3.h (device pointers owned by the caller, 16-byte
- * aligned, results apart from the arguments, no allocation, `stream` a hipStream_t of the current device,
- * argument errors returned before any launch, no exception crosses).  Status
- * codes are exl3_status.
+ * aligned, no allocation, `stream` a hipStream_t of the current device,
+ * argument errors returned before any launch, no exception crosses).  Results and
+ * the workspace share no byte with the arguments or each other (EXL3_EINVAL where
+ * they do; the space between the rows of an x is free).  Status codes are
+ * exl3_status.
  */
 #ifndef EXL3_MXFP4_H
 #define EXL3_MXFP4_H

@@ -1,0 +1,64 @@
+"""Calls of the MXFP4 and expert operators that are refused, at the C ABI and in the
+binding.  CPU only: every case returns before anything is launched."""
+import pytest
+import torch
+
+import decode_gemm_exl3_amd as ex
+
+A = 1 << 20  # stand-ins for device addresses: no call below reaches the device
+F16, BF16, F32 = 0, 1, 2
+EINVAL = -1
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from decode_gemm_exl3_amd import moe, mxfp4
+    for f in (mxfp4._quantize, mxfp4._dequantize, mxfp4._bytes, mxfp4._matmul, mxfp4._linear, moe._bytes, moe._sort,
+              moe._gather, moe._combine, moe._backward):
+        f.load()
+    return ex.load()
+
+
+def touching(at, nbytes, mine):
+    """Addresses, 16 apart, of `mine` bytes that share a byte with `nbytes` bytes at `at`: the
+    first, one in the middle and the last."""
+    last = (nbytes - 1) // 16 * 16
+    return [at + last, at + last // 32 * 16, at, at - (mine - 1) // 16 * 16]
+
+
+# ---- results that share bytes with an argument, wherever the two begin ----
+
+def test_mxfp4_results_that_touch_arguments(lib):
+    rows, n, n_out, groups, f32 = 40, 64, 48, 3, 4
+    x_bytes, codes, scales = rows * n * f32, rows * n // 2, rows * n // 32
+
+    def quantize(x=A, c=4 * A, s=8 * A, ld=n):
+        return lib.exl3_mxfp4_quantize(x, F32, rows, n, ld, c, s, None)
+    for at in touching(A, x_bytes, codes):
+        assert quantize(c=at) == EINVAL
+    for at in touching(A, x_bytes, scales) + touching(4 * A, codes, scales):
+        assert quantize(s=at) == EINVAL
+    assert quantize(ld=2 * n, c=A + 39 * 2 * n * f32) == EINVAL         # the last of rows further apart
+    assert quantize(ld=2 * n, c=A + 5 * 2 * n * f32 - 16) == EINVAL     # from the space before row 5 into it
+    for at in touching(A, codes, x_bytes) + touching(4 * A, scales, x_bytes):
+        assert lib.exl3_mxfp4_dequantize(A, 4 * A, rows, n, at, F32, None) == EINVAL
+
+    y_bytes, w_codes, w_scales = rows * n_out * f32, groups * n_out * n // 2, groups * n_out * n // 32
+
+    def matmul(y):
+        return lib.exl3_mxfp4_matmul(A, 2 * A, rows, 3 * A, groups, 4 * A, 5 * A, n, n_out, y, F32, None)
+    for at, nbytes in ((A, codes), (2 * A, scales), (3 * A, 4 * groups + 4), (4 * A, w_codes), (5 * A, w_scales)):
+        for y in touching(at, nbytes, y_bytes):
+            assert matmul(y) == EINVAL
+
+    def linear(y=6 * A, ws=7 * A, given=1 << 30):
+        return lib.exl3_mxfp4_linear(A, F32, rows, n, 3 * A, groups, 4 * A, 5 * A, n, n_out, y, ws, given, None)
+    need = lib.exl3_mxfp4_workspace_bytes(rows, groups, n)
+    assert need > 0
+    for at, nbytes in ((A, x_bytes), (3 * A, 4 * groups + 4), (4 * A, w_codes), (5 * A, w_scales)):
+        for y in touching(at, nbytes, y_bytes):
+            assert linear(y=y) == EINVAL
+        for ws in touching(at, nbytes, need):
+            assert linear(ws=ws) == EINVAL
+    for ws in touching(6 * A, y_bytes, need):
+        assert linear(ws=ws) == EINVAL
