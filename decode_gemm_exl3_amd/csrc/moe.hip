@@ -4,6 +4,7 @@
 
 #include "../../include/exl3_moe.h"
 #include "mxfp4_device.hpp"
+#include "spans.hpp"
 
 namespace exl3 {
 namespace moe {
@@ -356,8 +357,10 @@ int rows_op(RowOp op, int dtype, const RowParams& p, hipStream_t s) {
 bool misaligned(const void* ptr, uintptr_t to = 16) { return (reinterpret_cast<uintptr_t>(ptr) & (to - 1)) != 0; }
 bool bad_dtype(int32_t d) { return d < EXL3_F16 || d > EXL3_F32; }
 
+int64_t bytes_of(int64_t values, int32_t dtype) { return values * (dtype == EXL3_F32 ? 4 : 2); }
+
 bool streams(int64_t tokens, int64_t rows_each, int64_t n, int dtype) {
-    return tokens * rows_each * n * (dtype == EXL3_F32 ? 4 : 2) >= STREAM_BYTES;
+    return bytes_of(tokens * rows_each * n, dtype) >= STREAM_BYTES;
 }
 
 // Checks shared by the three row operators: <= 0 is the call's status.
@@ -365,7 +368,7 @@ int row_checks(const void* in, int32_t dtype, int32_t n_tokens, int32_t top_k, i
                const int32_t* kept, const void* out) {
     if (bad_dtype(dtype) || n_tokens < 0 || top_k < 1 || n < 1) return EXL3_EINVAL;
     if (n_tokens == 0) return EXL3_OK;
-    if (!in || !position || !kept || !out || out == in || out == position || out == kept) return EXL3_EINVAL;
+    if (!in || !position || !kept || !out) return EXL3_EINVAL;
     if (misaligned(in) || misaligned(position) || misaligned(kept, 4) || misaligned(out)) return EXL3_EINVAL;
     // a launch takes fewer than 2^32 threads: a workgroup a token, a wave a slot
     if (n_tokens >= (1 << 24) || (int64_t)n_tokens * top_k >= (1 << 26) - 4 || n > (1 << 24)) return EXL3_EUNSUPPORTED;
@@ -397,6 +400,7 @@ bool bad_sort(int32_t n_slots, int32_t n_experts) {
 
 extern "C" {
 
+using exl3::apart;
 using namespace exl3::moe;
 
 int64_t exl3_moe_workspace_bytes(int32_t n_slots, int32_t n_experts) {
@@ -413,11 +417,12 @@ int exl3_moe_sort(const void* ids, int32_t id_bytes, int32_t n_slots, int32_t n_
     if (n_slots > 0 && (!ids || !order || !position || misaligned(ids) || misaligned(order) || misaligned(position)))
         return EXL3_EINVAL;
     if (misaligned(workspace)) return EXL3_EINVAL;
-    if (n_slots > 0 && (order == ids || position == ids || order == position || offsets == ids || offsets == order || offsets == position))
-        return EXL3_EINVAL;
     if (n_slots > (1 << 30)) return EXL3_EUNSUPPORTED;
     const int64_t need = exl3_moe_workspace_bytes(n_slots, n_experts);
     if (need > 0 && (!workspace || (int64_t)workspace_bytes < need)) return EXL3_EWORKSPACE;
+    const int64_t slots = n_slots;
+    if (!apart({{order, 4 * slots}, {position, 4 * slots}, {offsets, 4 * ((int64_t)n_experts + 1)}, {workspace, need}}, {{ids, id_bytes * slots}}))
+        return EXL3_EINVAL;
     SortParams p = {ids, id_bytes, n_slots, n_experts, 0, 0, static_cast<int*>(workspace), order, position, offsets};
     plan_sort(n_slots, n_experts, &p.chunk, &p.chunks);
     hipStream_t s = (hipStream_t)stream;
@@ -433,6 +438,8 @@ int exl3_moe_gather(const void* x, int32_t dtype, int32_t n_tokens, int32_t top_
                     const int32_t* kept, void* rows, void* stream) {
     const int rc = row_checks(x, dtype, n_tokens, top_k, n, position, kept, rows);
     if (rc <= 0) return rc;
+    const int64_t tokens = n_tokens, slots = tokens * top_k;
+    if (!apart({{rows, bytes_of(slots * n, dtype)}}, {{x, bytes_of(tokens * n, dtype)}, {position, 4 * slots}, {kept, 4}})) return EXL3_EINVAL;
     const RowParams p = {x, nullptr, n_tokens, top_k, n, position, kept, nullptr, EXL3_F32, rows, nullptr, streams(n_tokens, top_k, n, dtype)};
     return rows_op(GATHER, dtype, p, (hipStream_t)stream);
 }
@@ -444,6 +451,9 @@ int exl3_moe_combine(const void* rows, int32_t dtype, int32_t n_tokens, int32_t 
     const int rc = row_checks(rows, dtype, n_tokens, top_k, n, position, kept, y);
     if (rc <= 0) return rc;
     if (misaligned(weights)) return EXL3_EINVAL;
+    const int64_t tokens = n_tokens, slots = tokens * top_k;
+    if (!apart({{y, bytes_of(tokens * n, dtype)}}, {{rows, bytes_of(slots * n, dtype)}, {position, 4 * slots}, {kept, 4}, {weights, bytes_of(slots, weights_dtype)}}))
+        return EXL3_EINVAL;
     const RowParams p = {rows, nullptr, n_tokens, top_k, n, position, kept, weights, weights_dtype, y, nullptr, streams(n_tokens, 1, n, dtype)};
     return rows_op(COMBINE, dtype, p, (hipStream_t)stream);
 }
@@ -455,8 +465,9 @@ int exl3_moe_combine_backward(const void* dy, const void* rows, int32_t dtype, i
     const int rc = row_checks(dy, dtype, n_tokens, top_k, n, position, kept, drows);
     if (rc <= 0) return rc;
     if (!rows || !weights || !dweights || misaligned(rows) || misaligned(weights) || misaligned(dweights)) return EXL3_EINVAL;
-    if (drows == rows || drows == weights || drows == dweights || dweights == weights || dweights == rows || dweights == dy ||
-        dweights == position)
+    const int64_t tokens = n_tokens, slots = tokens * top_k;
+    if (!apart({{drows, bytes_of(slots * n, dtype)}, {dweights, bytes_of(slots, weights_dtype)}},
+               {{dy, bytes_of(tokens * n, dtype)}, {rows, bytes_of(slots * n, dtype)}, {position, 4 * slots}, {kept, 4}, {weights, bytes_of(slots, weights_dtype)}}))
         return EXL3_EINVAL;
     const RowParams p = {dy, rows, n_tokens, top_k, n, position, kept, weights, weights_dtype, drows, dweights, streams(n_tokens, top_k, n, dtype)};
     return rows_op(COMBINE_BACKWARD, dtype, p, (hipStream_t)stream);

@@ -22,8 +22,8 @@
  * twice gives its row to one of the two.  EXL3_EINVAL for null or misaligned
  * pointers (kept: 4 bytes), bad types and sizes below 1 (no tokens or slots are a
  * no-op); EXL3_EUNSUPPORTED for 2^24 tokens, 2^26 - 4 slots (sort: more than
- * 2^30) or n > 2^24.  Results are apart from the
- * arguments and from each other (EXL3_EINVAL for the same pointer).  Sums are
+ * 2^30) or n > 2^24.  Results and the workspace share no byte with the
+ * arguments or each other (EXL3_EINVAL where they do).  Sums are
  * fp32, in the order of j, rounded once; results do not depend on timing.
  */
 #ifndef EXL3_MOE_H

@@ -62,3 +62,46 @@ def test_mxfp4_results_that_touch_arguments(lib):
             assert linear(ws=ws) == EINVAL
     for ws in touching(6 * A, y_bytes, need):
         assert linear(ws=ws) == EINVAL
+
+
+def test_moe_results_that_touch_arguments(lib):
+    tokens, k, n, f32 = 20, 2, 24, 4
+    slots = tokens * k
+    x, rows, index, w = tokens * n * f32, slots * n * f32, slots * 4, slots * 4
+
+    def combine(y, weights=8 * A):
+        return lib.exl3_moe_combine(A, F32, tokens, k, n, 2 * A, 3 * A, weights, F32, y, None)
+    for at, nbytes in ((A, rows), (2 * A, index), (3 * A, 4), (8 * A, w)):
+        for y in touching(at, nbytes, x):
+            assert combine(y) == EINVAL
+    assert combine(A + 16 * n, weights=None) == EINVAL
+
+    for at, nbytes in ((A, x), (2 * A, index), (3 * A, 4)):
+        for r in touching(at, nbytes, rows):
+            assert lib.exl3_moe_gather(A, F32, tokens, k, n, 2 * A, 3 * A, r, None) == EINVAL
+
+    def backward(drows=6 * A, dweights=7 * A):
+        return lib.exl3_moe_combine_backward(A, 2 * A, F32, tokens, k, n, 3 * A, 4 * A, 5 * A, F32, drows, dweights, None)
+    for at, nbytes in ((A, x), (2 * A, rows), (3 * A, index), (4 * A, 4), (5 * A, w)):
+        for r in touching(at, nbytes, rows):
+            assert backward(drows=r) == EINVAL
+        for r in touching(at, nbytes, w):
+            assert backward(dweights=r) == EINVAL
+    for r in touching(6 * A, rows, w):
+        assert backward(dweights=r) == EINVAL
+
+    slots, experts = 3000, 20
+    need, offsets = lib.exl3_moe_workspace_bytes(slots, experts), 4 * (experts + 1)
+    assert need > 0
+
+    def sort(order=2 * A, position=3 * A, offs=4 * A, ws=5 * A):
+        return lib.exl3_moe_sort(A, 8, slots, experts, order, position, offs, ws, 1 << 30, None)
+    for at in touching(A, 8 * slots, 4 * slots) + touching(3 * A, 4 * slots, 4 * slots):
+        assert sort(order=at) == EINVAL
+    for at in touching(A, 8 * slots, 4 * slots) + touching(4 * A, offsets, 4 * slots):
+        assert sort(position=at) == EINVAL
+    for at in touching(A, 8 * slots, offsets) + touching(2 * A, 4 * slots, offsets):
+        assert sort(offs=at) == EINVAL
+    for at, nbytes in ((A, 8 * slots), (2 * A, 4 * slots), (3 * A, 4 * slots), (4 * A, offsets)):
+        for ws in touching(at, nbytes, need):
+            assert sort(ws=ws) == EINVAL
