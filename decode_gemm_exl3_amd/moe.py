@@ -12,15 +12,22 @@ Tensors:
   x, y                 : float16, bfloat16 or float32 [tokens, n]
   rows                 : the same type, [tokens * top_k, n], in the experts' order, dropped slots last
   weights              : float32, float16 or bfloat16 [tokens, top_k]
+
+Nothing here is recorded by autograd: the gradients are calls of their own,
+moe_gather_backward and moe_combine_backward.  A tensor that requires grad is
+refused where grad mode is on (an autograd.Function's forward and backward run with
+it off).
 """
 from __future__ import annotations
 
 import functools
 
 import torch
+from torch.autograd import forward_ad
 
 from . import Exl3Error
-from ._args import FLOATS, I32, I64, INDEX, SIZE, VOID, Function, call, need, on_device, on_stream, result, scratch, too_large
+from ._args import (FLOATS, I32, I64, INDEX, SIZE, VOID, Function, call, need, no_gradient, on_device,
+                    on_stream, result, scratch, too_large)
 
 MAX_EXPERTS = 1024  # EXL3_MOE_MAX_EXPERTS
 _IDS = {torch.int32: 4, torch.int64: 8}
@@ -88,7 +95,17 @@ def _matrix(t, name: str, rows: int):
         too_large(name, shape)
     if code is None or shape[0] != rows or not t.is_contiguous() or at & 15:
         need(t, name, FLOATS, (rows, n))
+    if t.requires_grad or forward_ad._current_level >= 0:
+        no_gradient(t, name)
     return n, code, at
+
+
+def _weights(t, shape):
+    """The address of the router's weights."""
+    at = need(t, "weights", FLOATS, shape)
+    if t.requires_grad or forward_ad._current_level >= 0:
+        no_gradient(t, "weights")
+    return at
 
 
 def moe_gather(x, position, offsets, rows=None, stream=None):
@@ -111,7 +128,7 @@ def moe_combine(rows, position, offsets, weights=None, y=None, stream=None):
         return on_stream(stream, moe_combine, rows, position, offsets, weights, y)
     tokens, top_k, at, kept = _places(position, offsets)
     n, code, src = _matrix(rows, "rows", tokens * top_k)
-    w = None if weights is None else need(weights, "weights", FLOATS, (tokens, top_k))
+    w = None if weights is None else _weights(weights, (tokens, top_k))
     y, dst = result(y, "y", rows, rows.dtype, (tokens, n))
     dev = rows.get_device()
     if not (dev == position.get_device() == offsets.get_device() == y.get_device() >= 0
@@ -133,7 +150,9 @@ def moe_combine_backward(dy, rows, position, offsets, weights, drows=None, dweig
     tokens, top_k, at, kept = _places(position, offsets)
     n, code, src = _matrix(rows, "rows", tokens * top_k)
     grad = need(dy, "dy", (rows.dtype,), (tokens, n))
-    w = need(weights, "weights", FLOATS, (tokens, top_k))
+    if dy.requires_grad or forward_ad._current_level >= 0:
+        no_gradient(dy, "dy")
+    w = _weights(weights, (tokens, top_k))
     drows, dst = result(drows, "drows", rows, rows.dtype, (tokens * top_k, n))
     dweights, dw = result(dweights, "dweights", weights, weights.dtype, (tokens, top_k))
     dev = rows.get_device()

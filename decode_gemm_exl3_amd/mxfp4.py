@@ -7,16 +7,21 @@ Tensors:
 A weight is codes [n_out, n_in / 2] and scales [n_out, n_in / 32]; with offsets
 (int32 [groups + 1]) there is one per group, [groups, n_out, ...], and rows
 offsets[g] .. offsets[g + 1] - 1 go through weight g.
+
+Nothing here is recorded by autograd and the products have no gradient:
+mxfp4_linear refuses an x that requires grad where grad mode is on.  mxfp4_quantize
+takes one (a layer's parameter, say), as its results are integers.
 """
 from __future__ import annotations
 
 import functools
 
 import torch
+from torch.autograd import forward_ad
 
 from . import Exl3Error, _check
-from ._args import (BYTES, I32, I64, INDEX, SIZE, VOID, Function, call, dtype_code, need, need_rows, on_device,
-                    on_stream, result, scratch, too_large)
+from ._args import (BYTES, I32, I64, INDEX, SIZE, VOID, Function, call, dtype_code, need, need_rows, no_gradient,
+                    on_device, on_stream, result, scratch, too_large)
 
 BLOCK = 32  # EXL3_MXFP4_BLOCK
 
@@ -127,6 +132,8 @@ def mxfp4_linear(x, codes, scales, offsets=None, workspace=None, y=None, stream=
     m, n_in, ld, code, src = need_rows(x, "x")
     if m >> 31:
         too_large("x", x.shape)
+    if x.requires_grad or forward_ad._current_level >= 0:
+        no_gradient(x, "x")
     c, s, at, groups, n_out = _weight(codes, scales, offsets, n_in, _blocks(n_in, "x"))
     y, o = result(y, "y", x, x.dtype, (m, n_out))
     dev = x.get_device()

@@ -35,3 +35,43 @@ def test_results_between_the_rows_of_an_input(ex, dtype):
     ex.mxfp4_linear(buf[:, :n_in], dev(codes), dev(scales), y=y)
     R.assert_product(y, R.dequantize(*R.quantize(x)), R.dequantize(codes, scales), dt)
     assert torch.equal(buf[:, :n_in].cpu(), x) and (buf[1:, n_in:] == 7).all() and (buf[0, n_in + m * n_out:] == 7).all()
+
+
+def test_routing_inside_an_autograd_function(ex):
+    """The way to train through the routing: grad mode is off inside, the gradients are the calls."""
+    rng = np.random.default_rng(2)
+    tokens, top_k, experts, n = 7, 2, 4, 24
+    _, position, offsets = ex.moe_sort(dev(rng.integers(-1, experts, (tokens, top_k)).astype(np.int32)), experts)
+
+    class Gather(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return ex.moe_gather(x, position, offsets)
+
+        @staticmethod
+        def backward(ctx, drows):
+            return ex.moe_gather_backward(drows.contiguous(), position, offsets)
+
+    class Combine(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, rows, weights):
+            ctx.save_for_backward(rows, weights)
+            return ex.moe_combine(rows, position, offsets, weights)
+
+        @staticmethod
+        def backward(ctx, dy):
+            return ex.moe_combine_backward(dy.contiguous(), ctx.saved_tensors[0], position, offsets, ctx.saved_tensors[1])
+
+    x, w, dy = (torch.from_numpy(rng.standard_normal(s)).float().cuda() for s in ((tokens, n), (tokens, top_k), (tokens, n)))
+    x.requires_grad_(), w.requires_grad_()
+    with pytest.raises(ex.Exl3Error, match="requires grad"):
+        ex.moe_gather(x, position, offsets)
+    (Combine.apply(Gather.apply(x).tanh(), w) * dy).sum().backward()
+    live = (position < offsets[-1]).double().cpu()
+    xd, wd = (t.detach().cpu().double().requires_grad_() for t in (x, w))
+    (((live * wd)[..., None] * xd.tanh()[:, None]).sum(1) * dy.cpu().double()).sum().backward()
+    # tanh, its derivative and its argument's product a few steps of fp32 each (16 allowed), then top_k products and sums; dw: n of them
+    size = ((live * wd.detach()).abs().sum(1, keepdim=True) * dy.cpu().double().abs())
+    assert ((x.grad.cpu().double() - xd.grad).abs() <= (16 + 2 * top_k) * 2.0 ** -24 * size + 1e-30).all()
+    size = (xd.detach().tanh().abs() * dy.cpu().double().abs()).sum(1, keepdim=True).expand(tokens, top_k)
+    assert ((w.grad.cpu().double() - wd.grad).abs() <= (16 + n) * 2.0 ** -24 * size).all()

@@ -105,3 +105,62 @@ def test_moe_results_that_touch_arguments(lib):
     for at, nbytes in ((A, 8 * slots), (2 * A, 4 * slots), (3 * A, 4 * slots), (4 * A, offsets)):
         for ws in touching(at, nbytes, need):
             assert sort(ws=ws) == EINVAL
+
+
+# ---- tensors that ask for a gradient: it would be lost without a word ----
+
+def differentiable_calls():
+    """(call of its floating tensors, those tensors), on the CPU: past the checks of types and sizes
+    the next refusal is that of the device."""
+    ids, at = torch.zeros((3, 2), dtype=torch.int32), torch.zeros(5, dtype=torch.int32)
+    c, s = torch.zeros((5, 32), dtype=torch.uint8), torch.zeros((5, 2), dtype=torch.uint8)
+    x, rows, w, y = torch.zeros((3, 8)), torch.zeros((6, 8)), torch.zeros((3, 2)), torch.zeros((3, 5))
+    return {
+        "moe_gather": (lambda x, r: ex.moe_gather(x, ids, at, rows=r), (x, rows)),
+        "moe_gather_backward": (lambda r, d: ex.moe_gather_backward(r, ids, at, dx=d), (rows, x)),
+        "moe_combine": (lambda r, w, y: ex.moe_combine(r, ids, at, w, y=y), (rows, w, x)),
+        "moe_combine_backward": (lambda d, r, w, dr, dw: ex.moe_combine_backward(d, r, ids, at, w, drows=dr, dweights=dw),
+                                 (x, rows, w, rows.clone(), w.clone())),
+        "mxfp4_linear": (lambda x, y: ex.mxfp4_linear(x, c, s, y=y), (torch.zeros((3, 64)), y)),
+        "mxfp4_matmul": (lambda y: ex.mxfp4_matmul(c[:3], s[:3], c, s, torch.float32, y=y), (y,)),
+        "mxfp4_dequantize": (lambda out: ex.mxfp4_dequantize(c, s, torch.float32, out=out), (torch.zeros((5, 64)),)),
+    }
+
+
+@pytest.mark.parametrize("name", differentiable_calls())
+def test_gradients_are_refused_and_not_lost(name):
+    from torch.autograd import forward_ad
+    call, tensors = differentiable_calls()[name]
+    for i, t in enumerate(tensors):
+        asks = [u.clone() for u in tensors]
+        asks[i].requires_grad_()
+        with pytest.raises(ex.Exl3Error, match="requires grad"):
+            call(*asks)
+        with torch.no_grad(), pytest.raises(ex.Exl3Error, match="must be on a GPU"):
+            call(*asks)
+        with pytest.raises(ex.Exl3Error, match="must be on a GPU"):
+            call(*(u.detach() for u in asks))
+        with forward_ad.dual_level():
+            asks = [u.clone() for u in tensors]
+            asks[i] = forward_ad.make_dual(asks[i], torch.ones_like(t))
+            with pytest.raises(ex.Exl3Error, match="tangent"):
+                call(*asks)
+            with pytest.raises(ex.Exl3Error, match="must be on a GPU"):
+                call(*tensors)
+
+
+def test_quantize_takes_a_parameter():
+    with pytest.raises(ex.Exl3Error, match="must be on a GPU"):
+        ex.mxfp4_quantize(torch.nn.Parameter(torch.zeros((3, 64))))
+
+
+def test_an_autograd_function_calls_the_operators():
+    """Inside one grad mode is off: the tensors that require grad outside are taken."""
+    ids, at = torch.zeros((3, 2), dtype=torch.int32), torch.zeros(5, dtype=torch.int32)
+
+    class Gather(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return ex.moe_gather(x, ids, at)
+    with pytest.raises(ex.Exl3Error, match="must be on a GPU"):
+        Gather.apply(torch.zeros((3, 8), requires_grad=True))
