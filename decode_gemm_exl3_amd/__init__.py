@@ -304,8 +304,10 @@ def gemm(x, trellis, sign, out_scale, bits: int, workspace=None, y=None, stream=
     return _linear("exl3_gemm", x, trellis, sign, out_scale, bits, workspace, y, stream, codebook)
 
 
-# The MXFP4 and expert operators live in modules of their own, imported on the
-# first use of one of their names (they import torch, this module does not).
+# The MXFP4 and expert operators live in modules of their own, which import torch;
+# this module does not, and neither does `import *` of it.  Their names are looked up
+# on the first use: the function itself once torch is there, until then a stand-in
+# that finds the function when it is called.
 _LAZY = {**dict.fromkeys(("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear", "mxfp4_matmul", "mxfp4_workspace_bytes"), "mxfp4"),
          **dict.fromkeys(("moe_sort", "moe_gather", "moe_gather_backward", "moe_combine", "moe_combine_backward"), "moe")}
 
@@ -314,6 +316,15 @@ def __getattr__(name: str):
     if name not in _LAZY:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     import importlib
-    value = getattr(importlib.import_module("." + _LAZY[name], __name__), name)
-    globals()[name] = value
-    return value
+    import sys
+
+    def find():
+        globals()[name] = value = getattr(importlib.import_module("." + _LAZY[name], __name__), name)
+        return value
+    if "torch" in sys.modules:
+        return find()
+
+    def later(*args, **kwargs):
+        return (globals().get(name) or find())(*args, **kwargs)
+    later.__name__ = later.__qualname__ = name
+    return later

@@ -1,10 +1,16 @@
 """Calls of the MXFP4 and expert operators that are refused, at the C ABI and in the
-binding.  CPU only: every case returns before anything is launched."""
+binding, and the package without torch.  CPU only: every case returns before
+anything is launched."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 import decode_gemm_exl3_amd as ex
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 A = 1 << 20  # stand-ins for device addresses: no call below reaches the device
 F16, BF16, F32 = 0, 1, 2
 EINVAL = -1
@@ -164,3 +170,51 @@ def test_an_autograd_function_calls_the_operators():
             return ex.moe_gather(x, ids, at)
     with pytest.raises(ex.Exl3Error, match="must be on a GPU"):
         Gather.apply(torch.zeros((3, 8), requires_grad=True))
+
+
+# ---- the package without torch ----
+
+def in_a_new_process(code, blocked=True):
+    """Runs code where torch cannot be imported (or only is not yet)."""
+    block = """
+import sys
+class Block:
+    def find_spec(self, name, path=None, target=None):
+        if name.split(".")[0] == "torch":
+            raise ModuleNotFoundError("No module named 'torch'", name="torch")
+sys.meta_path.insert(0, Block())
+""" if blocked else "import sys\n"
+    r = subprocess.run([sys.executable, "-c", block + code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_import_star_needs_no_torch():
+    in_a_new_process("""
+from decode_gemm_exl3_amd import *
+assert pack_info(256, 32, 3)["n_in"] == 256 and "torch" not in sys.modules
+assert mxfp4_linear.__name__ == "mxfp4_linear"
+try:
+    mxfp4_linear(None, None, None)
+except ModuleNotFoundError:
+    pass
+else:
+    raise AssertionError
+""")
+
+
+def test_names_taken_before_torch_is_imported_work_after():
+    in_a_new_process("""
+import decode_gemm_exl3_amd as ex
+from decode_gemm_exl3_amd import mxfp4_workspace_bytes, moe_sort
+assert "torch" not in sys.modules
+import torch
+assert mxfp4_workspace_bytes(100, 512) == ex.mxfp4_workspace_bytes(100, 512) > 0
+from decode_gemm_exl3_amd import mxfp4
+assert ex.mxfp4_linear is mxfp4.mxfp4_linear and ex.mxfp4_workspace_bytes is mxfp4.mxfp4_workspace_bytes
+try:
+    moe_sort(torch.zeros((3, 2), dtype=torch.int32), n_experts=4)
+except ex.Exl3Error as e:
+    assert "must be on a GPU" in str(e)
+else:
+    raise AssertionError
+""", blocked=False)
