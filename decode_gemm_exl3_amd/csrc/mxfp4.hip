@@ -210,7 +210,9 @@ __device__ inline Side side(const uint8_t* codes, const uint8_t* scales, int64_t
 // workgroup brings them into LDS first, while the weight is on its way: quantised
 // ones (STAGED), or values that it quantises (QUANTISED).  With HELD_SPANS two
 // workgroups fit a CU: 2048 rows in 256 groups 1024 -> 1024 35 us staged against 57
-// streamed.  A run's sums meet in LDS and are added in the order of its waves.
+// streamed; where scales start at any byte too, as they take 5 dwords a row (one row
+// 4128 -> 14336 10.4 us; 12.4 with 8 dwords and one workgroup a CU, 9.5 for 4096).
+// A run's sums meet in LDS and are added in the order of its waves.
 //
 // Block b of row r sits in 16-byte slot b ^ swizzle(r): the 16 lanes that LDS
 // serves together (rows 0-3 and 12-15 of one quarter, 4-11 of the next) then
@@ -220,14 +222,7 @@ __device__ inline Side side(const uint8_t* codes, const uint8_t* scales, int64_t
 // us, 5.0 TB/s; three tokens through two of eight experts 4096 -> 14336 in 23 us.
 // A short launch is its start, the rows' and the weight's latency and the sums:
 // one row 4096 -> 4096 in 4.7 us, of which 1.7 are the weight's at the copy rate.
-constexpr int SMALL_WAVES = 8, SMALL_RING = 2, SMALL_MAX_ROWS = 16;
 enum Rows { STREAMED, STAGED, QUANTISED };
-constexpr int HELD_SPANS = 32, MORE_HELD_SPANS = 64;
-// Rows of a tile that holds `spans` spans of them (0: none fits).
-__host__ __device__ inline int held_rows(int n_in, int spans) {
-    const int rows = spans / ((n_in + SPAN_BLOCKS * BLOCK - 1) / (SPAN_BLOCKS * BLOCK));
-    return rows < SMALL_MAX_ROWS ? rows : SMALL_MAX_ROWS;
-}
 
 __device__ inline int small_swizzle(int row) {  // rows / 4: 0 1 2 3 -> 0 2 3 1
     return (row & 3) | (((0x78 >> (row >> 2 << 1)) & 3) << 2);
@@ -235,10 +230,11 @@ __device__ inline int small_swizzle(int row) {  // rows / 4: 0 1 2 3 -> 0 2 3 1
 
 template <typename OT, Rows ROWS, int HELD, bool WHOLE>
 __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductParams p, int split) {
-    constexpr int SDW = SCALE_DWORDS<WHOLE>, SIDES = HELD ? 1 : 2, LOADS = SIDES * (4 + SDW / 4);
-    constexpr int BUF = SIDES * (256 + 4 * SDW);  // slots: codes of each side, then scales
+    constexpr int SDW = small_scale_dwords(WHOLE), SIDES = HELD ? 1 : 2, SCALE_LOADS = (16 * SDW + 63) / 64, LOADS = SIDES * (4 + SCALE_LOADS);
+    constexpr int BUF = small_buf_slots(HELD, WHOLE);  // slots: codes of each side, then scales
     constexpr int RING = SMALL_WAVES * SMALL_RING * BUF;
-    __shared__ i32x4_t lds[RING + (HELD * 17)];  // and the held rows: codes, scales
+    __shared__ i32x4_t lds[small_slots(HELD, WHOLE)];  // the rings, and the held rows: codes, scales
+    static_assert(HELD != HELD_SPANS || small_per_cu(HELD, WHOLE) == 2, "two workgroups a CU");
     static_assert(SMALL_RING * BUF >= 64, "the sums of a wave fit its ring");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
     const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, blockIdx.y, HELD ? held_rows(p.n_in, HELD) : SMALL_MAX_ROWS);
@@ -254,15 +250,18 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductPa
         Side sides[SIDES];
         sides[0] = side(p.wc, p.ws, (int64_t)t.group * p.n_out + (cols > 0 ? n0 : 0), max(cols, 1), nb);
         if constexpr (!HELD) sides[1] = side(p.xc, p.xs, t.row0, t.rows, nb);
-        uint32_t row_at[SIDES][4], scale_at[SIDES][SDW / 4], shift[SIDES];
+        uint32_t row_at[SIDES][4], scale_at[SIDES][SCALE_LOADS], shift[SIDES];
+        // load i of a side's scales: 64 of its 16 SDW dwords; the second of 80 brings
+        // some of the first's again rather than run over the end
+        auto scale_first = [](int i) { return min(64 * i, 16 * SDW - 64); };
 #pragma unroll
         for (int s = 0; s < SIDES; ++s) {
             // load i: row 4 i + lane / 16, slot lane % 16; rows behind the tile re-read its last
 #pragma unroll
             for (int i = 0; i < 4; ++i) row_at[s][i] = (uint32_t)min(4 * i + (lane >> 4), sides[s].rows - 1) * (nb * 16);
 #pragma unroll
-            for (int i = 0; i < SDW / 4; ++i)
-                scale_at[s][i] = (uint32_t)min(i * (64 / SDW) + lane / SDW, sides[s].rows - 1) * nb + sides[s].lead;
+            for (int i = 0; i < SCALE_LOADS; ++i)
+                scale_at[s][i] = (uint32_t)min((scale_first(i) + lane) / SDW, sides[s].rows - 1) * nb + sides[s].lead;
             shift[s] = ((uint32_t)min(r, sides[s].rows - 1) * nb + sides[s].lead) & 3u;
         }
         // The loads of this wave's kth span; behind its last they give zeros.
@@ -278,9 +277,9 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductPa
                                   (uint32_t)sp * 256);
                 }
 #pragma unroll
-                for (int i = 0; i < SDW / 4; ++i)
-                    load4_to_lds(sides[s].scales, reinterpret_cast<uint32_t*>(buf + SIDES * 256 + s * 4 * SDW) + i * 64,
-                                 scale_offset<WHOLE>(scale_at[s][i], lane % SDW, sp, nb), (uint32_t)sp * SPAN_BLOCKS);
+                for (int i = 0; i < SCALE_LOADS; ++i)
+                    load4_to_lds(sides[s].scales, reinterpret_cast<uint32_t*>(buf + SIDES * 256 + s * 4 * SDW) + scale_first(i),
+                                 scale_offset<WHOLE>(scale_at[s][i], (scale_first(i) + lane) % SDW, sp, nb), (uint32_t)sp * SPAN_BLOCKS);
             }
         };
         auto scales = [&](int s, int k, int left) {
@@ -828,14 +827,11 @@ inline int held_spans(int64_t rows, int n_groups, int n_in) {
 
 template <typename OT, Rows ROWS, int HELD> hipError_t launch_small(const ProductParams& p, hipStream_t s) {
     const int64_t runs = (p.n_out + 15) / 16, tiles = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, HELD ? held_rows(p.n_in, HELD) : SMALL_MAX_ROWS);
-    // As many waves a run as the card holds at once (two workgroups a CU with
-    // HELD_SPANS, else one), so that one round of workgroups starts up and quantises: one row
-    // 4096 -> 14336 takes 9.0 us at 4 waves a run and 11.2 at 8, 8192 -> 28672
-    // 25.6 at 2, 29.9 at 4 and 30.2 at 1, 14336 -> 4096 9.5 at 8 and 11.1 at 4;
-    // 64 rows in 64 groups 2048 -> 2816 19 at 1 and 63 at 8.
-    const int64_t resident = 256 * SMALL_WAVES * (HELD == HELD_SPANS ? 2 : 1), spans = (p.n_in / BLOCK + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
-    int split = 1;
-    while (split < SMALL_WAVES && split < spans && runs * tiles * split * 2 <= resident) split *= 2;
+    // As many waves a run as the card holds at once: one row 4096 -> 14336 takes 9.0
+    // us at 4 waves a run and 11.2 at 8, 8192 -> 28672 25.6 at 2, 29.9 at 4 and 30.2
+    // at 1, 14336 -> 4096 9.5 at 8 and 11.1 at 4; 64 rows in 64 groups 2048 -> 2816 19
+    // at 1 and 63 at 8.
+    const int split = small_split(p.n_out, tiles, p.n_in, HELD);
     const dim3 grid((unsigned)((runs * split + SMALL_WAVES - 1) / SMALL_WAVES), (unsigned)tiles);
     if (p.n_in % (4 * BLOCK) == 0) small_kernel<OT, ROWS, HELD, true><<<grid, SMALL_WAVES * 64, 0, s>>>(p, split);
     else small_kernel<OT, ROWS, HELD, false><<<grid, SMALL_WAVES * 64, 0, s>>>(p, split);
@@ -875,7 +871,6 @@ template <typename OT> hipError_t launch_product(const ProductParams& p, hipStre
     const int held = held_spans(p.rows, p.n_groups, p.n_in);
     if (p.x) return held == HELD_SPANS ? launch_small<OT, QUANTISED, HELD_SPANS>(p, s) : launch_small<OT, QUANTISED, MORE_HELD_SPANS>(p, s);
     if (held == HELD_SPANS) return launch_small<OT, STAGED, HELD_SPANS>(p, s);
-    constexpr int64_t CUS = 256;
     // Few rows (us, with the quantisation): 16 rows 14336 -> 4096 13.2 in small
     // tiles and 23.8 in 64 x 64 ones, 4096 -> 14336 12.6 and 12.9; 24 rows 14336 ->
     // 4096 15.2 and 24.5, but 4096 -> 14336 17 and 13.2; 8 rows of each of 64

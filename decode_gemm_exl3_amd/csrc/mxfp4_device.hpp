@@ -15,6 +15,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "mxfp4_plan.hpp"
+
 namespace exl3 {
 namespace mx {
 
@@ -26,9 +28,6 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-
-constexpr int BLOCK = 32;        // values per scale
-constexpr int SPAN_BLOCKS = 16;  // blocks per span
 
 // Type tags of the 16- and 32-bit tensors.
 struct F16 { typedef uint16_t raw; static constexpr int bytes = 2; };
