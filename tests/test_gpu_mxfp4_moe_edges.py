@@ -75,3 +75,19 @@ def test_routing_inside_an_autograd_function(ex):
     assert ((x.grad.cpu().double() - xd.grad).abs() <= (16 + 2 * top_k) * 2.0 ** -24 * size + 1e-30).all()
     size = (xd.detach().tanh().abs() * dy.cpu().double().abs()).sum(1, keepdim=True).expand(tokens, top_k)
     assert ((w.grad.cpu().double() - wd.grad).abs() <= (16 + n) * 2.0 ** -24 * size).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_long_gradients_of_weights_keep_small_terms(ex, dtype):
+    """A product of 1 and 65535 of 1.875 * 2^-25, each less than half a step next to 1.  A lane
+    sums every 16-byte piece's N values apart: n / (64 N) products a chain, each rounded once, then
+    log2(N) sums of its own and 6 over the lanes (one step more for terms of second order)."""
+    n, dt = 65536, DTYPES[dtype]
+    per_piece = 128 // torch.finfo(dt).bits
+    rows, dy = torch.full((1, n), 1.875 * 2.0 ** -12, dtype=dt, device="cuda"), torch.full((1, n), 2.0 ** -13, dtype=dt, device="cuda")
+    rows[0, 0] = 2.0 ** 13
+    pos, at = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    _, dweights = ex.moe_combine_backward(dy, rows, pos, at, torch.ones((1, 1), device="cuda"))
+    ref = float((rows.double() * dy.double()).sum())
+    steps = n // (64 * per_piece) + {4: 2, 8: 3}[per_piece] + 6 + 1
+    assert abs(float(dweights) - ref) <= steps * 2.0 ** -24 * ref
