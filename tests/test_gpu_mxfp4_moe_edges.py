@@ -91,3 +91,16 @@ def test_long_gradients_of_weights_keep_small_terms(ex, dtype):
     ref = float((rows.double() * dy.double()).sum())
     steps = n // (64 * per_piece) + {4: 2, 8: 3}[per_piece] + 6 + 1
     assert abs(float(dweights) - ref) <= steps * 2.0 ** -24 * ref
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows, n, pad", [(2051, 1056, 0), (2051, 1056, 24), (1024, 4128, 0), (257, 8192, 8)])
+def test_quantize_of_many_values(ex, dtype, rows, n, pad):
+    """From 2^18 units of 8 values on a thread takes four: bit for bit, contiguous rows and slices."""
+    assert rows * (n // 8) >= 1 << 18
+    x = R.rows(np.random.default_rng([3, rows, pad]), rows, n + pad, DTYPES[dtype]).cuda()[:, :n]
+    codes, scales = ex.mxfp4_quantize(x)
+    ref_codes, ref_scales = R.quantize(x)
+    assert np.array_equal(scales.cpu().numpy(), ref_scales) and np.array_equal(codes.cpu().numpy(), ref_codes)
+    got = ex.mxfp4_dequantize(codes, scales, DTYPES[dtype])
+    assert np.array_equal(got.cpu().double().numpy(), R.dequantize(ref_codes, ref_scales))
