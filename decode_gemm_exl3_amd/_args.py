@@ -48,7 +48,7 @@ def dtype_code(t, name: str) -> int:
 
 def too_large(name: str, shape):
     """The library takes its sizes as 32-bit numbers, and ctypes would cut longer ones."""
-    raise Exl3Error(f"{name}: shape {tuple(shape)}, sizes must be below 2^31")
+    raise Exl3Error(f"{name}: shape {tuple(shape)}, sizes must be below 2^31 and not negative")
 
 
 def need(t, name: str, dtypes, shape) -> int:

@@ -76,7 +76,7 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None)
 @functools.lru_cache(maxsize=1024)  # a size, of sizes alone: 0.6 us of a call otherwise
 def mxfp4_workspace_bytes(rows: int, n_in: int, groups: int = 1) -> int:
     """Bytes of device scratch that mxfp4_linear needs (0: none)."""
-    if max(rows, n_in, groups) >> 31:
+    if max(rows, n_in, groups) >> 31 or min(rows, n_in, groups) < -1 << 31:
         too_large("mxfp4_workspace_bytes", (rows, n_in, groups))
     n = (_bytes.bound or _bytes.load())(rows, groups, n_in)
     if n < 0:

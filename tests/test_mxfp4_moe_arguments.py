@@ -218,3 +218,10 @@ except ex.Exl3Error as e:
 else:
     raise AssertionError
 """, blocked=False)
+
+
+def test_workspace_of_sizes_far_below_zero():
+    # cut to 32 bits these would be 0 and 64
+    for bad in ((-1 << 32, 64, 1), (100, 64 - (1 << 32), 1), (100, 64, 1 - (1 << 32)), (-1 << 33, 1 << 31, 1)):
+        with pytest.raises(ex.Exl3Error, match="below 2.31 and not negative"):
+            ex.mxfp4_workspace_bytes(*bad)
