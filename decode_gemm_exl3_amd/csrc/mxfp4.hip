@@ -805,7 +805,12 @@ template <typename T> hipError_t launch_quantize(const void* x, int64_t rows, in
     return few ? launch_quantize<T, 1>(x, rows, n, ldx, codes, scales, s) : launch_quantize<T, QUANT_UNROLL>(x, rows, n, ldx, codes, scales, s);
 }
 
-// Rows that a group has on average: what a tile's height is chosen by.
+// Rows that a group has on average, those behind the last group counted: what a
+// tile's height is chosen by, as the host knows no more of a route.  An uneven one
+// takes the same height: all of 256 rows in one of 64 groups 4096 -> 2816 34 us, 64
+// tiles of 4 rows that each read that group's weight (77 for an even route, which
+// reads every weight; 11 for a product of one weight), 512 rows 2048 -> 2816 24 (42;
+// 13), 2048 rows 20 (55; 20).
 inline int64_t typical_rows(int64_t rows, int n_groups) { return (rows + n_groups - 1) / n_groups; }
 
 // The spans that a product's workgroups hold in LDS, where a tile of them holds a
@@ -815,9 +820,10 @@ inline int64_t typical_rows(int64_t rows, int n_groups) { return (rows + n_group
 // 4 rows of each of 64 groups 2048 -> 2816 32 against 39; equal at 8, and 16 rows of
 // each of 512 groups 1024 -> 1024 115 against 93).  More than HELD_SPANS: 5 rows
 // 4096 -> 14336 9.1 against 11.0, 8 rows 9.9 against 10.9, but 12 rows (96 spans)
-// 11.4 against 11.1, 8192 -> 4096 4 rows 8.6 against 9.2 and 6 rows (96) 9.9; not for
-// groups, where the larger ones take more tiles (512 rows in 64 4096 -> 2816 110
-// against 89).
+// 11.4 against 11.1, 8192 -> 4096 4 rows 8.6 against 9.2 and 6 rows (96) 9.9.  These
+// leave a CU one workgroup, so they are for one row tile, which one round of
+// workgroups covers: groups, a tile or more each, take several (512 rows in 64
+// 4096 -> 2816 110 against 89).
 inline int held_spans(int64_t rows, int n_groups, int n_in) {
     const int64_t m = typical_rows(rows, n_groups);
     if (n_groups > 1 && m > 8) return 0;
@@ -871,12 +877,13 @@ template <typename OT> hipError_t launch_product(const ProductParams& p, hipStre
     const int held = held_spans(p.rows, p.n_groups, p.n_in);
     if (p.x) return held == HELD_SPANS ? launch_small<OT, QUANTISED, HELD_SPANS>(p, s) : launch_small<OT, QUANTISED, MORE_HELD_SPANS>(p, s);
     if (held == HELD_SPANS) return launch_small<OT, STAGED, HELD_SPANS>(p, s);
-    // Few rows (us, with the quantisation): 16 rows 14336 -> 4096 13.2 in small
-    // tiles and 23.8 in 64 x 64 ones, 4096 -> 14336 12.6 and 12.9; 24 rows 14336 ->
-    // 4096 15.2 and 24.5, but 4096 -> 14336 17 and 13.2; 8 rows of each of 64
-    // groups 2048 -> 2816 50 and 61.
+    // Few rows: one row tile of 16, or two while each CU has at most one run of 16
+    // outputs of a tile (us, with the quantisation): 16 rows 14336 -> 4096 13.2 in
+    // small tiles and 23.8 in 64 x 64 ones, 4096 -> 14336 12.6 and 12.9; 24 rows
+    // 14336 -> 4096 15.2 and 24.5, but 4096 -> 14336 17 and 13.2; 8 rows of each of
+    // 64 groups 2048 -> 2816 50 and 61.
     const int64_t m = typical_rows(p.rows, p.n_groups);
-    if (p.offsets ? m <= 8 : m <= 16 || (m <= 32 && p.n_out <= 4096)) return launch_small<OT, STREAMED, 0>(p, s);
+    if (p.offsets ? m <= 8 : m <= 16 || (m <= 32 && p.n_out <= 16 * CUS)) return launch_small<OT, STREAMED, 0>(p, s);
     // 32 x 32 tiles in one round: 64 rows 14336 -> 4096 (256 of them) 15.0 us against
     // 25.4 in 64 x 64, 256 rows 4096 -> 1024 6.2 against 8.7; two rounds lose (128
     // rows 14336 -> 4096 26.1 against 24.4, 1024 -> 4096 7.3 against 5.1).

@@ -6,7 +6,9 @@
     y = moe_combine(rows, position, offsets, weights)
 
 Tensors:
-  expert_ids, position : [tokens, top_k]; ids outside 0 .. n_experts - 1 are dropped slots
+  expert_ids, position : [tokens, top_k]; ids outside 0 .. n_experts - 1 are dropped slots,
+                         position holds each of 0 .. slots - 1 once, as moe_sort makes it
+                         (a row that no entry names is not written)
   order                : int32 [tokens * top_k]
   offsets              : int32 [n_experts + 1]
   x, y                 : float16, bfloat16 or float32 [tokens, n]

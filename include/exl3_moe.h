@@ -18,13 +18,15 @@
  * where a call writes them and are not read otherwise.
  *
  * Conventions: as in exl3.h and exl3_mxfp4.h (dtype is exl3_dtype).  position
- * entries outside 0 .. slots - 1 are treated as dropped; an entry that comes
- * twice gives its row to one of the two.  EXL3_EINVAL for null or misaligned
- * pointers (kept: 4 bytes), bad types and sizes below 1 (no tokens or slots are a
- * no-op); EXL3_EUNSUPPORTED for 2^24 tokens, 2^26 - 4 slots (sort: more than
- * 2^30) or n > 2^24.  Results and the workspace share no byte with the
- * arguments or each other (EXL3_EINVAL where they do).  Sums are
- * fp32, in the order of j, rounded once; results do not depend on timing.
+ * entries outside 0 .. slots - 1 are treated as dropped.  A row that no entry names
+ * is left as it was, and one that two entries name holds values of either (as
+ * exl3_moe_sort writes position, each row has one entry).  EXL3_EINVAL for null or
+ * misaligned pointers (kept: 4 bytes), bad types and sizes below 1 (no tokens or
+ * slots are a no-op); EXL3_EUNSUPPORTED for 2^24 tokens, 2^26 - 4 slots (sort: more
+ * than 2^30) or n > 2^24.  Results and the workspace share no byte with the
+ * arguments or each other (EXL3_EINVAL where they do).  Sums are fp32, in the order
+ * of j, rounded once; where position is a permutation results do not depend on
+ * timing.
  */
 #ifndef EXL3_MOE_H
 #define EXL3_MOE_H
@@ -60,7 +62,7 @@ int exl3_moe_sort(const void* ids, int32_t id_bytes, int32_t n_slots, int32_t n_
  *   x        : dtype [n_tokens][n]
  *   position : int32 [n_tokens][top_k]
  *   kept     : device pointer to offsets[n_experts]
- *   rows     : dtype [n_tokens * top_k][n]; every row is written
+ *   rows     : dtype [n_tokens * top_k][n]; every row that position names is written
  * Its gradient, dx[t] = sum over j of drows[position[t][j]], is
  * exl3_moe_combine without weights.
  */
@@ -81,7 +83,7 @@ int exl3_moe_combine(const void* rows, int32_t dtype, int32_t n_tokens, int32_t 
  * exl3_moe_combine_backward: the gradients of exl3_moe_combine,
  *   drows[position[t][j]] = weights[t][j] * dy[t]        (zero for a dropped slot)
  *   dweights[t][j]        = sum over c of rows[position[t][j]][c] * dy[t][c]   (likewise)
- *   drows    : dtype [n_tokens * top_k][n]; every row is written
+ *   drows    : dtype [n_tokens * top_k][n]; every row that position names is written
  *   dweights : weights_dtype [n_tokens][top_k], overwritten
  */
 int exl3_moe_combine_backward(const void* dy, const void* rows, int32_t dtype, int32_t n_tokens, int32_t top_k,

@@ -21,8 +21,9 @@
  * aligned, no allocation, `stream` a hipStream_t of the current device,
  * argument errors returned before any launch, no exception crosses).  Results and
  * the workspace share no byte with the arguments or each other (EXL3_EINVAL where
- * they do; the space between the rows of an x is free).  Status codes are
- * exl3_status.
+ * they do; the space between the rows of an x is free).  Rows r .. of a weight are
+ * one too where its scales are still 16-byte aligned: for r a multiple of 16, or any
+ * r where n_in % 512 == 0.  Status codes are exl3_status.
  */
 #ifndef EXL3_MXFP4_H
 #define EXL3_MXFP4_H
@@ -58,8 +59,10 @@ int exl3_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int32_t n, i
 
 /*
  * exl3_mxfp4_dequantize: codes and scales to the values they stand for, rounded
- * to dtype (exact in fp32 and bf16 for every scale; in fp16 for what was
- * quantised from fp16).  out: dtype [rows][n], overwritten.  Errors as above.
+ * to dtype.  Exact in fp32 and bf16 for scale bytes up to 252; at 253 and 254
+ * magnitudes of 2^128 and more become infinities, and 255 is NaN.  In fp16 exact
+ * for what was quantised from fp16.  out: dtype [rows][n], overwritten.  Errors as
+ * above.
  */
 int exl3_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t n, void* out,
                           int32_t dtype, void* stream);
