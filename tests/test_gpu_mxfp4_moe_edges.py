@@ -104,3 +104,64 @@ def test_quantize_of_many_values(ex, dtype, rows, n, pad):
     assert np.array_equal(scales.cpu().numpy(), ref_scales) and np.array_equal(codes.cpu().numpy(), ref_codes)
     got = ex.mxfp4_dequantize(codes, scales, DTYPES[dtype])
     assert np.array_equal(got.cpu().double().numpy(), R.dequantize(ref_codes, ref_scales))
+
+
+@pytest.mark.parametrize("m, n_out, n_in", [(1, 256, 96), (4, 256, 512), (16, 256, 672), (40, 256, 96), (256, 256, 96), (600, 256, 288),
+                                            (2048, 2048, 256)])
+@pytest.mark.parametrize("x_code, w_code", [(2, 2), (7, 15), (1, 3), (0, 7)])
+def test_product_of_every_pair_of_scales(ex, m, n_out, n_in, x_code, w_code):
+    """One product a result, of any scales: exact down to fp32's subnormals, infinite from 2^128 on, NaN for 255."""
+    rng = np.random.default_rng([4, m])
+    at = 17 if n_in < 200 else 130  # an odd column
+    xs, ws = (rng.permutation(256)[:m] if m < 256 else np.arange(m) % 256), np.arange(n_out) % 256
+    xc, wc = np.zeros((m, n_in // 2), np.uint8), np.zeros((n_out, n_in // 2), np.uint8)
+    xc[:, at // 2], wc[:, at // 2] = x_code << 4 * (at & 1), w_code << 4 * (at & 1)
+    x_scales, w_scales = np.full((m, n_in // 32), 127, np.uint8), np.full((n_out, n_in // 32), 127, np.uint8)
+    x_scales[:, at // 32], w_scales[:, at // 32] = xs, ws
+    y = ex.mxfp4_matmul(dev(xc), dev(x_scales), dev(wc), dev(w_scales), torch.float32).cpu().numpy()
+    value = R.VALUES[x_code] * R.VALUES[w_code & 7] * (-1 if w_code & 8 else 1)
+    with np.errstate(over="ignore", under="ignore"):
+        ref = np.ldexp(value, xs[:, None] + ws[None, :] - 254).astype(np.float32)
+    ref[xs == 255], ref[:, ws == 255] = np.nan, np.nan
+    assert np.array_equal(y, ref, equal_nan=True)
+
+
+def test_calls_on_two_streams_at_once(ex):
+    rng = np.random.default_rng(5)
+    codes, scales = (dev(a) for a in R.weight(rng, 512, 1056))
+    xs = [R.rows(rng, m, 1056, torch.bfloat16).cuda() for m in (300, 200)]
+    ids = [dev(rng.integers(-1, 40, (3000, 2)).astype(np.int32)) for _ in range(2)]
+    refs = [(ex.mxfp4_linear(x, codes, scales), *ex.moe_sort(i, 40)) for x, i in zip(xs, ids)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(8):
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                got[k].append((ex.mxfp4_linear(xs[k], codes, scales), *ex.moe_sort(ids[k], 40)))
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        for outs in got[k]:
+            assert all(torch.equal(a, b) for a, b in zip(outs, refs[k]))
+
+
+def test_captured_sort_of_many_slots(ex):
+    rng = np.random.default_rng(6)
+    cases = [rng.integers(-2, 70, (2500, 2)).astype(np.int32) for _ in range(4)]
+    refs = [R.sort(ids, 64) for ids in cases]
+    held = dev(cases[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ex.moe_sort(held, 64)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = ex.moe_sort(held, 64)
+    for i in (1, 2, 3, 0, 2):
+        held.copy_(dev(cases[i]))
+        graph.replay()
+        eager = ex.moe_sort(dev(cases[(i + 1) % 4]), 64)
+        torch.cuda.synchronize()
+        for out, ref in ((got, refs[i]), (eager, refs[(i + 1) % 4])):
+            assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(out, ref))
