@@ -32,7 +32,7 @@ template <typename T> __device__ inline uint32_t quantize_quad(const uint32_t (&
 }
 
 // Loads in flight a thread: four, or one where that leaves most CUs without a
-// workgroup (13 x 14336 bf16 values: 2.4 us against 3.4).
+// workgroup (13 x 14336 bf16 values: 1 us less; 1.9 from a graph, 2.8 traced).
 constexpr int QUANT_UNROLL = 4;
 
 template <typename T, bool FLAT, int U>
@@ -599,13 +599,14 @@ __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int 
 // Where rows start at any byte (WHOLE false: n_in % 128 != 0) the eight aligned
 // dwords that hold them are staged and two of them meet in an alignbyte.
 //
-// 256 x 256 tiles (one workgroup a CU): 8192^3 in 264 us, 4.2 PFLOP/s, half of the
-// 8.3 that the matrix cores issue alone; 2048 rows 8192 -> 28672 in 260 us with
-// the 128 x 128 tiles of the last columns.  The card's power bounds them: the
-// matrix cores are busy 53 % of the cycles at 1.57 GHz, and zeros instead of random codes
-// run 20 to 30 % faster.  128 x 128 tiles (two a CU): the address unit (64 bytes a
-// cycle) and the first touch of each line; 16384 rows in 64 groups 2048 -> 2816 in
-// 107 to 125 us, waiting for data half of the time (131 without a pause between calls).
+// 256 x 256 tiles (one workgroup a CU): 8192^3 in 260 us, 4.2 PFLOP/s, half of the
+// 8.4 that the matrix cores issue alone; 2048 rows 8192 -> 28672 in 260 us with the
+// 128 x 128 tiles of the last columns.  The matrix cores are busy 57 % of the cycles
+// at 1.66 GHz: one wave a SIMD waits at each stage's border with nothing else to
+// run, and the clock falls under load (zeros for codes: 2.11 GHz, 15 % faster).
+// 128 x 128 tiles (two a CU): 16384 rows in 64 groups 2048 -> 2816 in 105 to 131 us.
+// No unit is full (matrix cores busy 26 %, address units 57 %); waves wait for data or
+// a barrier 44 % of their time, as a stage's loads have one stage to land.
 
 constexpr int STAGE_BLOCKS = 8;
 

@@ -110,7 +110,7 @@ template <int J> __device__ inline f32x4_t mfma(const i32x4_t a, uint32_t sa, co
 // D += A * B for 32 x 32 x 64: lane l holds row l % 32 and the (l / 32)th of the
 // two blocks of 64 inputs; accumulator i is row 8 (i / 4) + 4 (l / 32) + i % 4 of
 // the first operand against row l % 32 of the second.  One wave can issue this
-// form at the matrix core's full rate (32 cycles each, 8.3 PFLOP/s measured over
+// form at the matrix core's full rate (32 cycles each, 8.4 PFLOP/s measured over
 // the card), the 16 x 16 x 128 form only every 29 cycles instead of 16.
 template <int J> __device__ inline f32x16_t mfma32(const i32x4_t a, uint32_t sa, const i32x4_t b, uint32_t sb, f32x16_t c) {
     const i32x8_t a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
