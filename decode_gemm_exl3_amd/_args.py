@@ -145,11 +145,17 @@ def call(fn: Function, dev: int, *args) -> None:
 
 def on_stream(stream, fn, first, *args):
     """fn(first, *args) with `stream` the current one, so that results and scratch
-    come from its memory as well and nothing of another stream is written early."""
+    come from its memory as well and nothing of another stream is written early.  The
+    tensors are marked as used there: one that is dropped right after the call (a
+    temporary, say) keeps its memory until `stream` has passed it."""
     if isinstance(first, torch.Tensor) and first.get_device() >= 0 and first.get_device() != stream.device_index:
         raise Exl3Error(f"{fn.__name__}: the stream is of GPU {stream.device_index}, the tensors are on GPU {first.get_device()}")
     with torch.cuda.stream(stream):
-        return fn(first, *args)
+        out = fn(first, *args)
+    for t in (first, *args):
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+    return out
 
 
 def scratch(workspace, nbytes: int, like):

@@ -165,3 +165,46 @@ def test_captured_sort_of_many_slots(ex):
         torch.cuda.synchronize()
         for out, ref in ((got, refs[i]), (eager, refs[(i + 1) % 4])):
             assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(out, ref))
+
+
+def test_temporaries_of_a_call_on_a_given_stream(ex):
+    """A tensor dropped right after a call with stream= is not handed out again before that stream has read it."""
+    rng = np.random.default_rng(7)
+    tokens, top_k, n = 600, 2, 512
+    codes, scales = (dev(a) for a in R.weight(rng, 256, n))
+    _, position, offsets = ex.moe_sort(dev(rng.integers(0, 9, (tokens, top_k)).astype(np.int32)), 9)
+    x, w = R.rows(rng, tokens, n, torch.bfloat16).cuda(), torch.rand((tokens, top_k), device="cuda")
+    rows = ex.moe_gather(x, position, offsets)
+    calls = [(lambda x, s: ex.mxfp4_linear(x, codes, scales, stream=s), (x,)), (lambda x, s: ex.mxfp4_quantize(x, stream=s)[0], (x,)),
+             (lambda x, p, s: ex.moe_gather(x, p, offsets, stream=s), (x, position)),
+             (lambda r, w, s: ex.moe_combine(r, position, offsets, w, stream=s), (rows, w))]
+    refs = [call(*args, None) for call, args in calls]
+    busy, side = torch.ones((4096, 4096), device="cuda"), torch.cuda.Stream()
+    for (call, args), ref in zip(calls, refs):
+        temporaries = [t.clone() for t in args]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(20):  # in front of the call
+                busy @ busy
+        got = call(*temporaries, side)
+        del temporaries
+        others = [torch.ones_like(t) for t in args for _ in range(4)]  # on the current stream, at once
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref) and all(bool((t == 1).all()) for t in others)
+
+
+def test_captured_calls_on_a_given_stream(ex):
+    rng = np.random.default_rng(8)
+    codes, scales = (dev(a) for a in R.weight(rng, 64, 512))
+    xs = [R.rows(rng, 200, 512, torch.float16).cuda() for _ in range(3)]
+    refs = [ex.mxfp4_linear(x, codes, scales) for x in xs]
+    held, graph = xs[0].clone(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        y = ex.mxfp4_linear(held, codes, scales, stream=torch.cuda.current_stream())
+    for i in (1, 2, 0, 1):
+        held.copy_(xs[i])
+        graph.replay()
+        eager = ex.mxfp4_linear(xs[(i + 1) % 3].clone(), codes, scales, stream=torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        assert torch.equal(y, refs[i]) and torch.equal(eager, refs[(i + 1) % 3])

@@ -1,6 +1,7 @@
 """Calls of the MXFP4 and expert operators that are refused, at the C ABI and in the
 binding, and the package without torch.  CPU only: every case returns before
 anything is launched."""
+import contextlib
 import os
 import subprocess
 import sys
@@ -225,3 +226,17 @@ def test_workspace_of_sizes_far_below_zero():
     for bad in ((-1 << 32, 64, 1), (100, 64 - (1 << 32), 1), (100, 64, 1 - (1 << 32)), (-1 << 33, 1 << 31, 1)):
         with pytest.raises(ex.Exl3Error, match="below 2.31 and not negative"):
             ex.mxfp4_workspace_bytes(*bad)
+
+
+def test_tensors_of_a_call_on_a_given_stream_are_marked(monkeypatch):
+    """Each tensor is recorded on the stream that uses it: its memory is not handed out again before."""
+    from decode_gemm_exl3_amd import _args
+
+    class Stream:
+        device_index = 0
+    marked, stream = [], Stream()
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: marked.append((t, s)))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    a, b, c = torch.zeros(1), torch.zeros(2), torch.zeros(3)
+    assert _args.on_stream(stream, lambda *args: len(args), a, None, b, 7, torch.float16, c) == 6
+    assert [(t is u, s is stream) for (t, s), u in zip(marked, (a, b, c))] == [(True, True)] * 3 and len(marked) == 3
