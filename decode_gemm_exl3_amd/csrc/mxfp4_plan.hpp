@@ -19,7 +19,7 @@ constexpr int CUS = 256, CU_LDS = 160 * 1024;
 constexpr int SMALL_WAVES = 8, SMALL_RING = 2, SMALL_MAX_ROWS = 16;
 constexpr int HELD_SPANS = 32, MORE_HELD_SPANS = 64;
 
-EXL3_PLAN int64_t spans_of(int n_in) { return (n_in + SPAN_BLOCKS * BLOCK - 1) / (SPAN_BLOCKS * BLOCK); }
+EXL3_PLAN int64_t spans_of(int n_in) { return ((int64_t)n_in + SPAN_BLOCKS * BLOCK - 1) / (SPAN_BLOCKS * BLOCK); }
 
 // Rows of a tile that holds `spans` spans of them (0: none fits).
 EXL3_PLAN int held_rows(int n_in, int spans) {

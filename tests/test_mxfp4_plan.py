@@ -13,6 +13,7 @@ PROGRAM = r"""
 #include <initializer_list>
 #include "mxfp4_plan.hpp"
 using namespace exl3::mx;
+static_assert(spans_of(2147483616) == 4194304 && held_rows(2147483616, 64) == 0, "no sum past 32 bits");
 int main() {
     for (int held : {0, HELD_SPANS, MORE_HELD_SPANS})
         for (int whole : {0, 1}) printf("lds %d %d %d %d\n", held, whole, small_slots(held, whole) * 16, small_per_cu(held, whole));
