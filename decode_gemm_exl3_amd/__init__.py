@@ -22,7 +22,9 @@ import os
 __all__ = ["Exl3Error", "lib_path", "load", "pack_info", "Workspace", "decode_tile", "gemv", "gemv_multi",
            "gemm", "linear", "linear_noalloc", "status_string", "MAX_PROJ", "CODEBOOK_BYTE_SUM", "bits_arg", "encode_slot_bytes",
            "encode_tiles", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear", "mxfp4_matmul", "mxfp4_workspace_bytes",
-           "moe_sort", "moe_gather", "moe_gather_backward", "moe_combine", "moe_combine_backward"]
+           "moe_sort", "moe_gather", "moe_gather_backward", "moe_combine", "moe_combine_backward", "moe_balance_loss",
+           "moe_balance_loss_backward", "int8_quantize", "int8_dequantize", "int8_rms_norm", "int8_linear", "int8_matmul",
+           "int8_workspace_bytes"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -304,12 +306,14 @@ def gemm(x, trellis, sign, out_scale, bits: int, workspace=None, y=None, stream=
     return _linear("exl3_gemm", x, trellis, sign, out_scale, bits, workspace, y, stream, codebook)
 
 
-# The MXFP4 and expert operators live in modules of their own, which import torch;
+# The MXFP4, 8-bit and expert operators live in modules of their own, which import torch;
 # this module does not, and neither does `import *` of it.  Their names are looked up
 # on the first use: the function itself once torch is there, until then a stand-in
 # that finds the function when it is called.
 _LAZY = {**dict.fromkeys(("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear", "mxfp4_matmul", "mxfp4_workspace_bytes"), "mxfp4"),
-         **dict.fromkeys(("moe_sort", "moe_gather", "moe_gather_backward", "moe_combine", "moe_combine_backward"), "moe")}
+         **dict.fromkeys(("int8_quantize", "int8_dequantize", "int8_rms_norm", "int8_linear", "int8_matmul", "int8_workspace_bytes"), "int8"),
+         **dict.fromkeys(("moe_sort", "moe_gather", "moe_gather_backward", "moe_combine", "moe_combine_backward", "moe_balance_loss",
+                          "moe_balance_loss_backward"), "moe")}
 
 
 def __getattr__(name: str):

@@ -1,4 +1,4 @@
-"""Argument checks shared by the bindings of the MXFP4 and expert operators.
+"""Argument checks shared by the bindings of the MXFP4, 8-bit and expert operators.
 
 The library reads and writes raw device memory, so every tensor is checked for
 element type, shape, contiguity, 16-byte alignment and device before a call
@@ -51,12 +51,12 @@ def too_large(name: str, shape):
     raise Exl3Error(f"{name}: shape {tuple(shape)}, sizes must be below 2^31 and not negative")
 
 
-def need(t, name: str, dtypes, shape) -> int:
+def need(t, name: str, dtypes, shape, align: int = 16) -> int:
     """Checks all but the device; returns the address."""
     if not isinstance(t, torch.Tensor):
         raise Exl3Error(f"{name}: expected a torch tensor")
     at = t.data_ptr()
-    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and not at & 15:
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and not at & (align - 1):
         return at
     if t.dtype not in dtypes:
         raise Exl3Error(f"{name}: dtype {t.dtype}, expected one of {tuple(str(d) for d in dtypes)}")
@@ -64,7 +64,7 @@ def need(t, name: str, dtypes, shape) -> int:
         raise Exl3Error(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise Exl3Error(f"{name}: must be contiguous")
-    raise Exl3Error(f"{name}: data must be 16-byte aligned (a view at an offset is not)")
+    raise Exl3Error(f"{name}: data must be {align}-byte aligned (a view at an offset is not)")
 
 
 def no_gradient(t, name: str) -> None:
@@ -73,18 +73,18 @@ def no_gradient(t, name: str) -> None:
     requires grad or a level of forward mode is open: 0.1 us of a call, not 0.4.)"""
     if t.requires_grad and torch.is_grad_enabled():
         raise Exl3Error(f"{name}: requires grad, but the results are outside autograd's graph: pass it detached or call under "
-                        "torch.no_grad() (moe_gather_backward and moe_combine_backward are the gradients there are)")
+                        "torch.no_grad() (moe_gather_backward, moe_combine_backward and moe_balance_loss_backward are the gradients there are)")
     if forward_ad.unpack_dual(t).tangent is not None:
         raise Exl3Error(f"{name}: carries a tangent, but the results are outside autograd's graph")
 
 
-def result(t, name: str, like, dtype, shape):
+def result(t, name: str, like, dtype, shape, align: int = 16):
     """A given output, checked, or a new one beside `like`; with its address."""
     if t is None:
         # sizes one by one, and no dtype where it is the same: 1.2 us against 1.6
         t = like.new_empty(*shape) if dtype is like.dtype else like.new_empty(*shape, dtype=dtype)
         return t, t.data_ptr()
-    at = need(t, name, (dtype,), shape)
+    at = need(t, name, (dtype,), shape, align)
     if t.requires_grad or forward_ad._current_level >= 0:
         no_gradient(t, name)
     return t, at

@@ -7,7 +7,8 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libexl3.so")
-SOURCES = ["exl3_api.hip", "exl3_kernels.hip", "exl3_gemm.hip", "exl3_encode.hip", "mxfp4.hip", "moe.hip"]
+SOURCES = ["exl3_api.hip", "exl3_kernels.hip", "exl3_gemm.hip", "exl3_encode.hip", "mxfp4.hip", "moe.hip",
+           "int8.hip", "int8_rows.hip", "balance.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

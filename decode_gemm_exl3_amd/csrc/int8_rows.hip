@@ -1,0 +1,311 @@
+// int8_rows.hip - rows of values to 8-bit codes and scales, with a norm before them or
+// without, and codes back to values (gfx950).
+#include <hip/hip_runtime.h>
+
+#include "int8_internal.hpp"
+#include "pieces_device.hpp"
+
+namespace exl3 {
+namespace i8 {
+
+using namespace mx;  // element types, pieces
+
+// ---- quantise, norm ----
+//
+// One pass over a row finds its largest magnitude A (and, for a norm, the sum of its
+// squares), the codes follow from the values kept in registers.  A norm's codes are
+// round(127 u / A) of u = h * weight: the row's 1 / rms is in u and A alike and cancels, so
+// it enters the scale alone.
+//
+// The codes are exact: q = u * fl(127 / A) is within 1.6e-5 of 127 u / A (two roundings
+// of a number up to 127), so only a piece that holds a q nearer than 2^-15 to a tie is
+// rounded again, from the quotient in 64 bits.  Ties are common in 16-bit types (u = A / 2
+// is one for every A).
+//
+// Squares are summed in 64 bits: those of fp32 and bf16 values pass the range of fp32.
+
+// Codes of the N values u of a piece, in N / 4 dwords.
+template <int N> __device__ inline void code_piece(const float (&u)[N], float largest, float inverse, uint32_t (&out)[N / 4]) {
+    constexpr float ROUND = 12582912.f;  // 1.5 * 2^23: a sum's low byte is the rounded value
+    uint32_t bits[N];
+    float nearest = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float q = u[i] * inverse, m = q + ROUND;
+        bits[i] = __builtin_bit_cast(uint32_t, m);
+        nearest = fmaxf(nearest, fabsf(q - (m - ROUND)));
+    }
+    // largest below 2^-100: 127 / largest may be infinite
+    if (nearest > 0.5f - 0x1p-15f || largest < 0x1p-100f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            bits[i] = largest > 0.f ? (uint32_t)(int)__builtin_rint(127.0 * (double)u[i] / (double)largest) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        out[i / 4] = (bits[i] & 255u) | ((bits[i + 1] & 255u) << 8) | ((bits[i + 2] & 255u) << 16) | (bits[i + 3] << 24);
+}
+
+// The largest of v, and the sum of s, over the lanes of a wave.
+__device__ inline uint32_t wave_max(uint32_t v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)v, d);
+        v = v > o ? v : o;
+    }
+    return v;
+}
+__device__ inline double wave_sum(double s) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
+    return s;
+}
+
+// N consecutive weights from column c on.
+template <int N> __device__ inline void load_weights(const void* w, int dtype, int c, float (&out)[N]) {
+    if (dtype == EXL3_F32) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(w) + c + i);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) out[i + k] = v[k];
+        }
+    } else {
+        uint32_t r[N / 2];
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(w) + c);
+        if constexpr (N == 8) {
+            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(src);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r[k] = v[k];
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(src);
+            r[0] = v.x;
+            r[1] = v.y;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint16_t b = (uint16_t)(r[i / 2] >> (16 * (i & 1)));
+            out[i] = dtype == EXL3_F16 ? to_f32(F16{}, b) : to_f32(BF16{}, b);
+        }
+    }
+}
+
+// WAVES waves a row (1: four rows a workgroup), P pieces of 16 bytes a thread; P == 0:
+// longer rows, read once for the sums and again for the codes.
+template <typename T, bool NORM, int WAVES, int P>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rows_kernel(const RowsParams p) {
+    constexpr int N = 16 / T::bytes, KEPT = P > 0 ? P : 1, THREADS = WAVES * 64;
+    __shared__ uint32_t wave_amax[2][WAVES];
+    __shared__ double wave_squares[2][WAVES];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int thread = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;  // of the row
+    const int64_t step = WAVES == 1 ? (int64_t)gridDim.x * 4 : gridDim.x;
+    int parity = 0;
+    for (int64_t row = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x; row < p.rows; row += step, parity ^= 1) {
+        const int64_t x0 = row * p.ldx, r0 = row * p.ldr, o0 = row * p.n;
+        float u[KEPT][N];
+        uint32_t amax = 0;
+        double squares = 0.0;
+        // the values of a piece, before the weight; `first`: the sum is stored
+        auto values = [&](int c, bool first, float (&v)[N]) {
+            const u32x4_t a = load_piece<T, true>(p.x, x0 + c, N);
+            if (NORM && p.residual) {
+                const u32x4_t b = load_piece<T, true>(p.residual, r0 + c, N);
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = piece_value<T>(a, i) + piece_value<T>(b, i);
+                const u32x4_t h = round_piece<T>(v);
+                if (first) *reinterpret_cast<u32x4_t*>(static_cast<typename T::raw*>(p.added) + o0 + c) = h;
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = piece_value<T>(h, i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = piece_value<T>(a, i);
+            }
+        };
+        auto piece = [&](int c, bool first, float (&v)[N]) {
+            values(c, first, v);
+            if constexpr (NORM) {
+                float w[N];
+                load_weights<N>(p.weight, p.weight_dtype, c, w);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    if (first) squares = __builtin_fma((double)v[i], (double)v[i], squares);
+                    v[i] *= w[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t b = __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu;
+                amax = amax > b ? amax : b;
+            }
+        };
+        if constexpr (P > 0) {
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                const int c = (k * THREADS + thread) * N;
+                if (c < p.n) piece(c, true, u[k]);
+                else
+#pragma unroll
+                    for (int i = 0; i < N; ++i) u[k][i] = 0.f;
+            }
+        } else {
+            for (int c = thread * N; c < p.n; c += THREADS * N) piece(c, true, u[0]);
+        }
+        amax = wave_max(amax);
+        if (NORM) squares = wave_sum(squares);
+        if constexpr (WAVES > 1) {
+            if ((threadIdx.x & 63) == 0) {
+                wave_amax[parity][wave] = amax;
+                if (NORM) wave_squares[parity][wave] = squares;
+            }
+            __syncthreads();
+            amax = 0;
+            squares = 0.0;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) {
+                amax = amax > wave_amax[parity][w] ? amax : wave_amax[parity][w];
+                if (NORM) squares += wave_squares[parity][w];
+            }
+        }
+        const bool bad = amax >= 0x7F800000u;  // a NaN or an infinity
+        const float largest = __builtin_bit_cast(float, amax), inverse = 127.f / largest;
+        if (thread == 0) {
+            double scale = (double)largest / 127.0;
+            if (NORM) scale /= sqrt(squares / p.n + p.eps);
+            p.scales[row] = bad ? __builtin_nanf("") : (amax == 0 ? 0.f : (float)scale);
+        }
+        auto store = [&](int c, const float (&v)[N]) {
+            uint32_t out[N / 4];
+            if (bad) {
+#pragma unroll
+                for (int i = 0; i < N / 4; ++i) out[i] = 0;
+            } else {
+                code_piece<N>(v, largest, inverse, out);
+            }
+            uint32_t* dst = reinterpret_cast<uint32_t*>(p.codes + o0 + c);
+            if constexpr (N == 8) *reinterpret_cast<uint2*>(dst) = uint2{out[0], out[1]};
+            else *dst = out[0];
+        };
+        if constexpr (P > 0) {
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                const int c = (k * THREADS + thread) * N;
+                if (c < p.n) store(c, u[k]);
+            }
+        } else {
+            for (int c = thread * N; c < p.n; c += THREADS * N) {
+                piece(c, false, u[0]);
+                store(c, u[0]);
+            }
+        }
+    }
+}
+
+// ---- dequantise ----
+//
+// A thread makes 16 values of 16 codes.
+template <typename T, typename INDEX>
+__global__ __launch_bounds__(256) void dequantize_kernel(const int8_t* __restrict__ codes, const float* __restrict__ scales,
+                                                         int64_t units, INDEX per_row, void* __restrict__ out) {
+    constexpr int N = 16 / T::bytes;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= units) return;
+    const u32x4_t c = reinterpret_cast<const u32x4_t*>(codes)[i];
+    const float s = scales[(INDEX)i / per_row];
+#pragma unroll
+    for (int k = 0; k < 16; k += N) {
+        float v[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = rounded((float)((int)(c[(k + e) / 4] << (24 - 8 * ((k + e) & 3))) >> 24) * s);
+        reinterpret_cast<u32x4_t*>(out)[i * (16 / N) + k / N] = round_piece<T>(v);
+    }
+}
+
+// ---- launches ----
+
+template <typename T, bool NORM, int WAVES, int P> hipError_t launch(const RowsParams& p, hipStream_t s) {
+    const int64_t groups = WAVES == 1 ? (p.rows + 3) / 4 : p.rows;
+    rows_kernel<T, NORM, WAVES, P><<<(unsigned)(groups < MAX_GRID ? groups : MAX_GRID), WAVES == 1 ? 256 : WAVES * 64, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+template <typename T, bool NORM> hipError_t launch_rows(const RowsParams& p, hipStream_t s) {
+    const int pieces = p.n * T::bytes / 16;  // n < 2^24
+    if (pieces <= 64) return launch<T, NORM, 1, 1>(p, s);
+    if (pieces <= 256) return launch<T, NORM, 1, 4>(p, s);
+    if (pieces <= 1024) return launch<T, NORM, 4, 4>(p, s);
+    if (pieces <= 4096) return launch<T, NORM, 16, 4>(p, s);
+    return launch<T, NORM, 16, 0>(p, s);
+}
+
+template <bool NORM> hipError_t launch_rows(int dtype, const RowsParams& p, hipStream_t s) {
+    switch (dtype) {
+        case EXL3_F16: return launch_rows<F16, NORM>(p, s);
+        case EXL3_BF16: return launch_rows<BF16, NORM>(p, s);
+        default: return launch_rows<F32, NORM>(p, s);
+    }
+}
+
+hipError_t launch_quantize(int dtype, const RowsParams& p, hipStream_t s) { return launch_rows<false>(dtype, p, s); }
+
+template <typename T> hipError_t launch_dequantize(const int8_t* codes, const float* scales, int64_t rows, int n, void* out, hipStream_t s) {
+    const int64_t units = rows * (n / 16);
+    const unsigned grid = (unsigned)((units + 255) / 256);
+    if (units < (1ll << 32)) dequantize_kernel<T, uint32_t><<<grid, 256, 0, s>>>(codes, scales, units, (uint32_t)(n / 16), out);
+    else dequantize_kernel<T, int64_t><<<grid, 256, 0, s>>>(codes, scales, units, (int64_t)(n / 16), out);
+    return hipGetLastError();
+}
+
+}  // namespace i8
+}  // namespace exl3
+
+extern "C" {
+
+using exl3::apart;
+using exl3::Span;
+using namespace exl3::i8;
+
+int exl3_int8_quantize(const void* x, int32_t dtype, int64_t rows, int32_t n, int64_t ldx, int8_t* codes,
+                       float* scales, void* stream) {
+    if (bad_dtype(dtype) || bad_row(n) || rows < 0 || bad_ld(ldx, n, dtype)) return EXL3_EINVAL;
+    if (rows == 0) return EXL3_OK;
+    if (!x || !codes || !scales || misaligned(x) || misaligned(codes) || misaligned(scales, 4)) return EXL3_EINVAL;
+    if (n > MAX_ROW || rows > MAX_ROWS) return EXL3_EUNSUPPORTED;
+    if (!apart({{codes, rows * n}, {scales, rows * 4}}, {values(x, dtype, rows, n, ldx)})) return EXL3_EINVAL;
+    const RowsParams p = {x, ldx, nullptr, 0, nullptr, 0, 0.0, rows, n, codes, scales, nullptr};
+    return launch_quantize(dtype, p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_EHIP;
+}
+
+int exl3_int8_dequantize(const int8_t* codes, const float* scales, int64_t rows, int32_t n, void* out, int32_t dtype,
+                         void* stream) {
+    if (bad_dtype(dtype) || bad_row(n) || rows < 0) return EXL3_EINVAL;
+    if (rows == 0) return EXL3_OK;
+    if (!out || !codes || !scales || misaligned(out) || misaligned(codes) || misaligned(scales, 4)) return EXL3_EINVAL;
+    // 2^37 values: 2^25 - 1 workgroups of 256 pieces would be too many threads for a launch
+    if (n > MAX_ROW || rows > MAX_ROWS || rows * (n / 16) > (int64_t)0xFFFFFF * 256) return EXL3_EUNSUPPORTED;
+    if (!apart({values(out, dtype, 1, rows * n, rows * n)}, {{codes, rows * n}, {scales, rows * 4}})) return EXL3_EINVAL;
+    hipStream_t s = (hipStream_t)stream;
+    const hipError_t e = dtype == EXL3_F16    ? launch_dequantize<exl3::mx::F16>(codes, scales, rows, n, out, s)
+                         : dtype == EXL3_BF16 ? launch_dequantize<exl3::mx::BF16>(codes, scales, rows, n, out, s)
+                                              : launch_dequantize<exl3::mx::F32>(codes, scales, rows, n, out, s);
+    return e == hipSuccess ? EXL3_OK : EXL3_EHIP;
+}
+
+int exl3_int8_rms_norm(const void* x, int32_t dtype, int64_t rows, int32_t n, int64_t ldx, const void* residual,
+                       int64_t ldr, const void* weight, int32_t weight_dtype, double eps, int8_t* codes, float* scales,
+                       void* added, void* stream) {
+    if (bad_dtype(dtype) || bad_dtype(weight_dtype) || bad_row(n) || rows < 0 || bad_ld(ldx, n, dtype)) return EXL3_EINVAL;
+    if (!(eps >= 0.0 && eps <= 1.7976931348623157e308) || !residual != !added || (residual && bad_ld(ldr, n, dtype))) return EXL3_EINVAL;
+    if (rows == 0) return EXL3_OK;
+    if (!x || !weight || !codes || !scales || misaligned(x) || misaligned(residual) || misaligned(weight) || misaligned(codes) ||
+        misaligned(scales, 4) || misaligned(added))
+        return EXL3_EINVAL;
+    if (n > MAX_ROW || rows > MAX_ROWS) return EXL3_EUNSUPPORTED;
+    if (!apart({{codes, rows * n}, {scales, rows * 4}, values(added, dtype, 1, rows * n, rows * n)},
+               {values(x, dtype, rows, n, ldx), values(residual, dtype, rows, n, ldr), values(weight, weight_dtype, 1, n, n)}))
+        return EXL3_EINVAL;
+    const RowsParams p = {x, ldx, residual, ldr, weight, weight_dtype, eps, rows, n, codes, scales, added};
+    return launch_rows<true>(dtype, p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_EHIP;
+}
+
+}  // extern "C"

@@ -1,9 +1,11 @@
-"""Mixture-of-experts routing (include/exl3_moe.h).
+"""Mixture-of-experts routing (include/exl3_moe.h) and the loss that evens it out
+(include/exl3_balance.h).
 
     order, position, offsets = moe_sort(expert_ids, n_experts)
     rows = moe_gather(x, position, offsets)
     rows = mxfp4_linear(rows, codes, scales, offsets=offsets)     # one weight per expert
     y = moe_combine(rows, position, offsets, weights)
+    loss, counts = moe_balance_loss(logits, expert_ids)           # of the router's logits [tokens, n_experts]
 
 Tensors:
   expert_ids, position : [tokens, top_k]; ids outside 0 .. n_experts - 1 are dropped slots,
@@ -16,12 +18,13 @@ Tensors:
   weights              : float32, float16 or bfloat16 [tokens, top_k]
 
 Nothing here is recorded by autograd: the gradients are calls of their own,
-moe_gather_backward and moe_combine_backward.  A tensor that requires grad is
+moe_gather_backward, moe_combine_backward and moe_balance_loss_backward.  A tensor that requires grad is
 refused where grad mode is on (an autograd.Function's forward and backward run with
 it off).
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 
 import torch
@@ -39,6 +42,11 @@ _sort = Function("exl3_moe_sort", VOID, I32, I32, I32, VOID, VOID, VOID, VOID, S
 _gather = Function("exl3_moe_gather", VOID, I32, I32, I32, I32, VOID, VOID, VOID, VOID)
 _combine = Function("exl3_moe_combine", VOID, I32, I32, I32, I32, VOID, VOID, VOID, I32, VOID, VOID)
 _backward = Function("exl3_moe_combine_backward", VOID, VOID, I32, I32, I32, I32, VOID, VOID, VOID, I32, VOID, VOID, VOID)
+
+_balance_bytes = Function("exl3_moe_balance_workspace_bytes", I32, I32, restype=I64)
+_balance = Function("exl3_moe_balance_loss", VOID, I32, VOID, I32, I32, I32, I32, ctypes.c_double, VOID, VOID, VOID, SIZE, VOID)
+_balance_backward = Function("exl3_moe_balance_loss_backward", VOID, VOID, I32, VOID, I32, I32, I32, I32, VOID, ctypes.c_double,
+                             VOID, VOID)
 
 
 @functools.lru_cache(maxsize=1024)  # a size, of sizes alone
@@ -163,3 +171,69 @@ def moe_combine_backward(dy, rows, position, offsets, weights, drows=None, dweig
         on_device(dev, rows=rows, dy=dy, position=position, offsets=offsets, weights=weights, drows=drows, dweights=dweights)
     call(_backward, dev, grad, src, code, tokens, top_k, n, at, kept, w, FLOATS[weights.dtype], dst, dw)
     return drows, dweights
+
+
+@functools.lru_cache(maxsize=1024)  # a size, of sizes alone
+def _balance_workspace_bytes(tokens: int, n_experts: int) -> int:
+    return (_balance_bytes.bound or _balance_bytes.load())(tokens, n_experts)
+
+
+def _router(logits, expert_ids, coefficient):
+    """Checks a router's logits and choices: tokens, top_k, n_experts, exl3_dtype of the logits and both addresses."""
+    if not isinstance(expert_ids, torch.Tensor) or expert_ids.dim() != 2 or expert_ids.shape[1] < 1:
+        raise Exl3Error("expert_ids: expected a torch tensor [tokens, top_k]")
+    tokens, top_k = expert_ids.shape
+    if tokens * top_k >> 31:
+        too_large("expert_ids", expert_ids.shape)
+    ids = need(expert_ids, "expert_ids", _IDS, expert_ids.shape)
+    n, code, at = _matrix(logits, "logits", tokens)
+    if n > MAX_EXPERTS:
+        raise Exl3Error(f"logits: {n} experts, expected 1 to {MAX_EXPERTS}")
+    if not abs(coefficient) < float("inf"):
+        raise Exl3Error(f"coefficient: {coefficient}, expected a finite number")
+    return tokens, top_k, n, code, at, ids
+
+
+def moe_balance_loss(logits, expert_ids, coefficient: float = 1.0, loss=None, counts=None, workspace=None, stream=None):
+    """The loss that evens out a router's experts, and how many slots each has: (loss, counts).
+
+    With p the softmax of logits [tokens, n_experts], a token counted if one of its slots
+    is kept, V their number and c[e] the kept slots of expert e, the loss (float32 []) is
+    coefficient * n_experts * sum_e (c[e] / (V * top_k)) * (mean over those tokens of p[:, e]);
+    counts (int32 [n_experts + 1]) holds c and V.  A padding token (all its slots
+    dropped) takes no part, whatever its logits.
+
+    workspace: a uint8 device tensor of exl3_moe_balance_workspace_bytes; by default new
+    scratch where that is not 0.
+    """
+    if stream is not None:
+        return on_stream(stream, moe_balance_loss, logits, expert_ids, coefficient, loss, counts, workspace)
+    tokens, top_k, n, code, at, ids = _router(logits, expert_ids, coefficient)
+    if loss is None:
+        loss = logits.new_empty((), dtype=torch.float32)
+    _, l = result(loss, "loss", logits, torch.float32, (), 4)
+    counts, c = result(counts, "counts", expert_ids, torch.int32, (n + 1,))
+    dev = logits.get_device()
+    if not dev == expert_ids.get_device() == loss.get_device() == counts.get_device() >= 0:
+        on_device(dev, logits=logits, expert_ids=expert_ids, loss=loss, counts=counts)
+    ws, nbytes, held = scratch(workspace, 0 if workspace is not None else _balance_workspace_bytes(tokens, n), logits)
+    call(_balance, dev, at, code, ids, _IDS[expert_ids.dtype], tokens, top_k, n, coefficient, l, c, ws, nbytes)
+    return loss, counts
+
+
+def moe_balance_loss_backward(dloss, logits, expert_ids, counts, coefficient: float = 1.0, dlogits=None, stream=None):
+    """The gradient of moe_balance_loss to the logits, in their type: dloss (float32 []) is the
+    gradient that reaches the loss, counts what moe_balance_loss made of these ids."""
+    if stream is not None:
+        return on_stream(stream, moe_balance_loss_backward, dloss, logits, expert_ids, counts, coefficient, dlogits)
+    tokens, top_k, n, code, at, ids = _router(logits, expert_ids, coefficient)
+    d = need(dloss, "dloss", (torch.float32,), (), 4)
+    if dloss.requires_grad or forward_ad._current_level >= 0:
+        no_gradient(dloss, "dloss")
+    c = need(counts, "counts", INDEX, (n + 1,))
+    dlogits, o = result(dlogits, "dlogits", logits, logits.dtype, (tokens, n))
+    dev = logits.get_device()
+    if not dev == expert_ids.get_device() == dloss.get_device() == counts.get_device() == dlogits.get_device() >= 0:
+        on_device(dev, logits=logits, expert_ids=expert_ids, dloss=dloss, counts=counts, dlogits=dlogits)
+    call(_balance_backward, dev, d, at, code, ids, _IDS[expert_ids.dtype], tokens, top_k, n, c, coefficient, o)
+    return dlogits
