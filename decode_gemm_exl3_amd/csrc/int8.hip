@@ -1,17 +1,17 @@
 // int8.hip - products of 8-bit rows with 8-bit weights (gfx950).
 #include <hip/hip_runtime.h>
 
+#include "int8_device.hpp"
 #include "int8_internal.hpp"
+#include "int8_plan.hpp"
 #include "tile_device.hpp"
 
 namespace exl3 {
 namespace i8 {
 
-using namespace mx;  // element types, row tiles of groups, tile order
-
-typedef int i32x16_t __attribute__((ext_vector_type(16)));
-
 struct ProductParams {
+    const void* x;  // rows of values (quantised inside), or null
+    int64_t ldx;
     const int8_t* xc;  // quantised rows
     const float* xs;
     const int* offsets;  // null: one group of all rows
@@ -20,164 +20,668 @@ struct ProductParams {
     const float* ws;
     int n_in, n_out;
     void* y;
+    int ldy;  // outputs from a row of y to the next: n_out, or more where this launch makes some of the columns
 };
-
-constexpr int PIECE = EXL3_INT8_PIECE;
 
 __device__ inline __amdgpu_buffer_rsrc_t buffer(const int8_t* base, int64_t bytes) {
     return mx::buffer(reinterpret_cast<const uint8_t*>(base), bytes);
 }
 
-// A wave's results, 32 RT rows from `row0` and 32 CT outputs from `col0`, of which
-// `rows` rows are written.  A lane holds 4 consecutive outputs of a row; the sums take
-// both scales (xs: of this lane's rows, ws: of the outputs, in LDS) and 32 rows at a time
-// go through LDS (`part`, the wave's own), so that a store writes whole pieces of a row.
-template <typename OT, int CT> constexpr int store_part_bytes() { return 32 * (32 * CT * OT::bytes + 16); }
+// v_mfma_i32_16x16x64_i8 takes, per lane, 16 codes (a block) of row lane % 16, of the
+// (lane / 16)th of the four blocks of 64 inputs; accumulator i is row 4 (lane / 16) + i of
+// the first operand (an output) against row lane % 16 of the second.  (32 x 32 x 32 issues at
+// the same rate, but holds the clock lower: 8192^3 takes 425 us with this one, 446 with that.)
+__device__ inline i32x4_t mfma(const i32x4_t w, const i32x4_t x, const i32x4_t c) { return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, c, 0, 0, 0); }
 
-template <typename OT, int RT, int CT>
-__device__ inline void store_tile(const i32x16_t (&acc)[RT][CT], const float (&xs)[RT], const float* ws, char* part, const ProductParams& p,
-                                  int row0, int rows, int col0) {
-    typedef typename OT::raw raw;
-    constexpr int PITCH = 32 * CT * OT::bytes + 16;
-    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
-    const int cols = min(32 * CT, p.n_out - col0);
-    const bool vec = ((int64_t)p.n_out * OT::bytes) % 16 == 0;
-    raw* y = static_cast<raw*>(p.y);
+// Few rows: eight waves, `split` of them on each run of 16 outputs (8 / split runs a
+// workgroup), for up to 16 rows; of a run's waves, wave w takes the spans (256 inputs) w,
+// w + split, ...  Each wave brings its spans of the weight straight into a ring of its own
+// in LDS, four rows of 256 bytes a load, and waits for nobody.  The rows come quantised, the same
+// way (STREAMED), or, up to HELD blocks of them, the workgroup brings all of them into LDS
+// first, while the weight is on its way: quantised ones (STAGED), or values that it quantises
+// (QUANTISED).  A run's sums meet in LDS.
+//
+// Block b of row r sits in 16-byte slot b ^ r of the row's 256 bytes: the 16 lanes that LDS
+// serves together (rows 0-3 and 12-15 of one quarter of the wave, 4-11 of the next) then read
+// 16 different slots.
+enum Rows { STREAMED, STAGED, QUANTISED };
+
+template <typename OT, Rows ROWS>
+__global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductParams p, int split) {
+    constexpr bool HELD = ROWS != STREAMED;
+    constexpr int SIDES = HELD ? 1 : 2, LOADS = SIDES * 4, BUF = SIDES * 256, RING = SMALL_WAVES * SMALL_RING * BUF;
+    __shared__ i32x4_t lds[small_slots(HELD)];  // the rings, and the held rows
+    static_assert(!HELD || small_per_cu(HELD) == 2, "two workgroups a CU");
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
+    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, blockIdx.y, HELD ? held_rows(p.n_in) : SMALL_MAX_ROWS);
+    if (t.rows == 0) return;
+    const int first = wave % split;  // of the run's spans
+    const int n0 = (blockIdx.x * (SMALL_WAVES / split) + wave / split) * 16, cols = min(16, p.n_out - n0);
+    const int nb = p.n_in / BLOCK, spans = (nb + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
+    i32x4_t* const ring = lds + wave * SMALL_RING * BUF;
+
+    i32x4_t acc = {0, 0, 0, 0};
+    float xs = 0.f;
+    f32x4_t ws = {0.f, 0.f, 0.f, 0.f};
+    if (t.group < p.n_groups) {
+        const int mine = cols > 0 ? (spans - first + split - 1) / split : 0;  // spans of this wave
+        const int64_t w0 = (int64_t)t.group * p.n_out + (cols > 0 ? n0 : 0);
+        const int w_rows = max(cols, 1);
+        const __amdgpu_buffer_rsrc_t bw = buffer(p.wc + w0 * p.n_in, (int64_t)w_rows * p.n_in);
+        const __amdgpu_buffer_rsrc_t bx = buffer(HELD ? p.wc : p.xc + (int64_t)t.row0 * p.n_in, HELD ? 0 : (int64_t)t.rows * p.n_in);
+        uint32_t w_at[4], x_at[4];
 #pragma unroll
-    for (int m = 0; m < RT; ++m) {
-        const int live = min(32, rows - 32 * m);
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const f32x4_t w = *reinterpret_cast<const f32x4_t*>(ws + 32 * c + 8 * g + 4 * h);
-                f32x4_t v;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = rounded((float)acc[m][c][4 * g + i] * xs[m] * w[i]);
-                store4<OT>(part + r * PITCH, 32 * c + 8 * g + 4 * h, 4, true, v);
-            }
-        __builtin_amdgcn_wave_barrier();
-        const int64_t y0 = (int64_t)(row0 + 32 * m) * p.n_out + col0;
-        if (vec) {
-            constexpr int PER = 16 / OT::bytes, LANES = 32 * CT / PER;  // outputs of a lane, lanes of a row
-#pragma unroll
-            for (int i = 0; i < 32; i += 64 / LANES) {
-                const int row = i + lane / LANES, o = lane % LANES * PER;
-                const i32x4_t v = *reinterpret_cast<const i32x4_t*>(part + row * PITCH + o * OT::bytes);
-                if (row < live && o < cols) *reinterpret_cast<i32x4_t*>(y + y0 + (int64_t)row * p.n_out + o) = v;
-            }
-        } else {
-            for (int i = lane; i < live * 32 * CT; i += 64) {
-                const int row = i / (32 * CT), o = i % (32 * CT);
-                const raw v = reinterpret_cast<const raw*>(part + row * PITCH)[o];
-                if (o < cols) y[y0 + (int64_t)row * p.n_out + o] = v;
-            }
+        for (int i = 0; i < 4; ++i) {
+            // load i: row 4 i + lane / 16, slot lane % 16; rows behind the tile re-read its last
+            const int row = 4 * i + (lane >> 4), block = (lane & 15) ^ row;
+            w_at[i] = (uint32_t)min(row, w_rows - 1) * p.n_in + 16 * block;
+            x_at[i] = (uint32_t)min(row, t.rows - 1) * p.n_in + 16 * block;
         }
-        __builtin_amdgcn_wave_barrier();
+        // The loads of this wave's kth span; behind its last, and behind the end of a row, they give zeros.
+        auto ask = [&](int k) {
+            const int sp = k < mine ? first + k * split : spans;
+            i32x4_t* const buf = ring + k % SMALL_RING * BUF;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int block = (lane & 15) ^ (4 * i + (lane >> 4));
+                const bool in = sp * SPAN_BLOCKS + block < nb;
+                load16_to_lds(bw, buf + i * 64, in ? w_at[i] : OUTSIDE, (uint32_t)sp * 256);
+                if constexpr (!HELD) load16_to_lds(bx, buf + 256 + i * 64, in ? x_at[i] : OUTSIDE, (uint32_t)sp * 256);
+            }
+        };
+        i32x4_t* const xq = lds + RING;  // [row][spans * 16], block b of row r at b ^ r
+        uint32_t* const amax = reinterpret_cast<uint32_t*>(xq);  // before the codes: each row's largest magnitude
+        if constexpr (ROWS == QUANTISED) {
+            if (threadIdx.x < SMALL_MAX_ROWS) amax[threadIdx.x] = 0;
+        }
+        if (first == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ws[i] = p.ws[w0 + min(4 * q + i, w_rows - 1)];
+        }
+        if constexpr (ROWS != QUANTISED) xs = p.xs[t.row0 + min(r, t.rows - 1)];
+        // The rows are asked for before the weight, as loads come back in order.
+        auto ask_ring = [&]() {
+#pragma unroll
+            for (int k = 0; k < SMALL_RING; ++k) ask(k);
+        };
+        if constexpr (ROWS == STREAMED) ask_ring();
+        if constexpr (ROWS == STAGED) {
+            // HELD_BLOCKS / 512 blocks a thread (blocks behind a row's end are anything: the weight's are zeros)
+            constexpr int ROUNDS = HELD_BLOCKS / (SMALL_WAVES * 64);
+            const int units = t.rows * nb;
+            i32x4_t v[ROUNDS];
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                const int u = threadIdx.x + i * SMALL_WAVES * 64;
+                if (u < units) v[i] = *reinterpret_cast<const i32x4_t*>(p.xc + ((int64_t)t.row0 * nb + u) * BLOCK);
+            }
+            ask_ring();
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                const int u = threadIdx.x + i * SMALL_WAVES * 64, row = u / nb, block = u - row * nb;
+                if (u < units) xq[row * spans * 16 + (block ^ row)] = v[i];
+            }
+            __syncthreads();
+        }
+        if constexpr (ROWS == QUANTISED) {
+            // all rows' values in registers: their largest magnitudes meet in LDS, then the codes go there
+            constexpr int THREADS = SMALL_WAVES * 64, N = 16 / OT::bytes, ROUNDS = HELD_BLOCKS * BLOCK / N / THREADS;
+            const int per_row = p.n_in / N, units = t.rows * per_row;
+            float u[ROUNDS][N];
+            u32x4_t v[ROUNDS];
+            int row[ROUNDS];
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                const int at = threadIdx.x + i * THREADS;
+                row[i] = at / per_row;
+                v[i] = u32x4_t{0, 0, 0, 0};
+                if (at < units) v[i] = load_piece<OT, true>(p.x, (int64_t)(t.row0 + row[i]) * p.ldx + (at - row[i] * per_row) * N, N);
+            }
+            ask_ring();
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i)
+#pragma unroll
+                for (int e = 0; e < N; ++e) u[i][e] = piece_value<OT>(v[i], e);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                const uint32_t mine = amax_piece<N>(0, u[i]);
+                const int one = __builtin_amdgcn_readfirstlane(row[i]);
+                if (i * THREADS >= units) break;
+                if (__all(row[i] == one)) {
+                    const uint32_t most = wave_max(mine);
+                    if (lane == 0 && one < t.rows) atomicMax(&amax[one], most);
+                } else if (row[i] < t.rows) {
+                    atomicMax(&amax[row[i]], mine);
+                }
+            }
+            __syncthreads();
+            uint32_t most[ROUNDS];
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) most[i] = amax[min(row[i], t.rows - 1)];
+            xs = row_scale(amax[min(r, t.rows - 1)], 1.0);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                const int at = threadIdx.x + i * THREADS;
+                if (at >= units) break;
+                const uint32_t a = most[i];
+                const float largest = __builtin_bit_cast(float, a);
+                uint32_t c[N / 4] = {};
+                if (a < NOT_FINITE) code_piece<N>(u[i], largest, 127.f / largest, c);
+                const int col = (at - row[i] * per_row) * N, block = col / BLOCK;
+                uint32_t* const dst = reinterpret_cast<uint32_t*>(xq + row[i] * spans * 16 + (block ^ row[i])) + col % BLOCK / 4;
+                if constexpr (N == 8) *reinterpret_cast<uint2*>(dst) = uint2{c[0], c[1]};
+                else *dst = c[0];
+            }
+            __syncthreads();
+        }
+        for (int k = 0; k < mine; ++k) {
+            __builtin_amdgcn_sched_barrier(0);
+            wait_loads<(SMALL_RING - 1) * LOADS, false>();
+            __builtin_amdgcn_sched_barrier(0);
+            const int sp = first + k * split;
+            const i32x4_t* const buf = ring + k % SMALL_RING * BUF;
+            i32x4_t wv[4], xv[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                wv[j] = buf[r * 16 + ((4 * j + q) ^ r)];
+                const int row = HELD ? min(r, t.rows - 1) : r;  // rows behind the tile re-read its last
+                xv[j] = HELD ? xq[(row * spans + sp) * 16 + ((4 * j + q) ^ row)] : buf[256 + r * 16 + ((4 * j + q) ^ r)];
+            }
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the buffer is read
+            __builtin_amdgcn_sched_barrier(0);
+            ask(k + SMALL_RING);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc = mfma(wv[j], xv[j], acc);
+        }
+        wait_loads<0, false>();  // nothing is on its way into LDS any more
+    }
+    // each wave's sums over its own ring
+    ring[lane] = acc;
+    __syncthreads();
+    if (first == 0) {
+        for (int w = 1; w < split; ++w) acc += ring[w * SMALL_RING * BUF + lane];
+        const int o = n0 + 4 * q;
+        if (r < t.rows && o < p.n_out) {
+            f32x4_t v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = rounded((float)acc[i] * xs * ws[i]);
+            store4<OT>(p.y, (int64_t)(t.row0 + r) * p.ldy + o, p.n_out - o, (p.ldy & 3) == 0, v);
+        }
     }
 }
 
-// A workgroup of four waves owns 64 RT rows and 64 CT outputs, each wave a quarter of
-// them.  Stages of 128 inputs of both sides go straight from memory into LDS, double
-// buffered.  Block c (16 inputs) of row r sits in 16-byte slot c ^ (r / 2 & 7) of the
-// row's 128 bytes: the 16 lanes that LDS serves together (0-3, 12-15, 20-23, 24-27
-// and so on) then read 16 different slots of its 256-byte width.
-//
-// v_mfma_i32_32x32x32_i8 takes, per lane, 16 codes of row lane % 32, of the first or the
-// second 16 inputs by lane / 32; accumulator i is row 8 (i / 4) + 4 (lane / 32) + i % 4 of
-// the first operand (an output) against row lane % 32 of the second.
-constexpr int STAGE_BLOCKS = 8;
+// v, computed where this stands: what follows from it takes no registers over a loop before.
+__device__ inline int here(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
 
-template <typename OT, int RT, int CT>
-__global__ __launch_bounds__(256, RT * CT > 4 ? 1 : 2) void tile_kernel(const ProductParams p, int row_tiles, int col_tiles) {
-    constexpr int BM = 64 * RT, BN = 64 * CT;
-    constexpr int STAGE = (BM + BN) * STAGE_BLOCKS;  // 16-byte slots: the rows', then the weight's
-    constexpr int ROW_LOADS = BM / 32, W_LOADS = BN / 32;  // a wave's loads per stage, 8 rows each
-    constexpr int PART = store_part_bytes<OT, CT>();
-    constexpr int SLOTS = 2 * STAGE * 16 > 4 * PART ? 2 * STAGE : 4 * PART / 16;
-    __shared__ i32x4_t lds[SLOTS + BN / 4];  // the buffers (later the waves' parts), then the outputs' scales
-    float* const lds_scales = reinterpret_cast<float*>(lds + SLOTS);
+// A wave's results: RT times 16 rows, STEP from one 16 to the next, the first at `row0`, and 16 CT
+// outputs from `col0`, of which those less than `rows` behind row0 are written.  The sums take
+// both scales: xs of this lane's rows, ws of output lane % (16 CT).  A lane holds 4 consecutive
+// outputs of a row; for 16-bit results lanes 16 apart exchange halves of two tiles, so that
+// each has 8.  A store then writes 64 bytes of each of 16 rows.
+template <typename OT, int STEP, int RT, int CT>
+__device__ inline void store_tile(const i32x4_t (&acc)[RT][CT], const float (&xs)[RT], float ws, const ProductParams& p, int row0, int rows, int col0) {
+    typedef typename OT::raw raw;
+    const int lane = here(threadIdx.x & 63), r = lane & 15, q = lane >> 4;
+    raw* y = static_cast<raw*>(p.y);
+    auto store = [&](int row, int o, auto v) {  // 16 bytes, or what is left of the row
+        constexpr int N = 16 / OT::bytes;
+        raw* const dst = y + (int64_t)(row0 + row) * p.ldy + o;
+        if (row >= rows) return;
+        if (o + N <= p.n_out) {
+            __builtin_memcpy(dst, &v, 16);  // rows start at any value: an unaligned store
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (o + i < p.n_out) dst[i] = (raw)(OT::bytes == 2 ? v[i / 2] >> (16 * (i & 1)) : v[i]);
+        }
+    };
+    float w[CT][4];
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[c][i] = __shfl(ws, 16 * c + 4 * q + i);
+#pragma unroll
+    for (int m = 0; m < RT; ++m) {
+        auto value = [&](int c, int i) { return rounded((float)acc[m][c][i] * xs[m] * w[c][i]); };
+        if constexpr (OT::bytes == 4) {
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                u32x4_t v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = from_f32(OT{}, value(c, i));
+                store(m * STEP + r, col0 + 16 * c + 4 * q, v);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < CT; c += 2) {
+                u32x4_t v;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t lo = (uint32_t)from_f32(OT{}, value(c, 2 * i)) | ((uint32_t)from_f32(OT{}, value(c, 2 * i + 1)) << 16);
+                    const uint32_t hi = (uint32_t)from_f32(OT{}, value(c + 1, 2 * i)) | ((uint32_t)from_f32(OT{}, value(c + 1, 2 * i + 1)) << 16);
+                    // odd rows of 16 lanes of the one for even rows of the other
+                    const auto both = __builtin_amdgcn_permlane16_swap(lo, hi, false, false);
+                    v[i] = both[0];
+                    v[2 + i] = both[1];
+                }
+                store(m * STEP + r, col0 + 16 * (c + (q & 1)) + 8 * (q >> 1), v);
+            }
+        }
+    }
+}
+
+// Some rows, or few tiles: a workgroup of four waves owns T rows and T outputs.  Stages of
+// a span (256 bytes a row of both sides) go straight into a ring in LDS, all but one of it
+// ahead: a stage is little work, so it is the bytes in flight that count.  T = 64: each wave a
+// quarter of the tile.  T = 32: each wave the whole tile over a quarter of the stage's
+// inputs, and the waves' sums meet in LDS at the end; four times the workgroups where 64 x 64
+// tiles would leave most of the card idle.  Block b of row r sits in slot b ^ (r & 15) of the
+// row's 256 bytes.
+template <int T> constexpr int MEDIUM_RING = T == 64 ? 4 : 8;
+
+template <typename OT, int T>
+__global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int row_tiles, int col_tiles) {
+    constexpr int RING = MEDIUM_RING<T>, LOADS = T / 8, BUF = 2 * T * 16;  // loads of a wave and stage; slots: rows, then weight rows
+    __shared__ i32x4_t lds[RING * BUF];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 31, h = lane >> 5, wy = wave >> 1, wx = wave & 1;
-    int row_tile, col;
-    if (!tile_of(xcd_tile(blockIdx.x), row_tiles, col_tiles, &row_tile, &col)) return;
-    const RowTile t = find_tile(p.offsets, p.n_groups, p.rows, row_tile, BM);
+    const int r = lane & 15, q = lane >> 4, wy = T == 64 ? wave >> 1 : 0, wx = T == 64 ? wave & 1 : 0;
+    const ProductTile t = product_tile(p.offsets, p.n_groups, p.rows, xcd_tile(blockIdx.x), T, row_tiles, col_tiles);
     if (t.rows == 0) return;
-    const int n0 = col * BN, cols = min(BN, p.n_out - n0);
-    const int nb = p.n_in / PIECE, stages = (nb + STAGE_BLOCKS - 1) / STAGE_BLOCKS;
+    const int n0 = t.col * T, cols = min(T, p.n_out - n0);
+    const int nb = p.n_in / BLOCK, stages = (nb + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
 
-    i32x16_t acc[RT][CT];
-    float xs[RT];
+    i32x4_t acc[2][2];
+    float xs[2] = {0.f, 0.f}, ws = 0.f;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) acc[m][c] = i32x4_t{0, 0, 0, 0};
+    if (t.group < p.n_groups) {
+        const int64_t w0 = (int64_t)t.group * p.n_out + n0;
+        const __amdgpu_buffer_rsrc_t bx = buffer(p.xc + (int64_t)t.row0 * p.n_in, (int64_t)t.rows * p.n_in);
+        const __amdgpu_buffer_rsrc_t bw = buffer(p.wc + w0 * p.n_in, (int64_t)cols * p.n_in);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) xs[m] = p.xs[t.row0 + min(wy * 32 + 16 * m + r, t.rows - 1)];
+        ws = p.ws[w0 + min(wx * 32 + (lane & 31), cols - 1)];
+        // Rows of both sides together, the weight's from T on.  Load i of a wave: row
+        // 16 i + 4 wave + lane / 16, slot lane % 16; rows behind a side's end re-read its last.
+        const int srow = 4 * wave + (lane >> 4), block = (lane & 15) ^ srow;
+        uint32_t at[LOADS];
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int row = 16 * i + srow;
+            at[i] = (uint32_t)(16 * i < T ? min(row, t.rows - 1) : min(row - T, cols - 1)) * p.n_in + 16 * block;
+        }
+        auto ask = [&](int st) {  // behind the last stage: zeros
+            i32x4_t* const buf = lds + st % RING * BUF;
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i)
+                load16_to_lds(16 * i < T ? bx : bw, buf + i * 256 + wave * 64, st * SPAN_BLOCKS + block < nb ? at[i] : OUTSIDE, (uint32_t)st * 256);
+        };
+#pragma unroll
+        for (int k = 0; k < RING - 1; ++k) ask(k);
+        for (int st = 0; st < stages; ++st) {
+            // this stage has landed in every wave, and the one before it is read
+            __builtin_amdgcn_sched_barrier(0);
+            wait_loads<(RING - 2) * LOADS, true>();
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            ask(st + RING - 1);
+            const i32x4_t* const buf = lds + st % RING * BUF;
+#pragma unroll
+            for (int j = 0; j < (T == 64 ? 4 : 1); ++j) {
+                const int slot = r * 16 + ((4 * (T == 64 ? j : wave) + q) ^ r);
+                i32x4_t xv[2], wv[2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m) xv[m] = buf[(wy * 2 + m) * 256 + slot];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) wv[c] = buf[T * 16 + (wx * 2 + c) * 256 + slot];
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) acc[m][c] = mfma(wv[c], xv[m], acc[m][c]);
+            }
+        }
+        wait_loads<0, true>();  // nothing is on its way into LDS any more
+    }
+    if constexpr (T == 32) {
+        // the four waves' sums, added by wave 0, over the ring that every wave has read
+        __syncthreads();
+        i32x4_t* const sums = lds;
+        if (wave > 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sums[((wave - 1) * 4 + e) * 64 + lane] = acc[e >> 1][e & 1];
+        }
+        __syncthreads();
+        if (wave > 0) return;
+#pragma unroll
+        for (int v = 0; v < 3; ++v)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e >> 1][e & 1] += sums[(v * 4 + e) * 64 + lane];
+    }
+    store_tile<OT, 16, 2, 2>(acc, xs, ws, p, t.row0 + wy * 32, t.rows - wy * 32, n0 + wx * 32);
+}
+
+// More rows: a workgroup of four waves owns 128 rows and 128 outputs, each wave a quarter of
+// them; two workgroups a CU.  A stage is 128 inputs, a unit of 16 KB of each side, that go
+// straight from memory into LDS.  LDS holds five units in a ring, weight, rows, weight, rows,
+// weight: the rows are asked for one stage ahead, the weight (which more often comes from
+// memory) two.  Block b of row r sits in 16-byte slot b ^ (r / 2 & 7) of the row's 128 bytes:
+// the 16 lanes that LDS serves together then read 16 different slots of its 256-byte width.
+constexpr int STAGE_BLOCKS = 8;
+// Units of the ring of this stage's rows, the next stage's rows and the weight of the one after
+// that, from that of this stage's weight; and that of the next stage's weight.
+__device__ inline int rows_unit(int u) { return u == 4 ? 0 : u + 1; }
+__device__ inline int next_rows_unit(int u) { return u >= 2 ? u - 2 : u + 3; }
+__device__ inline int after_next_weight_unit(int u) { return u >= 1 ? u - 1 : u + 4; }
+__device__ inline int next_weight_unit(int u) { return u >= 3 ? u - 3 : u + 2; }
+
+template <typename OT>
+__global__ __launch_bounds__(256, 2) void middle_kernel(const ProductParams p, int row_tiles, int col_tiles) {
+    constexpr int RT = 4, CT = 4, BM = 128, BN = 128, UNIT = 128 * STAGE_BLOCKS;
+    __shared__ i32x4_t lds[5 * UNIT];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, q = lane >> 4, wy = wave >> 1, wx = wave & 1;
+    const ProductTile t = product_tile(p.offsets, p.n_groups, p.rows, xcd_tile(blockIdx.x), BM, row_tiles, col_tiles);
+    if (t.rows == 0) return;
+    const int n0 = t.col * BN, cols = min(BN, p.n_out - n0);
+    const int nb = p.n_in / BLOCK, stages = (nb + STAGE_BLOCKS - 1) / STAGE_BLOCKS;
+
+    i32x4_t acc[RT][CT];
+    float xs[RT], ws = 0.f;
 #pragma unroll
     for (int m = 0; m < RT; ++m) {
         xs[m] = 0.f;
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[m][c][i] = 0;
+        for (int c = 0; c < CT; ++c) acc[m][c] = i32x4_t{0, 0, 0, 0};
     }
     if (t.group < p.n_groups) {
         const int64_t w0 = (int64_t)t.group * p.n_out + n0;
         const __amdgpu_buffer_rsrc_t bx = buffer(p.xc + (int64_t)t.row0 * p.n_in, (int64_t)t.rows * p.n_in);
         const __amdgpu_buffer_rsrc_t bw = buffer(p.wc + w0 * p.n_in, (int64_t)cols * p.n_in);
 #pragma unroll
-        for (int m = 0; m < RT; ++m) xs[m] = p.xs[t.row0 + min((wy * RT + m) * 32 + r, t.rows - 1)];
-        for (int i = threadIdx.x; i < BN; i += 256) lds_scales[i] = p.ws[w0 + min(i, cols - 1)];
+        for (int m = 0; m < RT; ++m) xs[m] = p.xs[t.row0 + min((wy * RT + m) * 16 + r, t.rows - 1)];
+        ws = p.ws[w0 + min(wx * 64 + lane, cols - 1)];
         // Rows behind the tile re-read its last (never stored).  Load i of a wave brings
-        // rows 32 i + 8 wave .. + 7, lane l slot l % 8 of row l / 8.
+        // rows 32 i + 8 wave .. + 7 of a unit, lane l slot l % 8 of row l / 8.
         const int srow = 8 * wave + (lane >> 3), sblock = (lane & 7) ^ ((srow >> 1) & 7);
-        uint32_t xat[ROW_LOADS], wat[W_LOADS];
+        uint32_t xat[4], wat[4];
 #pragma unroll
-        for (int i = 0; i < ROW_LOADS; ++i) xat[i] = (uint32_t)min(32 * i + srow, t.rows - 1) * p.n_in + 16 * sblock;
-#pragma unroll
-        for (int i = 0; i < W_LOADS; ++i) wat[i] = (uint32_t)min(32 * i + srow, cols - 1) * p.n_in + 16 * sblock;
-        auto ask = [&](int st) {  // blocks behind the end: zeros
+        for (int i = 0; i < 4; ++i) {
+            xat[i] = (uint32_t)min(32 * i + srow, t.rows - 1) * p.n_in + 16 * sblock;
+            wat[i] = (uint32_t)min(32 * i + srow, cols - 1) * p.n_in + 16 * sblock;
+        }
+        // The loads of a side of stage st into unit `to` of the ring; behind the end of a row: zeros.
+        auto ask = [&](__amdgpu_buffer_rsrc_t b, const uint32_t (&at)[4], int st, int to) {
             const bool in = st * STAGE_BLOCKS + sblock < nb;
-            i32x4_t* dst = lds + (st & 1) * STAGE + wave * 64;
+            i32x4_t* dst = lds + to * UNIT + wave * 64;
 #pragma unroll
-            for (int i = 0; i < ROW_LOADS; ++i) load16_to_lds(bx, dst + i * 256, in ? xat[i] : OUTSIDE, (uint32_t)st * 128);
-#pragma unroll
-            for (int i = 0; i < W_LOADS; ++i) load16_to_lds(bw, dst + BM * 8 + i * 256, in ? wat[i] : OUTSIDE, (uint32_t)st * 128);
+            for (int i = 0; i < 4; ++i) load16_to_lds(b, dst + i * 256, in ? at[i] : OUTSIDE, (uint32_t)st * 128);
         };
-        ask(0);
+        ask(bw, wat, 0, 0);
+        ask(bx, xat, 0, 1);
+        ask(bw, wat, 1, 2);
+        int uw = 0;  // the ring's unit of this stage's weight
         for (int st = 0; st < stages; ++st) {
-            __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0): this stage has landed, the one before it is read
+            __builtin_amdgcn_sched_barrier(0);
+            wait_loads<4, true>();  // all but the next stage's weight: this stage has landed, the one before it is read
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
-            if (st + 1 < stages) ask(st + 1);
-            const i32x4_t* const buf = lds + (st & 1) * STAGE;
+            ask(bx, xat, st + 1, next_rows_unit(uw));
+            ask(bw, wat, st + 2, after_next_weight_unit(uw));
+            const i32x4_t* const xbuf = lds + rows_unit(uw) * UNIT + wy * RT * 128;
+            const i32x4_t* const wbuf = lds + uw * UNIT + wx * CT * 128;
 #pragma unroll
-            for (int j = 0; j < STAGE_BLOCKS / 2; ++j) {
-                const int slot = r * 8 + ((2 * j + h) ^ ((r >> 1) & 7));
+            for (int j = 0; j < 2; ++j) {
+                const int slot = r * 8 + ((4 * j + q) ^ ((r >> 1) & 7));
                 i32x4_t xv[RT], wv[CT];
 #pragma unroll
-                for (int m = 0; m < RT; ++m) xv[m] = buf[(wy * RT + m) * 256 + slot];
+                for (int m = 0; m < RT; ++m) xv[m] = xbuf[m * 128 + slot];
 #pragma unroll
-                for (int c = 0; c < CT; ++c) wv[c] = buf[BM * 8 + (wx * CT + c) * 256 + slot];
+                for (int c = 0; c < CT; ++c) wv[c] = wbuf[c * 128 + slot];
 #pragma unroll
                 for (int m = 0; m < RT; ++m)
 #pragma unroll
-                    for (int c = 0; c < CT; ++c) acc[m][c] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[c], xv[m], acc[m][c], 0, 0, 0);
+                    for (int c = 0; c < CT; ++c) acc[m][c] = mfma(wv[c], xv[m], acc[m][c]);
             }
+            uw = next_weight_unit(uw);
         }
-    } else {
-        for (int i = threadIdx.x; i < BN; i += 256) lds_scales[i] = 0.f;
+        wait_loads<0, true>();  // nothing is on its way into LDS any more
     }
-    __syncthreads();
-    store_tile<OT, RT, CT>(acc, xs, lds_scales + wx * CT * 32, reinterpret_cast<char*>(lds) + wave * PART, p, t.row0 + wy * RT * 32,
-                           t.rows - wy * RT * 32, n0 + wx * CT * 32);
+    store_tile<OT, 16, RT, CT>(acc, xs, ws, p, t.row0 + wy * RT * 16, t.rows - wy * RT * 16, n0 + wx * CT * 16);
+}
+
+// Many rows: a workgroup of eight waves takes tiles of 256 rows and 256 outputs, one after the
+// other; one workgroup a CU.  The waves form two groups, one of each on a SIMD, that take turns:
+// while one group reads its operands from LDS and asks for memory, the other has the matrix
+// cores; a barrier ends each turn.  A wave has every other 16 of the rows, by its group, and 64 of
+// the outputs: where a tile has fewer rows both groups have less to do.
+//
+// A stage is 128 inputs.  With 256 rows it is a unit of 32 KB of each side, and LDS holds five of
+// them in a ring as above; with 128 rows LDS holds three whole stages of 48 KB, and both sides
+// are asked for two ahead.  The ring does not run dry between tiles: the last stages of a tile ask
+// for the first of the next, and its results leave from registers.
+constexpr int LARGE_COLS = 256;
+
+template <typename OT, int RT>
+__global__ __launch_bounds__(512, 2) void large_kernel(const ProductParams p, int row_tiles, int col_tiles, int tiles) {
+    constexpr int CT = 4, ROWS = 32 * RT, UNIT = 256 * STAGE_BLOCKS, STAGE = (ROWS + LARGE_COLS) * STAGE_BLOCKS;
+    constexpr bool UNITS = RT == 8;  // a ring of units, not of stages
+    constexpr int AHEAD = UNITS ? 4 : 4 + RT / 2;  // loads of a wave in flight over the end of a stage
+    __shared__ i32x4_t lds[UNITS ? 5 * UNIT : 3 * STAGE];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, q = lane >> 4, wy = wave >> 2, wx = wave & 3;
+    const int nb = p.n_in / BLOCK, stages = max(2, (nb + STAGE_BLOCKS - 1) / STAGE_BLOCKS);
+
+    struct Tile {
+        int row0, rows, n0, cols;
+        int64_t w0;
+    };
+    // The next tile from `index` on, or one without rows behind the last; tiles of rows of no
+    // group are filled with zeros on the way.
+    int index = blockIdx.x;
+    auto next_tile = [&]() {
+        for (; index < tiles; index += gridDim.x) {
+            const ProductTile t = product_tile(p.offsets, p.n_groups, p.rows, xcd_tile(index), ROWS, row_tiles, col_tiles);
+            if (t.rows == 0) continue;
+            const int n0 = t.col * LARGE_COLS, cols = min(LARGE_COLS, p.n_out - n0);
+            if (t.group >= p.n_groups) {
+                typedef typename OT::raw raw;
+                for (int i = threadIdx.x; i < t.rows * LARGE_COLS; i += 512)
+                    if (i % LARGE_COLS < cols) static_cast<raw*>(p.y)[(int64_t)(t.row0 + i / LARGE_COLS) * p.ldy + n0 + i % LARGE_COLS] = 0;
+                continue;
+            }
+            index += gridDim.x;
+            return Tile{t.row0, t.rows, n0, cols, (int64_t)t.group * p.n_out + n0};
+        }
+        return Tile{0, 0, 0, 0, 0};
+    };
+    // Rows and outputs behind a tile's end are outside its memory: zeros.
+    auto rows_of = [&](const Tile& t) { return buffer(p.xc + (int64_t)t.row0 * p.n_in, (int64_t)t.rows * p.n_in); };
+    auto weight_of = [&](const Tile& t) { return buffer(p.wc + t.w0 * p.n_in, (int64_t)t.cols * p.n_in); };
+
+    // Load i of a wave brings rows 64 i + 8 wave .. + 7 of a unit, lane l slot l % 8 of row l / 8.
+    const int srow = 8 * wave + (lane >> 3), sblock = (lane & 7) ^ ((srow >> 1) & 7);
+    uint32_t at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) at[i] = (uint32_t)(64 * i + srow) * p.n_in + 16 * sblock;
+    // The loads of `loads` times 64 rows of a side of stage st to `dst`; behind the end of a row: zeros.
+    auto ask = [&](__amdgpu_buffer_rsrc_t b, int loads, int st, i32x4_t* dst) {
+        const bool in = st * STAGE_BLOCKS + sblock < nb;
+#pragma unroll
+        for (int i = 0; i < loads; ++i) load16_to_lds(b, dst + wave * 64 + i * 512, in ? at[i] : OUTSIDE, (uint32_t)st * 128);
+    };
+    // Where the ring has this stage's weight and rows: u is a unit, or the number of a stage.
+    auto weight_at = [&](int u) { return lds + u * (UNITS ? UNIT : STAGE); };
+    auto rows_at = [&](int u) { return UNITS ? lds + rows_unit(u) * UNIT : lds + u * STAGE + LARGE_COLS * STAGE_BLOCKS; };
+    int frag[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) frag[j] = r * 8 + ((4 * j + q) ^ ((r >> 1) & 7));
+
+    Tile t = {0, 0, 0, 0, 0};
+    __amdgpu_buffer_rsrc_t bx, bw;
+    int u = 0;  // where the ring has this stage
+    bool started = false;
+    for (;;) {
+        const Tile after = next_tile();
+        const __amdgpu_buffer_rsrc_t ax = rows_of(after), aw = weight_of(after);
+        if (!started) {
+            if (after.rows == 0) return;
+            started = true;
+            t = after;
+            bx = ax;
+            bw = aw;
+            ask(bw, 4, 0, weight_at(0));
+            ask(bx, RT / 2, 0, rows_at(0));
+            ask(bw, 4, 1, weight_at(UNITS ? 2 : 1));
+            if (!UNITS) ask(bx, RT / 2, 1, rows_at(1));
+            __builtin_amdgcn_sched_barrier(0);
+            wait_loads<AHEAD, false>();  // the first stage has landed
+            __builtin_amdgcn_s_barrier();
+            if (wy == 1) __builtin_amdgcn_s_barrier();  // the second group is a turn behind
+            __builtin_amdgcn_sched_barrier(0);
+            continue;
+        }
+        i32x4_t acc[RT][CT];
+        float xs[RT];
+        const int own = here(lane);
+#pragma unroll
+        for (int m = 0; m < RT; ++m) {
+            xs[m] = p.xs[t.row0 + min(32 * m + 16 * wy + (own & 15), t.rows - 1)];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) acc[m][c] = i32x4_t{0, 0, 0, 0};
+        }
+        const float ws = p.ws[t.w0 + min(wx * 64 + own, t.cols - 1)];
+        for (int st = 0; st < stages; ++st) {
+            const i32x4_t* const xbuf = rows_at(u) + wy * 128;
+            const i32x4_t* const wbuf = weight_at(u) + wx * CT * 128;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                i32x4_t xv[RT], wv[CT];
+#pragma unroll
+                for (int c = 0; c < CT; ++c) wv[c] = wbuf[c * 128 + frag[j]];
+#pragma unroll
+                for (int m = 0; m < RT; ++m) xv[m] = xbuf[m * 256 + frag[j]];
+                // Into what held the stage before, which every wave has read; one side in each half of
+                // the stage, as the address unit takes 16 cycles a load.
+                const int next = st + (UNITS && j == 0 ? 1 : 2);
+                const bool in = next < stages;
+                const int of = in ? next : next - stages;
+                if constexpr (UNITS) {
+                    if (j == 0) ask(in ? bx : ax, 4, of, lds + next_rows_unit(u) * UNIT);
+                    else ask(in ? bw : aw, 4, of, lds + after_next_weight_unit(u) * UNIT);
+                } else {
+                    const int to = u == 0 ? 2 : u - 1;
+                    if (j == 0) ask(in ? bw : aw, 4, of, weight_at(to));
+                    else ask(in ? bx : ax, RT / 2, of, rows_at(to));
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                if (j == 1) wait_loads<AHEAD, true>();  // the next stage has landed
+                else __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+                for (int m = 0; m < RT; ++m)
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) acc[m][c] = mfma(wv[c], xv[m], acc[m][c]);
+                __builtin_amdgcn_s_setprio(0);
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            u = UNITS ? next_weight_unit(u) : u == 2 ? 0 : u + 1;
+        }
+        store_tile<OT, 32, RT, CT>(acc, xs, ws, p, t.row0 + 16 * wy, t.rows - 16 * wy, t.n0 + wx * 64);
+        if (after.rows == 0) break;
+        t = after;
+        bx = ax;
+        bw = aw;
+    }
+    if (wy == 0) __builtin_amdgcn_s_barrier();
+    wait_loads<0, false>();  // nothing is on its way into LDS any more
 }
 
 // ---- launches ----
 
-template <typename OT, int RT, int CT> hipError_t launch_tiles(const ProductParams& p, hipStream_t s) {
-    const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, 64 * RT), cols = (p.n_out + 64 * CT - 1) / (64 * CT);
-    tile_kernel<OT, RT, CT><<<(unsigned)xcd_padded(rows * cols), 256, 0, s>>>(p, (int)rows, (int)cols);
+template <typename OT, Rows ROWS> hipError_t launch_small(const ProductParams& p, hipStream_t s) {
+    constexpr bool HELD = ROWS != STREAMED;
+    const int64_t runs = (p.n_out + 15) / 16, tiles = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, HELD ? held_rows(p.n_in) : SMALL_MAX_ROWS);
+    const int split = small_split(p.n_out, tiles, p.n_in, HELD);
+    const dim3 grid((unsigned)((runs * split + SMALL_WAVES - 1) / SMALL_WAVES), (unsigned)tiles);
+    small_kernel<OT, ROWS><<<grid, SMALL_WAVES * 64, 0, s>>>(p, split);
     return hipGetLastError();
 }
 
+template <typename OT, int T> hipError_t launch_medium(const ProductParams& p, hipStream_t s) {
+    const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, T), cols = (p.n_out + T - 1) / T;
+    medium_kernel<OT, T><<<(unsigned)xcd_padded(rows * cols), 256, 0, s>>>(p, (int)rows, (int)cols);
+    return hipGetLastError();
+}
+
+template <typename OT> hipError_t launch_middle(const ProductParams& p, hipStream_t s) {
+    const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, 128), cols = (p.n_out + 127) / 128;
+    middle_kernel<OT><<<(unsigned)xcd_padded(rows * cols), 256, 0, s>>>(p, (int)rows, (int)cols);
+    return hipGetLastError();
+}
+
+template <typename OT, int RT> hipError_t launch_large(const ProductParams& p, hipStream_t s) {
+    const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, 32 * RT), cols = (p.n_out + LARGE_COLS - 1) / LARGE_COLS;
+    const int64_t tiles = xcd_padded(rows * cols);
+    large_kernel<OT, RT><<<(unsigned)(tiles < CUS ? tiles : CUS), 512, 0, s>>>(p, (int)rows, (int)cols, (int)tiles);
+    return hipGetLastError();
+}
+
+// Row tiles of `high` rows that a product is expected to have: with groups, half a
+// tile of each group (or row) is padding.
+inline int64_t expected_tiles(const ProductParams& p, int high) {
+    if (!p.offsets) return (p.rows + high - 1) / high;
+    return p.rows / high + (p.n_groups < p.rows ? p.n_groups : p.rows) / 2 + 1;
+}
+
+// The time of a product in tiles, in us per 4096 inputs, from whole rounds of 256 workgroups
+// (us, 4096 inputs): 128 x 128 tiles two a CU, 28 for one of them and 39 for both; 128 x 256 36.7;
+// 256 x 256 52.
+inline double middle_time(const ProductParams& p) {
+    const int64_t each = (expected_tiles(p, 128) * ((p.n_out + 127) / 128) + CUS - 1) / CUS;
+    return (double)(each / 2) * 39 + (double)(each % 2) * 28;
+}
+inline double large_time(const ProductParams& p, int rt, int64_t n_out) {
+    const int64_t rounds = (expected_tiles(p, 32 * rt) * ((n_out + LARGE_COLS - 1) / LARGE_COLS) + CUS - 1) / CUS;
+    return (double)rounds * (rt == 8 ? 52 : 36.7);
+}
+
 template <typename OT> hipError_t launch_product(const ProductParams& p, hipStream_t s) {
-    return launch_tiles<OT, 1, 1>(p, s);
+    if (p.x) return launch_small<OT, QUANTISED>(p, s);
+    const int64_t m = typical_rows(p.rows, p.n_groups), runs = (p.n_out + 15) / 16;
+    if (p.offsets ? m < held_rows(p.n_in) : m <= held_rows(p.n_in)) return launch_small<OT, STAGED>(p, s);
+    if (p.offsets ? m < 8 : m <= 16 || expected_tiles(p, 16) * runs <= 2 * CUS) return launch_small<OT, STREAMED>(p, s);
+    if (expected_tiles(p, 32) * ((p.n_out + 31) / 32) <= CUS) return launch_medium<OT, 32>(p, s);
+    if (expected_tiles(p, 64) * ((p.n_out + 63) / 64) <= 2 * CUS) return launch_medium<OT, 64>(p, s);
+    const double middle = middle_time(p), low = large_time(p, 4, p.n_out), high = large_time(p, 8, p.n_out);
+    // Whole rounds of 256 x 256 tiles, and 128 x 256 ones for the columns left over.
+    const int64_t row_tiles = expected_tiles(p, 256), whole = row_tiles * ((p.n_out + LARGE_COLS - 1) / LARGE_COLS) / CUS;
+    const int64_t cols = whole * CUS / row_tiles * LARGE_COLS;
+    if (!p.offsets && cols > 0 && cols < p.n_out) {
+        const double both = large_time(p, 8, cols) + large_time(p, 4, p.n_out - cols);
+        if (both < 0.95 * high && both < low && both < middle) {
+            ProductParams left = p, right = p;
+            left.n_out = (int)cols;
+            right.n_out = (int)(p.n_out - cols);
+            right.wc += cols * p.n_in;
+            right.ws += cols;
+            right.y = static_cast<char*>(p.y) + cols * OT::bytes;
+            const hipError_t e = launch_large<OT, 8>(left, s);
+            return e == hipSuccess ? launch_large<OT, 4>(right, s) : e;
+        }
+    }
+    if (middle <= low && middle < high) return launch_middle<OT>(p, s);
+    return low < high ? launch_large<OT, 4>(p, s) : launch_large<OT, 8>(p, s);
 }
 
 hipError_t product(int dtype, const ProductParams& p, hipStream_t s) {
@@ -216,7 +720,7 @@ using namespace exl3::i8;
 
 int64_t exl3_int8_workspace_bytes(int32_t rows, int32_t n_groups, int32_t n_in) {
     if (rows < 0 || n_groups < 1 || bad_row(n_in)) return EXL3_EINVAL;
-    return codes_bytes(rows, n_in) + (((int64_t)rows * 4 + 255) & ~int64_t(255));
+    return quantised_inside(rows, n_groups, n_in) ? 0 : codes_bytes(rows, n_in) + (((int64_t)rows * 4 + 255) & ~int64_t(255));
 }
 
 int exl3_int8_matmul(const int8_t* x_codes, const float* x_scales, int32_t rows, const int32_t* offsets,
@@ -229,7 +733,7 @@ int exl3_int8_matmul(const int8_t* x_codes, const float* x_scales, int32_t rows,
     if (!apart({values(y, dtype, 1, size, size)}, {{x_codes, in * n_in}, {x_scales, in * 4}, {codes, w * n_in}, {scales, w * 4},
                {offsets, 4 * ((int64_t)n_groups + 1)}}))
         return EXL3_EINVAL;
-    const ProductParams p = {x_codes, x_scales, offsets, n_groups, rows, codes, scales, n_in, n_out, y};
+    const ProductParams p = {nullptr, 0, x_codes, x_scales, offsets, n_groups, rows, codes, scales, n_in, n_out, y, n_out};
     return product(dtype, p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_EHIP;
 }
 
@@ -247,11 +751,16 @@ int exl3_int8_linear(const void* x, int32_t dtype, int32_t rows, int64_t ldx, co
     if (!apart({values(y, dtype, 1, size, size), {workspace, need}}, {values(x, dtype, rows, n_in, ldx), {codes, w * n_in}, {scales, w * 4},
                {offsets, 4 * ((int64_t)n_groups + 1)}}))
         return EXL3_EINVAL;
-    int8_t* const xc = static_cast<int8_t*>(workspace);
-    float* const xs = reinterpret_cast<float*>(xc + codes_bytes(rows, n_in));
-    const RowsParams q = {x, ldx, nullptr, 0, nullptr, 0, 0.0, rows, n_in, xc, xs, nullptr};
-    if (launch_quantize(dtype, q, (hipStream_t)stream) != hipSuccess) return EXL3_EHIP;
-    const ProductParams p = {xc, xs, offsets, n_groups, rows, codes, scales, n_in, n_out, y};
+    ProductParams p = {x, ldx, nullptr, nullptr, offsets, n_groups, rows, codes, scales, n_in, n_out, y, n_out};
+    if (need > 0) {
+        int8_t* const xc = static_cast<int8_t*>(workspace);
+        float* const xs = reinterpret_cast<float*>(xc + codes_bytes(rows, n_in));
+        const RowsParams q = {x, ldx, nullptr, 0, nullptr, 0, 0.0, rows, n_in, xc, xs, nullptr};
+        if (launch_quantize(dtype, q, (hipStream_t)stream) != hipSuccess) return EXL3_EHIP;
+        p.x = nullptr;
+        p.xc = xc;
+        p.xs = xs;
+    }
     return product(dtype, p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_EHIP;
 }
 

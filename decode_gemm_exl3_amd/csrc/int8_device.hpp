@@ -1,0 +1,152 @@
+// int8_device.hpp - device building blocks of the 8-bit integer kernels (gfx950).
+#pragma once
+#include "pieces_device.hpp"
+#include "tile_device.hpp"
+
+namespace exl3 {
+namespace i8 {
+
+using namespace mx;  // element types, pieces, row tiles of groups
+
+// Waits for all but `PENDING` of this wave's loads from memory; with LDS for its reads of LDS too.
+template <int PENDING, bool LDS> __device__ inline void wait_loads() {
+    static_assert(PENDING < 64, "a wait counts to 63");
+    __builtin_amdgcn_s_waitcnt((LDS ? 0x0070 : 0x0F70) | (PENDING & 15) | ((PENDING >> 4) << 14));
+}
+
+// A product, rounded to fp32: without this a conversion to fp16 that follows would become one
+// instruction with it and round the exact product, about 1 in 2^13 of them to another value.
+__device__ inline float rounded(float v) {
+    asm("" : "+v"(v));
+    return v;
+}
+
+// Codes of N values u, in N / 4 dwords: 127 u / largest, rounded to the nearest, ties to even,
+// exactly.  q = u * inverse with inverse = fl(127 / largest) is within 1.6e-5 of the quotient
+// (two roundings of a number up to 127), so only a piece that holds a q nearer than 2^-15 to a
+// tie is rounded again, from the quotient in 64 bits.  (127 u has at most 31 bits, so that a
+// quotient that is a tie comes out as one, and any other is far enough away.)  Ties are common
+// in 16-bit types: u = largest / 2 is one.
+template <int N> __device__ inline void code_piece(const float (&u)[N], float largest, float inverse, uint32_t (&out)[N / 4]) {
+    constexpr float ROUND = 12582912.f;  // 1.5 * 2^23: a sum's low byte is the rounded value
+    uint32_t bits[N];
+    float nearest = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float q = u[i] * inverse, m = q + ROUND;
+        bits[i] = __builtin_bit_cast(uint32_t, m);
+        nearest = fmaxf(nearest, fabsf(q - (m - ROUND)));
+    }
+    // largest below 2^-100: 127 / largest may be infinite
+    if (nearest > 0.5f - 0x1p-15f || largest < 0x1p-100f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            bits[i] = largest > 0.f ? (uint32_t)(int)__builtin_rint(127.0 * (double)u[i] / (double)largest) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        // bytes 0 of two, then of the other two on top
+        const uint32_t lo = __builtin_amdgcn_perm(bits[i + 1], bits[i], 0x0C0C0400u), hi = __builtin_amdgcn_perm(bits[i + 3], bits[i + 2], 0x04000C0Cu);
+        out[i / 4] = lo | hi;
+    }
+}
+
+// The magnitudes' bits of a piece's values join `amax` (NaN and infinity have an all-ones
+// exponent: magnitudes order like their bits).
+template <int N> __device__ inline uint32_t amax_piece(uint32_t amax, const float (&u)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, u[i]) & 0x7FFFFFFFu;
+        amax = amax > b ? amax : b;
+    }
+    return amax;
+}
+constexpr uint32_t NOT_FINITE = 0x7F800000u;  // and above
+
+// A row's scale from the bits of its largest magnitude; `root`: what a norm divides by.
+__device__ inline float row_scale(uint32_t amax, double root) {
+    if (amax >= NOT_FINITE) return __builtin_nanf("");
+    return amax == 0 ? 0.f : (float)((double)__builtin_bit_cast(float, amax) / 127.0 / root);
+}
+
+// Over the lanes of a wave, in each of them: DPP moves inside rows of 16 lanes, then each
+// row's last lane to the rows behind it; the last lane has everything.
+template <int CTRL, int ROWS> __device__ inline uint32_t dpp(uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, ROWS == 0xF); }
+__device__ inline uint32_t wave_max(uint32_t v) {
+    auto join = [&](uint32_t o) { v = v > o ? v : o; };
+    join(dpp<0x111, 0xF>(v));  // row_shr:1
+    join(dpp<0x112, 0xF>(v));  // row_shr:2
+    join(dpp<0x114, 0xF>(v));  // row_shr:4
+    join(dpp<0x118, 0xF>(v));  // row_shr:8
+    join(dpp<0x142, 0xA>(v));  // row_bcast:15 into rows 1 and 3
+    join(dpp<0x143, 0xC>(v));  // row_bcast:31 into rows 2 and 3
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+template <int CTRL, int ROWS> __device__ inline double dpp(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)dpp<CTRL, ROWS>((uint32_t)b) | ((uint64_t)dpp<CTRL, ROWS>((uint32_t)(b >> 32)) << 32));
+}
+__device__ inline double wave_sum(double v) {
+    v += dpp<0x111, 0xF>(v);
+    v += dpp<0x112, 0xF>(v);
+    v += dpp<0x114, 0xF>(v);
+    v += dpp<0x118, 0xF>(v);
+    v += dpp<0x142, 0xA>(v);
+    v += dpp<0x143, 0xC>(v);
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63) |
+                                          ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63) << 32));
+}
+
+// Tile `index` of a product: its group, first row, row count and output tile, of tiles of bm rows in
+// col_tiles runs of outputs.  rows == 0: no such tile.  With groups a group's tiles follow each
+// other, in bands of row tiles as above, so that a weight comes from memory once (in bands
+// over all groups' row tiles those that a band's border splits came twice: 16384 rows in 64 groups
+// 2048 -> 2816 read 590 MB, of which the rows and weights are 403).
+struct ProductTile {
+    int group, row0, rows, col;
+};
+__device__ inline ProductTile product_tile(const int* offsets, int n_groups, int rows, int index, int bm, int row_tiles, int col_tiles) {
+    int row, col;
+    if (!offsets) {
+        if (!tile_of(index, row_tiles, col_tiles, &row, &col)) return ProductTile{0, 0, 0, 0};
+        return ProductTile{0, row * bm, max(min(bm, rows - row * bm), 0), col};
+    }
+    const int lane = threadIdx.x & 63;
+    constexpr int U = 4;  // scans whose offsets are asked for together
+    int before = 0;
+    for (int g0 = 0; g0 <= n_groups; g0 += 64 * U) {
+        int lo[U], hi[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int g = g0 + 64 * u + lane;
+            lo[u] = hi[u] = 0;
+            if (g <= n_groups) {
+                lo[u] = offsets[g];
+                hi[u] = g < n_groups ? offsets[g + 1] : rows;
+            }
+        }
+        wait_loads<0, false>();  // for those that are not used too: nothing waits for them behind this
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (g0 + 64 * u > n_groups) break;
+            const int first = clamp_row(lo[u], rows), end = clamp_row(hi[u], rows);
+            const int count = end > first ? end - first : 0;
+            const int tiles = (count + bm - 1) / bm;
+            const int sum = before + wave_scan(tiles);
+            const uint64_t past = __ballot((int64_t)sum * col_tiles > index);
+            if (past) {
+                const int at = __ffsll((unsigned long long)past) - 1;
+                const int mine = __builtin_amdgcn_readlane(tiles, at), start = __builtin_amdgcn_readlane(sum, at) - mine;
+                tile_of(index - start * col_tiles, mine, col_tiles, &row, &col);
+                return ProductTile{g0 + 64 * u + at, __builtin_amdgcn_readlane(first, at) + row * bm,
+                                   min(bm, __builtin_amdgcn_readlane(count, at) - row * bm), col};
+            }
+            before = __builtin_amdgcn_readlane(sum, 63);
+        }
+    }
+    return ProductTile{0, 0, 0, 0};
+}
+
+}  // namespace i8
+}  // namespace exl3

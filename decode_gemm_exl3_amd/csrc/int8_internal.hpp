@@ -13,13 +13,6 @@ constexpr int MAX_ROW = 1 << 24;                // values of a row that the row 
 constexpr int64_t MAX_ROWS = (int64_t)1 << 40;
 constexpr int64_t MAX_GRID = 1 << 20;           // workgroups of a row operator, which take row after row
 
-// A product, rounded to fp32: without this a conversion to fp16 that follows would become one
-// instruction with it and round the exact product, about 1 in 2^13 of them to another value.
-__device__ inline float rounded(float v) {
-    asm("" : "+v"(v));
-    return v;
-}
-
 // Rows to codes and scales; with a weight, after the norm.
 struct RowsParams {
     const void* x;

@@ -2,13 +2,11 @@
 // without, and codes back to values (gfx950).
 #include <hip/hip_runtime.h>
 
+#include "int8_device.hpp"
 #include "int8_internal.hpp"
-#include "pieces_device.hpp"
 
 namespace exl3 {
 namespace i8 {
-
-using namespace mx;  // element types, pieces
 
 // ---- quantise, norm ----
 //
@@ -17,49 +15,7 @@ using namespace mx;  // element types, pieces
 // round(127 u / A) of u = h * weight: the row's 1 / rms is in u and A alike and cancels, so
 // it enters the scale alone.
 //
-// The codes are exact: q = u * fl(127 / A) is within 1.6e-5 of 127 u / A (two roundings
-// of a number up to 127), so only a piece that holds a q nearer than 2^-15 to a tie is
-// rounded again, from the quotient in 64 bits.  Ties are common in 16-bit types (u = A / 2
-// is one for every A).
-//
 // Squares are summed in 64 bits: those of fp32 and bf16 values pass the range of fp32.
-
-// Codes of the N values u of a piece, in N / 4 dwords.
-template <int N> __device__ inline void code_piece(const float (&u)[N], float largest, float inverse, uint32_t (&out)[N / 4]) {
-    constexpr float ROUND = 12582912.f;  // 1.5 * 2^23: a sum's low byte is the rounded value
-    uint32_t bits[N];
-    float nearest = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float q = u[i] * inverse, m = q + ROUND;
-        bits[i] = __builtin_bit_cast(uint32_t, m);
-        nearest = fmaxf(nearest, fabsf(q - (m - ROUND)));
-    }
-    // largest below 2^-100: 127 / largest may be infinite
-    if (nearest > 0.5f - 0x1p-15f || largest < 0x1p-100f) {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            bits[i] = largest > 0.f ? (uint32_t)(int)__builtin_rint(127.0 * (double)u[i] / (double)largest) : 0u;
-    }
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-        out[i / 4] = (bits[i] & 255u) | ((bits[i + 1] & 255u) << 8) | ((bits[i + 2] & 255u) << 16) | (bits[i + 3] << 24);
-}
-
-// The largest of v, and the sum of s, over the lanes of a wave.
-__device__ inline uint32_t wave_max(uint32_t v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)v, d);
-        v = v > o ? v : o;
-    }
-    return v;
-}
-__device__ inline double wave_sum(double s) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
-    return s;
-}
 
 // N consecutive weights from column c on.
 template <int N> __device__ inline void load_weights(const void* w, int dtype, int c, float (&out)[N]) {
@@ -133,11 +89,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rows_kernel(con
                     v[i] *= w[i];
                 }
             }
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint32_t b = __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu;
-                amax = amax > b ? amax : b;
-            }
+            amax = amax_piece<N>(amax, v);
         };
         if constexpr (P > 0) {
 #pragma unroll
@@ -167,13 +119,9 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rows_kernel(con
                 if (NORM) squares += wave_squares[parity][w];
             }
         }
-        const bool bad = amax >= 0x7F800000u;  // a NaN or an infinity
+        const bool bad = amax >= NOT_FINITE;
         const float largest = __builtin_bit_cast(float, amax), inverse = 127.f / largest;
-        if (thread == 0) {
-            double scale = (double)largest / 127.0;
-            if (NORM) scale /= sqrt(squares / p.n + p.eps);
-            p.scales[row] = bad ? __builtin_nanf("") : (amax == 0 ? 0.f : (float)scale);
-        }
+        if (thread == 0) p.scales[row] = row_scale(amax, NORM ? sqrt(squares / p.n + p.eps) : 1.0);
         auto store = [&](int c, const float (&v)[N]) {
             uint32_t out[N / 4];
             if (bad) {

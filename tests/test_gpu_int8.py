@@ -495,3 +495,16 @@ def test_weights_of_more_than_32_bits(ex, rows):
         assert torch.equal(y[a:b], ex.int8_matmul(xc[a:b].clone(), xs[a:b].clone(), w[g], scales[g], torch.float32)), g
     ref = (xc[1:3].double().cpu() @ w[-1].double().cpu().T).float()
     assert torch.equal(y[1:3].cpu(), ref)
+
+
+# 256 x 256 and 128 x 256 tiles, several a workgroup, whole rounds of the former with the latter behind them, and groups in either
+@pytest.mark.parametrize("m, n_in, n_out, dtype", [(2050, 272, 20003, "bf16"), (2050, 16, 20003, "fp32"), (1030, 144, 40001, "fp16"), (4100, 256, 5001, "fp32"),
+                                                    (2048, 400, 28672, "bf16"), (2048, 272, 28669, "fp16"), (770, 1040, 28671, "fp32"), (1500, 528, 4100, "bf16")])
+def test_linear_of_several_tiles_a_workgroup(ex, m, n_in, n_out, dtype):
+    check_product(ex, m, n_in, n_out, dtype)
+
+
+@pytest.mark.parametrize("counts, behind, n_in, n_out, dtype", [([700, 0, 900, 450, 1, 256, 257], 300, 144, 9001, "fp16"), ([3000, 20, 1500], 0, 272, 12003, "bf16"),
+                                                                 ([260] * 12, 5, 400, 2816, "fp32"), ([0, 0, 5000], 0, 16, 7000, "bf16"), ([0, 0], 3000, 48, 9000, "fp32")])
+def test_groups_of_several_tiles_a_workgroup(ex, counts, behind, n_in, n_out, dtype):
+    check_groups(ex, counts, behind, n_in, n_out, dtype)
