@@ -19,31 +19,96 @@ struct Params {
     int blocks;        // workgroups of the loss's first launch
     float* part;       // [blocks][experts]: sums of probabilities
     int* part_counts;  // [blocks][experts + 1]
+    uint64_t* along;   // of the second launch's workgroups: counts times sums, as fp64
+    int* arrived;      // how many of them are done
     float* loss;
     int* counts;
     const float* dloss;
     void* dlogits;
 };
 
-constexpr int THREADS = 256, WAVES = THREADS / 64;
-constexpr int MAX_BLOCKS = 256;
+constexpr int SUM_THREADS = 1024, FINAL_THREADS = 1024, BACKWARD_THREADS = 256;
+constexpr int MAX_BLOCKS = 256;          // workgroups of the loss's first launch
+constexpr int FINAL_EXPERTS = 64;        // experts of a workgroup of its second
 
 // A token's logits lie in LANES lanes (a power of two), Q pieces of N = 16 bytes each:
 // piece q of lane l is columns (q * LANES + l) * N and on.  A wave holds 64 / LANES tokens.
 // LANES * Q * N >= experts.
 
+// v joined over the LANES lanes of a token, in each of them.
+template <int CTRL> __device__ inline float moved(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+template <int LANES, typename F> __device__ inline float over_lanes(float v, F join) {
+    if constexpr (LANES > 1) v = join(v, moved<0xB1>(v));    // lanes 1 0 3 2
+    if constexpr (LANES > 2) v = join(v, moved<0x4E>(v));    // lanes 2 3 0 1
+    if constexpr (LANES > 4) v = join(v, moved<0x141>(v));   // half rows mirrored: the other four
+    if constexpr (LANES > 8) v = join(v, moved<0x140>(v));   // rows mirrored: the other eight
+    // swaps leave the lower rows' values in one result and the upper ones' in the other
+    if constexpr (LANES > 16) {
+        const uint32_t w = __builtin_bit_cast(uint32_t, v);
+        const auto both = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+        const uint32_t lower = both[0], upper = both[1];
+        v = join(__builtin_bit_cast(float, lower), __builtin_bit_cast(float, upper));
+    }
+    if constexpr (LANES > 32) {
+        const uint32_t w = __builtin_bit_cast(uint32_t, v);
+        const auto both = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+        const uint32_t lower = both[0], upper = both[1];
+        v = join(__builtin_bit_cast(float, lower), __builtin_bit_cast(float, upper));
+    }
+    return v;
+}
+
+// 16 bytes of a row, or what is left of it.  Rows that are no whole pieces (VEC false) start at any
+// value: unaligned loads and stores.
+template <typename T, bool VEC> __device__ inline u32x4_t load_columns(const void* base, int64_t at, int left) {
+    if constexpr (VEC) return load_piece<T, true>(base, at, left);
+    if (left < 16 / T::bytes) return load_piece<T, false>(base, at, left);
+    u32x4_t r;
+    __builtin_memcpy(&r, static_cast<const char*>(base) + at * T::bytes, 16);
+    return r;
+}
+template <typename T, bool VEC> __device__ inline void store_columns(void* base, int64_t at, int left, const u32x4_t r) {
+    if constexpr (VEC) return store_piece<T, true, false>(base, at, left, r);
+    if (left < 16 / T::bytes) return store_piece<T, false, false>(base, at, left, r);
+    __builtin_memcpy(static_cast<char*>(base) + at * T::bytes, &r, 16);
+}
+
+// What a lane asks for of a token: its pieces of the logits, and the token's slot `lane`.
+template <int Q> struct Asked {
+    u32x4_t piece[Q];
+    int64_t id;
+};
+__device__ inline int64_t load_id(const Params& p, int64_t at) {
+    return p.id_bytes == 8 ? static_cast<const int64_t*>(p.ids)[at] : (int64_t) static_cast<const int*>(p.ids)[at];
+}
+template <typename T, int LANES, int Q, bool VEC> __device__ inline Asked<Q> ask(const Params& p, int token, int lane) {
+    constexpr int N = 16 / T::bytes;
+    Asked<Q> r;
+    r.id = -1;
+    if (token < p.tokens && lane < p.top_k) r.id = load_id(p, (int64_t)token * p.top_k + lane);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const int c = (q * LANES + lane) * N;
+        r.piece[q] = u32x4_t{0, 0, 0, 0};
+        if (token < p.tokens && c < p.experts) r.piece[q] = load_columns<T, VEC>(p.logits, (int64_t)token * p.experts + c, p.experts - c);
+    }
+    return r;
+}
+
 // Does the token have a slot that is kept?  All lanes of the wave come here; lanes of a
 // token share its slots out.  COUNT: kept slots go into the histogram.
-template <int LANES, bool COUNT> __device__ inline bool counts_token(const Params& p, int token, bool live, int lane, int* hist) {
+template <int LANES, bool COUNT> __device__ inline bool counts_token(const Params& p, int token, int64_t id, int lane, int* hist) {
     bool kept = false;
-    for (int j = lane; j < p.top_k; j += LANES) {
-        if (!live) break;
-        const int64_t at = (int64_t)token * p.top_k + j;
-        const int64_t id = p.id_bytes == 8 ? static_cast<const int64_t*>(p.ids)[at] : (int64_t) static_cast<const int*>(p.ids)[at];
+    for (int j = lane;;) {
         if (id >= 0 && id < p.experts) {
             kept = true;
             if (COUNT) atomicAdd(&hist[(int)id], 1);
         }
+        j += LANES;
+        if (token >= p.tokens || j >= p.top_k) break;
+        id = load_id(p, (int64_t)token * p.top_k + j);
     }
     if constexpr (LANES == 1) return kept;
     const uint64_t all = __ballot(kept);
@@ -52,38 +117,46 @@ template <int LANES, bool COUNT> __device__ inline bool counts_token(const Param
     return ((all >> first) & ((1ull << (LANES & 63)) - 1)) != 0;
 }
 
+// e^d of d <= 0 as 2^y, y = fl(d / ln 2); 0 below -104, where fp32 ends (v_exp_f32 gives 0 below
+// -87 already).  y is off by up to its own size times 2^-24, which makes a relative 1.2 |d| 2^-24 of
+// the result: less than a tenth of a step of the 16-bit gradients, and of their loss that far down
+// (|d| = 10) 7e-7 a token.  For fp32 logits the result takes (1 + (d / ln 2 - y) ln 2) too, four instructions.
+template <typename T> __device__ inline float exp_below(float d) {
+    constexpr float INV_LN2 = 1.44269502f, INV_LN2_LOW = 1.92596299e-8f, LN2 = 0.693147182f;  // 1 / ln 2 in two parts
+    d = fmaxf(d, -104.f);
+    const float y = d * INV_LN2, e = __builtin_amdgcn_exp2f(y);
+    if constexpr (T::bytes == 2) return e;
+    const float rest = __builtin_fmaf(d, INV_LN2_LOW, __builtin_fmaf(d, INV_LN2, -y));
+    return __builtin_fmaf(e * LN2, rest, e);
+}
+
 // The softmax of a token's logits: probabilities of this lane's columns, 0 behind the last.
-template <typename T, int LANES, int Q, bool VEC>
-__device__ inline void softmax(const Params& p, int token, bool live, int lane, float (&v)[Q][16 / T::bytes]) {
+template <typename T, int LANES, int Q> __device__ inline void softmax(const Params& p, const u32x4_t (&piece)[Q], int lane, float (&v)[Q][16 / T::bytes]) {
     constexpr int N = 16 / T::bytes;
     const float lowest = -__builtin_inff();
     float top = lowest;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        const int c = (q * LANES + lane) * N;
-        u32x4_t r = {0, 0, 0, 0};
-        const bool in = live && c < p.experts;
-        if (in) r = load_piece<T, VEC>(p.logits, (int64_t)token * p.experts + c, p.experts - c);
+    for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            v[q][i] = in && c + i < p.experts ? piece_value<T>(r, i) : lowest;
-            top = fmaxf(top, v[q][i]);
+            v[q][i] = (q * LANES + lane) * N + i < p.experts ? piece_value<T>(piece[q], i) : lowest;
+            top = __builtin_elementwise_maximum(top, v[q][i]);  // a NaN stays one
         }
-    }
-#pragma unroll
-    for (int d = 1; d < LANES; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-    if (top == lowest) top = 0.f;  // nothing but -infinity: exp gives zeros (a NaN stays one)
+    top = over_lanes<LANES>(top, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
+    const bool bad = !(top < __builtin_inff());  // a NaN or +infinity: all of the token's are NaN
+    if (top == lowest) top = 0.f;                // nothing but -infinity: exp gives zeros
     float sum = 0.f;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            v[q][i] = expf(v[q][i] - top);
+            v[q][i] = exp_below<T>(v[q][i] - top);
             sum += v[q][i];
         }
-#pragma unroll
-    for (int d = 1; d < LANES; d *= 2) sum += __shfl_xor(sum, d);
-    const float inverse = sum == 0.f ? 0.f : 1.f / sum;
+    sum = over_lanes<LANES>(sum, [](float a, float b) { return a + b; });
+    // 1 / sum to a step of fp32: an estimate and one step of Newton's
+    const float guess = __builtin_amdgcn_rcpf(sum), newton = __builtin_fmaf(__builtin_fmaf(-sum, guess, 1.f), guess, guess);
+    const float inverse = bad ? __builtin_nanf("") : sum == 0.f ? 0.f : newton;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
@@ -97,11 +170,12 @@ __device__ inline float loss_of(const Params& p, int tokens, double along) {
     return (float)(p.coefficient * p.experts * along / (of * of * p.top_k));
 }
 
-// Sum over the threads of a workgroup.
+// Sum over the threads of a workgroup, in each of them.
 template <int COUNT> __device__ inline double block_sum(double v) {
     __shared__ double part[COUNT / 64];
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    __syncthreads();  // a sum before this one is read
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
     v = 0.0;
@@ -111,26 +185,30 @@ template <int COUNT> __device__ inline double block_sum(double v) {
 }
 
 // Sums of probabilities and counts of the tokens of a workgroup: each lane adds up its
-// columns over the wave's tokens in registers.  One workgroup alone writes the results.
-template <typename T, int LANES, int Q, bool VEC> __global__ __launch_bounds__(THREADS) void sum_kernel(const Params p) {
-    constexpr int N = 16 / T::bytes, EACH = 64 / LANES;
+// columns over the wave's tokens in registers; the next token's logits and slots are on their
+// way meanwhile.  One workgroup alone writes the results.
+template <typename T, int LANES, int Q, bool VEC> __global__ __launch_bounds__(SUM_THREADS) void sum_kernel(const Params p) {
+    constexpr int N = 16 / T::bytes, EACH = 64 / LANES, WAVES = SUM_THREADS / 64;
     __shared__ int hist[EXL3_MOE_MAX_EXPERTS + 1];
     __shared__ float sums[WAVES][LANES * Q * N];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & (LANES - 1), slot = (threadIdx.x & 63) / LANES;
-    for (int e = threadIdx.x; e <= p.experts; e += THREADS) hist[e] = 0;
+    const int step = p.blocks * WAVES * EACH;
+    int t0 = (blockIdx.x * WAVES + wave) * EACH;
+    Asked<Q> next = ask<T, LANES, Q, VEC>(p, t0 + slot, lane);
+    for (int e = threadIdx.x; e <= p.experts; e += SUM_THREADS) hist[e] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.blocks > 1) *p.arrived = 0;
     __syncthreads();
     float acc[Q][N];
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[q][i] = 0.f;
-    const int step = p.blocks * WAVES * EACH;
-    for (int t0 = (blockIdx.x * WAVES + wave) * EACH; t0 < p.tokens; t0 += step) {
-        const int token = t0 + slot;
-        const bool live = token < p.tokens;
-        const bool valid = counts_token<LANES, true>(p, token, live, lane, hist);
+    for (; t0 < p.tokens; t0 += step) {
+        const Asked<Q> now = next;
+        next = ask<T, LANES, Q, VEC>(p, t0 + step + slot, lane);
+        const bool valid = counts_token<LANES, true>(p, t0 + slot, now.id, lane, hist);
         float v[Q][N];
-        softmax<T, LANES, Q, VEC>(p, token, live, lane, v);
+        softmax<T, LANES, Q>(p, now.piece, lane, v);
         if (valid) {
 #pragma unroll
             for (int q = 0; q < Q; ++q)
@@ -149,7 +227,7 @@ template <typename T, int LANES, int Q, bool VEC> __global__ __launch_bounds__(T
         }
     __syncthreads();
     double along = 0.0;
-    for (int e = threadIdx.x; e < p.experts; e += THREADS) {
+    for (int e = threadIdx.x; e < p.experts; e += SUM_THREADS) {
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) s += sums[w][e];
@@ -165,87 +243,124 @@ template <typename T, int LANES, int Q, bool VEC> __global__ __launch_bounds__(T
         if (threadIdx.x == 0) p.part_counts[(int64_t)blockIdx.x * (p.experts + 1) + p.experts] = hist[p.experts];
         return;
     }
-    along = block_sum<THREADS>(along);
+    along = block_sum<SUM_THREADS>(along);
     if (threadIdx.x == 0) {
         p.counts[p.experts] = hist[p.experts];
         *p.loss = loss_of(p, hist[p.experts], along);
     }
 }
 
-// The workgroups' sums to the loss and the counts, in the order of the workgroups.
-constexpr int FINAL_THREADS = 1024;
+// The workgroups' sums to the loss and the counts: a workgroup takes 64 experts, 16 threads each.
+// The last one to arrive adds up what they made, in their order.
 __global__ __launch_bounds__(FINAL_THREADS) void loss_kernel(const Params p) {
-    __shared__ float sums[FINAL_THREADS];
-    __shared__ int counts[FINAL_THREADS];
+    constexpr int SLICES = FINAL_THREADS / FINAL_EXPERTS, EACH = MAX_BLOCKS / SLICES;
+    static_assert(FINAL_EXPERTS == 64 && EXL3_MOE_MAX_EXPERTS / FINAL_EXPERTS <= 64, "an expert, and a workgroup, a lane");
+    __shared__ float sums[SLICES][FINAL_EXPERTS];
+    __shared__ int counts[SLICES][FINAL_EXPERTS];
     __shared__ int tokens;
-    // `slices` threads an expert, each over every slices-th workgroup
-    const int slices = FINAL_THREADS / p.experts, e = threadIdx.x / slices, k = threadIdx.x - e * slices;
+    __shared__ bool last;
+    __shared__ double sum_of_all;
+    const int lane = threadIdx.x & 63, k = threadIdx.x >> 6, e = blockIdx.x * FINAL_EXPERTS + lane;
+    if (threadIdx.x == 0) tokens = 0;
+    float part[EACH];
+    int part_counts[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int b = k + i * SLICES;
+        const bool in = e < p.experts && b < p.blocks;
+        part[i] = in ? p.part[(int64_t)b * p.experts + e] : 0.f;
+        part_counts[i] = in ? p.part_counts[(int64_t)b * (p.experts + 1) + e] : 0;
+    }
+    const int mine = threadIdx.x < p.blocks ? p.part_counts[(int64_t)threadIdx.x * (p.experts + 1) + p.experts] : 0;  // tokens
     float s = 0.f;
     int c = 0;
-    if (threadIdx.x == 0) tokens = 0;
-    if (e < p.experts)
-        for (int b = k; b < p.blocks; b += slices) {
-            s += p.part[(int64_t)b * p.experts + e];
-            c += p.part_counts[(int64_t)b * (p.experts + 1) + e];
-        }
-    sums[threadIdx.x] = s;
-    counts[threadIdx.x] = c;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        s += part[i];
+        c += part_counts[i];
+    }
+    sums[k][lane] = s;
+    counts[k][lane] = c;
     __syncthreads();
-    if (threadIdx.x < p.blocks) atomicAdd(&tokens, p.part_counts[(int64_t)threadIdx.x * (p.experts + 1) + p.experts]);
-    double along = 0.0;
-    if (threadIdx.x < p.experts) {
+    if (mine) atomicAdd(&tokens, mine);
+    if (threadIdx.x < 64) {
         s = 0.f;
         c = 0;
-        for (int i = 0; i < slices; ++i) {
-            s += sums[threadIdx.x * slices + i];
-            c += counts[threadIdx.x * slices + i];
+#pragma unroll
+        for (int i = 0; i < SLICES; ++i) {
+            s += sums[i][lane];
+            c += counts[i][lane];
         }
-        p.counts[threadIdx.x] = c;
-        along = (double)c * s;
+        if (e < p.experts) p.counts[e] = c;
+        double along = (double)c * s;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) along += __shfl_xor(along, d);
+        if (threadIdx.x == 0) {
+            last = true;
+            if (gridDim.x > 1) {
+                __hip_atomic_store(&p.along[blockIdx.x], __builtin_bit_cast(uint64_t, along), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                last = __hip_atomic_fetch_add(p.arrived, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+            }
+        }
+        if (gridDim.x > 1 && __builtin_amdgcn_readfirstlane(last)) {
+            along = 0.0;
+            if (threadIdx.x < gridDim.x)
+                along = __builtin_bit_cast(double, __hip_atomic_load(&p.along[threadIdx.x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) along += __shfl_xor(along, d);
+        }
+        sum_of_all = along;
     }
-    along = block_sum<FINAL_THREADS>(along);  // its barrier also ends the count of tokens
-    if (threadIdx.x == 0) {
+    __syncthreads();
+    if (threadIdx.x == 0 && last) {
         p.counts[p.experts] = tokens;
-        *p.loss = loss_of(p, tokens, along);
+        *p.loss = loss_of(p, tokens, sum_of_all);
     }
 }
 
 // dlogits: the shares of this lane's columns stay in registers over all its tokens.
-template <typename T, int LANES, int Q, bool VEC> __global__ __launch_bounds__(THREADS) void backward_kernel(const Params p) {
-    constexpr int N = 16 / T::bytes, EACH = 64 / LANES;
+template <typename T, int LANES, int Q, bool VEC> __global__ __launch_bounds__(BACKWARD_THREADS) void backward_kernel(const Params p) {
+    constexpr int N = 16 / T::bytes, EACH = 64 / LANES, WAVES = BACKWARD_THREADS / 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & (LANES - 1), slot = (threadIdx.x & 63) / LANES;
-    const int tokens = p.counts[p.experts];
-    const double of = tokens > 0 ? tokens : 1;
-    const float factor = (float)(*p.dloss * p.coefficient * (p.experts / of));
-    float share[Q][N];
+    const int step = gridDim.x * WAVES * EACH;
+    int t0 = (blockIdx.x * WAVES + wave) * EACH;
+    Asked<Q> next = ask<T, LANES, Q, VEC>(p, t0 + slot, lane);
+    int counts[Q][N];
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = (q * LANES + lane) * N + i;
-            share[q][i] = c < p.experts ? (float)(p.counts[c] / (of * p.top_k)) : 0.f;
+            counts[q][i] = c < p.experts ? p.counts[c] : 0;
         }
-    const int step = gridDim.x * WAVES * EACH;
-    for (int t0 = (blockIdx.x * WAVES + wave) * EACH; t0 < p.tokens; t0 += step) {
+    const int tokens = p.counts[p.experts];
+    const double of = tokens > 0 ? tokens : 1, each = 1.0 / (of * p.top_k);
+    const float factor = (float)(*p.dloss * p.coefficient * (p.experts / of));
+    float share[Q][N];
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int i = 0; i < N; ++i) share[q][i] = (float)(counts[q][i] * each);
+    for (; t0 < p.tokens; t0 += step) {
         const int token = t0 + slot;
-        const bool live = token < p.tokens;
-        const bool valid = counts_token<LANES, false>(p, token, live, lane, nullptr);
+        const Asked<Q> now = next;
+        next = ask<T, LANES, Q, VEC>(p, token + step, lane);
+        const bool valid = counts_token<LANES, false>(p, token, now.id, lane, nullptr);
         float v[Q][N];
-        softmax<T, LANES, Q, VEC>(p, token, live, lane, v);
+        softmax<T, LANES, Q>(p, now.piece, lane, v);
         float along = 0.f;
 #pragma unroll
         for (int q = 0; q < Q; ++q)
 #pragma unroll
             for (int i = 0; i < N; ++i) along += v[q][i] * share[q][i];
-#pragma unroll
-        for (int d = 1; d < LANES; d *= 2) along += __shfl_xor(along, d);
+        along = over_lanes<LANES>(along, [](float a, float b) { return a + b; });
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const int c = (q * LANES + lane) * N;
             float g[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) g[i] = valid ? factor * (v[q][i] * (share[q][i] - along)) : 0.f;
-            if (live && c < p.experts) store_piece<T, VEC, false>(p.dlogits, (int64_t)token * p.experts + c, p.experts - c, round_piece<T>(g));
+            if (token < p.tokens && c < p.experts) store_columns<T, VEC>(p.dlogits, (int64_t)token * p.experts + c, p.experts - c, round_piece<T>(g));
         }
     }
 }
@@ -256,10 +371,11 @@ enum Op { LOSS, BACKWARD };
 
 template <typename T, int LANES, int Q, bool VEC> hipError_t launch(Op op, const Params& p, hipStream_t s) {
     if (op == LOSS) {
-        sum_kernel<T, LANES, Q, VEC><<<p.blocks, THREADS, 0, s>>>(p);
+        sum_kernel<T, LANES, Q, VEC><<<p.blocks, SUM_THREADS, 0, s>>>(p);
     } else {
-        const int64_t blocks = ((int64_t)p.tokens + WAVES * (64 / LANES) - 1) / (WAVES * (64 / LANES));
-        backward_kernel<T, LANES, Q, VEC><<<(unsigned)(blocks < 2048 ? blocks : 2048), THREADS, 0, s>>>(p);
+        constexpr int EACH = BACKWARD_THREADS / LANES;
+        const int64_t blocks = ((int64_t)p.tokens + EACH - 1) / EACH;
+        backward_kernel<T, LANES, Q, VEC><<<(unsigned)(blocks < 1024 ? blocks : 1024), BACKWARD_THREADS, 0, s>>>(p);
     }
     return hipGetLastError();
 }
@@ -290,15 +406,28 @@ hipError_t launch(int dtype, Op op, const Params& p, hipStream_t s) {
     }
 }
 
-// Workgroups of the first launch: one for few logits, else one for each 32 KB of fp32 logits, at most MAX_BLOCKS.
+// Workgroups of the first launch: one for few logits, else one for each 64 KB of fp32 logits, at most MAX_BLOCKS.
 int plan_blocks(int tokens, int experts) {
-    const int64_t blocks = ((int64_t)tokens * experts + 8191) / 8192;
+    const int64_t blocks = ((int64_t)tokens * experts + 16383) / 16384;
     return blocks < 1 ? 1 : blocks > MAX_BLOCKS ? MAX_BLOCKS : (int)blocks;
 }
 
 bool misaligned(const void* ptr, uintptr_t to = 16) { return (reinterpret_cast<uintptr_t>(ptr) & (to - 1)) != 0; }
 int64_t value_bytes(int dtype) { return dtype == EXL3_F32 ? 4 : 2; }
-int64_t sums_bytes(int blocks, int experts) { return ((int64_t)blocks * experts * 4 + 255) & ~int64_t(255); }
+int64_t padded(int64_t bytes) { return (bytes + 255) & ~int64_t(255); }
+int final_blocks(int experts) { return (experts + FINAL_EXPERTS - 1) / FINAL_EXPERTS; }
+// The workspace's parts, one after the other: part, part_counts, along, arrived.
+struct Parts {
+    int64_t counts, along, arrived, bytes;
+};
+Parts parts(int blocks, int experts) {
+    Parts w;
+    w.counts = padded((int64_t)blocks * experts * 4);
+    w.along = w.counts + padded((int64_t)blocks * (experts + 1) * 4);
+    w.arrived = w.along + padded((int64_t)final_blocks(experts) * 8);
+    w.bytes = w.arrived + 256;
+    return w;
+}
 
 // Checks shared by both directions: <= 0 is the call's status.
 int checks(const void* logits, int32_t dtype, const void* ids, int32_t id_bytes, int32_t n_tokens, int32_t top_k, int32_t n_experts,
@@ -321,7 +450,7 @@ using namespace exl3::balance;
 int64_t exl3_moe_balance_workspace_bytes(int32_t n_tokens, int32_t n_experts) {
     if (n_tokens < 0 || n_experts < 1 || n_experts > EXL3_MOE_MAX_EXPERTS) return EXL3_EINVAL;
     const int blocks = plan_blocks(n_tokens, n_experts);
-    return blocks == 1 ? 0 : sums_bytes(blocks, n_experts) + (int64_t)blocks * (n_experts + 1) * 4;
+    return blocks == 1 ? 0 : parts(blocks, n_experts).bytes;
 }
 
 int exl3_moe_balance_loss(const void* logits, int32_t dtype, const void* ids, int32_t id_bytes, int32_t n_tokens,
@@ -337,11 +466,19 @@ int exl3_moe_balance_loss(const void* logits, int32_t dtype, const void* ids, in
         return EXL3_EINVAL;
     const int blocks = plan_blocks(n_tokens, n_experts);
     char* const ws = static_cast<char*>(workspace);
-    const Params p = {logits, ids, id_bytes, n_tokens, top_k, n_experts, coefficient, blocks, reinterpret_cast<float*>(ws),
-                      reinterpret_cast<int*>(ws + (blocks > 1 ? sums_bytes(blocks, n_experts) : 0)), loss, counts, nullptr, nullptr};
+    const Parts w = parts(blocks, n_experts);
+    Params p = {logits, ids, id_bytes, n_tokens, top_k, n_experts, coefficient, blocks};
+    p.loss = loss;
+    p.counts = counts;
+    if (blocks > 1) {
+        p.part = reinterpret_cast<float*>(ws);
+        p.part_counts = reinterpret_cast<int*>(ws + w.counts);
+        p.along = reinterpret_cast<uint64_t*>(ws + w.along);
+        p.arrived = reinterpret_cast<int*>(ws + w.arrived);
+    }
     hipStream_t s = (hipStream_t)stream;
     if (launch(dtype, LOSS, p, s) != hipSuccess) return EXL3_EHIP;
-    if (blocks > 1) loss_kernel<<<1, FINAL_THREADS, 0, s>>>(p);
+    if (blocks > 1) loss_kernel<<<final_blocks(n_experts), FINAL_THREADS, 0, s>>>(p);
     return hipGetLastError() == hipSuccess ? EXL3_OK : EXL3_EHIP;
 }
 
@@ -355,7 +492,10 @@ int exl3_moe_balance_loss_backward(const float* dloss, const void* logits, int32
     const int64_t size = (int64_t)n_tokens * n_experts * value_bytes(dtype);
     if (!apart({{dlogits, size}}, {{logits, size}, {ids, (int64_t)n_tokens * top_k * id_bytes}, {dloss, 4}, {counts, 4 * ((int64_t)n_experts + 1)}}))
         return EXL3_EINVAL;
-    const Params p = {logits, ids, id_bytes, n_tokens, top_k, n_experts, coefficient, 1, nullptr, nullptr, nullptr, const_cast<int*>(counts), dloss, dlogits};
+    Params p = {logits, ids, id_bytes, n_tokens, top_k, n_experts, coefficient, 1};
+    p.counts = const_cast<int*>(counts);
+    p.dloss = dloss;
+    p.dlogits = dlogits;
     return launch(dtype, BACKWARD, p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_EHIP;
 }
 
