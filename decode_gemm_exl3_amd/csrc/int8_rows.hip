@@ -177,11 +177,20 @@ template <typename T, bool NORM, int WAVES, int P> hipError_t launch(const RowsP
     return hipGetLastError();
 }
 
+// Waves a row and pieces a thread (us): as few pieces as there are where rows are few, since a
+// row is then one latency after the other (256 rows of 2048 bf16, norm: 3.4 with 4 waves of one piece,
+// 6.8 with one wave of 4; one row of 4096 3.3 with 8 x 1, 4.1 with 4 x 4); where they are many, two
+// pieces of four waves or eight (16384 rows of 2048, quantised: 19.6 with 2 x 2, 23.0 with 1 x 4; 2048
+// rows of 8192, norm: 26.9 with 8 x 2, 30.4 with 4 x 4; 2048 rows of 16384: 54.7 with 8 x 4, 65.9 with 16 x 4).
 template <typename T, bool NORM> hipError_t launch_rows(const RowsParams& p, hipStream_t s) {
-    const int pieces = p.n * T::bytes / 16;  // n < 2^24
+    const int pieces = p.n * T::bytes / 16;  // n <= 2^24
+    const bool few = p.rows <= 512;
     if (pieces <= 64) return launch<T, NORM, 1, 1>(p, s);
-    if (pieces <= 256) return launch<T, NORM, 1, 4>(p, s);
-    if (pieces <= 1024) return launch<T, NORM, 4, 4>(p, s);
+    if (pieces <= 128) return launch<T, NORM, 1, 2>(p, s);
+    if (pieces <= 256) return NORM || few ? launch<T, NORM, 4, 1>(p, s) : launch<T, NORM, 2, 2>(p, s);
+    if (pieces <= 512) return few ? launch<T, NORM, 8, 1>(p, s) : launch<T, NORM, 4, 2>(p, s);
+    if (pieces <= 1024) return launch<T, NORM, 8, 2>(p, s);
+    if (pieces <= 2048) return few ? launch<T, NORM, 16, 2>(p, s) : launch<T, NORM, 8, 4>(p, s);
     if (pieces <= 4096) return launch<T, NORM, 16, 4>(p, s);
     return launch<T, NORM, 16, 0>(p, s);
 }

@@ -45,6 +45,19 @@ def test_quantize_sizes(ex, dtype, rows, n, pad):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [16, 512, 1024, 1040, 2048, 2064, 4096, 4112, 8192, 14336])
+def test_many_rows(ex, dtype, n):
+    """More than the few rows that other waves and pieces are chosen for."""
+    rng = np.random.default_rng([21, n])
+    x, r = (R.rows(rng, 700, n, DTYPES[dtype]).cuda() for _ in range(2))
+    x[3, n // 2] = float("nan")
+    codes, scales = ex.int8_quantize(x)
+    ref = R.quantize(x)
+    assert same(codes, ref[0]) and same(scales, ref[1])
+    check_norm(ex, x, torch.from_numpy(1 + 0.3 * rng.standard_normal(n)).to(DTYPES[dtype]).cuda(), r, 1e-6)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("largest", [1.0, 127.0, 254.0, 1.9921875, 93.0, 2.0 ** -14, 2.0 ** -24])
 def test_quantize_ties(ex, dtype, largest):
     """Half of the largest value is a tie for any of them, every odd multiple of 1 / 254 for 127."""
