@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/exl3_balance.h"
+#include "lanes_device.hpp"
 #include "pieces_device.hpp"
 #include "spans.hpp"
 
@@ -34,31 +35,6 @@ constexpr int FINAL_EXPERTS = 64;        // experts of a workgroup of its second
 // A token's logits lie in LANES lanes (a power of two), Q pieces of N = 16 bytes each:
 // piece q of lane l is columns (q * LANES + l) * N and on.  A wave holds 64 / LANES tokens.
 // LANES * Q * N >= experts.
-
-// v joined over the LANES lanes of a token, in each of them.
-template <int CTRL> __device__ inline float moved(float v) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
-}
-template <int LANES, typename F> __device__ inline float over_lanes(float v, F join) {
-    if constexpr (LANES > 1) v = join(v, moved<0xB1>(v));    // lanes 1 0 3 2
-    if constexpr (LANES > 2) v = join(v, moved<0x4E>(v));    // lanes 2 3 0 1
-    if constexpr (LANES > 4) v = join(v, moved<0x141>(v));   // half rows mirrored: the other four
-    if constexpr (LANES > 8) v = join(v, moved<0x140>(v));   // rows mirrored: the other eight
-    // swaps leave the lower rows' values in one result and the upper ones' in the other
-    if constexpr (LANES > 16) {
-        const uint32_t w = __builtin_bit_cast(uint32_t, v);
-        const auto both = __builtin_amdgcn_permlane16_swap(w, w, false, false);
-        const uint32_t lower = both[0], upper = both[1];
-        v = join(__builtin_bit_cast(float, lower), __builtin_bit_cast(float, upper));
-    }
-    if constexpr (LANES > 32) {
-        const uint32_t w = __builtin_bit_cast(uint32_t, v);
-        const auto both = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-        const uint32_t lower = both[0], upper = both[1];
-        v = join(__builtin_bit_cast(float, lower), __builtin_bit_cast(float, upper));
-    }
-    return v;
-}
 
 // 16 bytes of a row, or what is left of it.  Rows that are no whole pieces (VEC false) start at any
 // value: unaligned loads and stores.

@@ -149,7 +149,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(const ProductPa
                 const int one = __builtin_amdgcn_readfirstlane(row[i]);
                 if (i * THREADS >= units) break;
                 if (__all(row[i] == one)) {
-                    const uint32_t most = wave_max(mine);
+                    const uint32_t most = over_lanes<64>(mine, larger);
                     if (lane == 0 && one < t.rows) atomicMax(&amax[one], most);
                 } else if (row[i] < t.rows) {
                     atomicMax(&amax[row[i]], mine);
@@ -282,18 +282,18 @@ __device__ inline void store_tile(const i32x4_t (&acc)[RT][CT], const float (&xs
 // inputs, and the waves' sums meet in LDS at the end; four times the workgroups where 64 x 64
 // tiles would leave most of the card idle.  Block b of row r sits in slot b ^ (r & 15) of the
 // row's 256 bytes.
-template <int T> constexpr int MEDIUM_RING = T == 64 ? 4 : 8;
-
-template <typename OT, int T>
+template <typename OT, int T, int PER, int RING>
 __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int row_tiles, int col_tiles) {
-    constexpr int RING = MEDIUM_RING<T>, LOADS = T / 8, BUF = 2 * T * 16;  // loads of a wave and stage; slots: rows, then weight rows
+    constexpr int BUF = 2 * T * PER, LOADS = BUF / 256, EACH = 64 / PER;  // slots: rows, then weight rows; loads of a wave and stage; rows of a load
+    auto swizzle = [](int row) { return PER == 16 ? row & 15 : row >> 1 & 7; };
+    static_assert(T == 64 || PER == 16, "a quarter of a stage a wave");
     __shared__ i32x4_t lds[RING * BUF];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4, wy = T == 64 ? wave >> 1 : 0, wx = T == 64 ? wave & 1 : 0;
     const ProductTile t = product_tile(p.offsets, p.n_groups, p.rows, xcd_tile(blockIdx.x), T, row_tiles, col_tiles);
     if (t.rows == 0) return;
     const int n0 = t.col * T, cols = min(T, p.n_out - n0);
-    const int nb = p.n_in / BLOCK, stages = (nb + SPAN_BLOCKS - 1) / SPAN_BLOCKS;
+    const int nb = p.n_in / BLOCK, stages = (nb + PER - 1) / PER;
 
     i32x4_t acc[2][2];
     float xs[2] = {0.f, 0.f}, ws = 0.f;
@@ -308,20 +308,20 @@ __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int 
 #pragma unroll
         for (int m = 0; m < 2; ++m) xs[m] = p.xs[t.row0 + min(wy * 32 + 16 * m + r, t.rows - 1)];
         ws = p.ws[w0 + min(wx * 32 + (lane & 31), cols - 1)];
-        // Rows of both sides together, the weight's from T on.  Load i of a wave: row
-        // 16 i + 4 wave + lane / 16, slot lane % 16; rows behind a side's end re-read its last.
-        const int srow = 4 * wave + (lane >> 4), block = (lane & 15) ^ srow;
+        // Rows of both sides together, the weight's from T on.  Load i of a wave: rows
+        // 4 EACH i + EACH wave and on, slot lane % PER; rows behind a side's end re-read its last.
+        const int srow = EACH * wave + lane / PER, block = (lane % PER) ^ swizzle(srow);
         uint32_t at[LOADS];
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            const int row = 16 * i + srow;
-            at[i] = (uint32_t)(16 * i < T ? min(row, t.rows - 1) : min(row - T, cols - 1)) * p.n_in + 16 * block;
+            const int row = 4 * EACH * i + srow;
+            at[i] = (uint32_t)(4 * EACH * i < T ? min(row, t.rows - 1) : min(row - T, cols - 1)) * p.n_in + 16 * block;
         }
         auto ask = [&](int st) {  // behind the last stage: zeros
             i32x4_t* const buf = lds + st % RING * BUF;
 #pragma unroll
             for (int i = 0; i < LOADS; ++i)
-                load16_to_lds(16 * i < T ? bx : bw, buf + i * 256 + wave * 64, st * SPAN_BLOCKS + block < nb ? at[i] : OUTSIDE, (uint32_t)st * 256);
+                load16_to_lds(4 * EACH * i < T ? bx : bw, buf + i * 256 + wave * 64, st * PER + block < nb ? at[i] : OUTSIDE, (uint32_t)st * PER * 16);
         };
 #pragma unroll
         for (int k = 0; k < RING - 1; ++k) ask(k);
@@ -334,13 +334,13 @@ __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int 
             ask(st + RING - 1);
             const i32x4_t* const buf = lds + st % RING * BUF;
 #pragma unroll
-            for (int j = 0; j < (T == 64 ? 4 : 1); ++j) {
-                const int slot = r * 16 + ((4 * (T == 64 ? j : wave) + q) ^ r);
+            for (int j = 0; j < (T == 64 ? PER / 4 : 1); ++j) {
+                const int slot = r * PER + ((4 * (T == 64 ? j : wave) + q) ^ swizzle(r));
                 i32x4_t xv[2], wv[2];
 #pragma unroll
-                for (int m = 0; m < 2; ++m) xv[m] = buf[(wy * 2 + m) * 256 + slot];
+                for (int m = 0; m < 2; ++m) xv[m] = buf[(wy * 2 + m) * 16 * PER + slot];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) wv[c] = buf[T * 16 + (wx * 2 + c) * 256 + slot];
+                for (int c = 0; c < 2; ++c) wv[c] = buf[(T + (wx * 2 + c) * 16) * PER + slot];
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -618,9 +618,9 @@ template <typename OT, Rows ROWS> hipError_t launch_small(const ProductParams& p
     return hipGetLastError();
 }
 
-template <typename OT, int T> hipError_t launch_medium(const ProductParams& p, hipStream_t s) {
+template <typename OT, int T, int PER, int RING> hipError_t launch_medium(const ProductParams& p, hipStream_t s) {
     const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, T), cols = (p.n_out + T - 1) / T;
-    medium_kernel<OT, T><<<(unsigned)xcd_padded(rows * cols), 256, 0, s>>>(p, (int)rows, (int)cols);
+    medium_kernel<OT, T, PER, RING><<<(unsigned)xcd_padded(rows * cols), 256, 0, s>>>(p, (int)rows, (int)cols);
     return hipGetLastError();
 }
 
@@ -661,8 +661,10 @@ template <typename OT> hipError_t launch_product(const ProductParams& p, hipStre
     const int64_t m = typical_rows(p.rows, p.n_groups), runs = (p.n_out + 15) / 16;
     if (p.offsets ? m < held_rows(p.n_in) : m <= held_rows(p.n_in)) return launch_small<OT, STAGED>(p, s);
     if (p.offsets ? m < 8 : m <= 16 || expected_tiles(p, 16) * runs <= 2 * CUS) return launch_small<OT, STREAMED>(p, s);
-    if (expected_tiles(p, 32) * ((p.n_out + 31) / 32) <= CUS) return launch_medium<OT, 32>(p, s);
-    if (expected_tiles(p, 64) * ((p.n_out + 63) / 64) <= 2 * CUS) return launch_medium<OT, 64>(p, s);
+    if (expected_tiles(p, 32) * ((p.n_out + 31) / 32) <= 2 * CUS) return launch_medium<OT, 32, 16, 4>(p, s);
+    const int64_t tiles = expected_tiles(p, 64) * ((p.n_out + 63) / 64);
+    if (tiles <= CUS) return launch_medium<OT, 64, 16, 4>(p, s);
+    if (tiles <= 2 * CUS) return launch_medium<OT, 64, 8, 5>(p, s);
     const double middle = middle_time(p), low = large_time(p, 4, p.n_out), high = large_time(p, 8, p.n_out);
     // Whole rounds of 256 x 256 tiles, and 128 x 256 ones for the columns left over.
     const int64_t row_tiles = expected_tiles(p, 256), whole = row_tiles * ((p.n_out + LARGE_COLS - 1) / LARGE_COLS) / CUS;

@@ -1,5 +1,6 @@
 // int8_device.hpp - device building blocks of the 8-bit integer kernels (gfx950).
 #pragma once
+#include "lanes_device.hpp"
 #include "pieces_device.hpp"
 #include "tile_device.hpp"
 
@@ -69,34 +70,7 @@ __device__ inline float row_scale(uint32_t amax, double root) {
     return amax == 0 ? 0.f : (float)((double)__builtin_bit_cast(float, amax) / 127.0 / root);
 }
 
-// Over the lanes of a wave, in each of them: DPP moves inside rows of 16 lanes, then each
-// row's last lane to the rows behind it; the last lane has everything.
-template <int CTRL, int ROWS> __device__ inline uint32_t dpp(uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, ROWS == 0xF); }
-__device__ inline uint32_t wave_max(uint32_t v) {
-    auto join = [&](uint32_t o) { v = v > o ? v : o; };
-    join(dpp<0x111, 0xF>(v));  // row_shr:1
-    join(dpp<0x112, 0xF>(v));  // row_shr:2
-    join(dpp<0x114, 0xF>(v));  // row_shr:4
-    join(dpp<0x118, 0xF>(v));  // row_shr:8
-    join(dpp<0x142, 0xA>(v));  // row_bcast:15 into rows 1 and 3
-    join(dpp<0x143, 0xC>(v));  // row_bcast:31 into rows 2 and 3
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-template <int CTRL, int ROWS> __device__ inline double dpp(double v) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    return __builtin_bit_cast(double, (uint64_t)dpp<CTRL, ROWS>((uint32_t)b) | ((uint64_t)dpp<CTRL, ROWS>((uint32_t)(b >> 32)) << 32));
-}
-__device__ inline double wave_sum(double v) {
-    v += dpp<0x111, 0xF>(v);
-    v += dpp<0x112, 0xF>(v);
-    v += dpp<0x114, 0xF>(v);
-    v += dpp<0x118, 0xF>(v);
-    v += dpp<0x142, 0xA>(v);
-    v += dpp<0x143, 0xC>(v);
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63) |
-                                          ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63) << 32));
-}
+__device__ inline uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // Tile `index` of a product: its group, first row, row count and output tile, of tiles of bm rows in
 // col_tiles runs of outputs.  rows == 0: no such tile.  With groups a group's tiles follow each

@@ -46,18 +46,17 @@ template <int N> __device__ inline void load_weights(const void* w, int dtype, i
     }
 }
 
-// WAVES waves a row (1: four rows a workgroup), P pieces of 16 bytes a thread; P == 0:
-// longer rows, read once for the sums and again for the codes.
-template <typename T, bool NORM, int WAVES, int P>
-__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rows_kernel(const RowsParams p) {
-    constexpr int N = 16 / T::bytes, KEPT = P > 0 ? P : 1, THREADS = WAVES * 64;
-    __shared__ uint32_t wave_amax[2][WAVES];
-    __shared__ double wave_squares[2][WAVES];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int thread = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;  // of the row
-    const int64_t step = WAVES == 1 ? (int64_t)gridDim.x * 4 : gridDim.x;
+// THREADS threads a row (up to 64: 256 / THREADS rows a workgroup), P pieces of 16 bytes a thread;
+// P == 0: longer rows, read once for the sums and again for the codes.
+template <typename T, bool NORM, int THREADS, int P>
+__global__ __launch_bounds__(THREADS <= 64 ? 256 : THREADS) void rows_kernel(const RowsParams p) {
+    constexpr int N = 16 / T::bytes, KEPT = P > 0 ? P : 1, WAVES = THREADS / 64, LANES = THREADS <= 64 ? THREADS : 64;
+    constexpr int ROWS = THREADS <= 64 ? 256 / THREADS : 1;  // of a workgroup
+    __shared__ uint32_t wave_amax[2][WAVES > 0 ? WAVES : 1];
+    __shared__ double wave_squares[2][WAVES > 0 ? WAVES : 1];
+    const int thread = threadIdx.x % THREADS;  // of the row
     int parity = 0;
-    for (int64_t row = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x; row < p.rows; row += step, parity ^= 1) {
+    for (int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / THREADS; row < p.rows; row += (int64_t)gridDim.x * ROWS, parity ^= 1) {
         const int64_t x0 = row * p.ldx, r0 = row * p.ldr, o0 = row * p.n;
         float u[KEPT][N];
         uint32_t amax = 0;
@@ -103,12 +102,12 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rows_kernel(con
         } else {
             for (int c = thread * N; c < p.n; c += THREADS * N) piece(c, true, u[0]);
         }
-        amax = wave_max(amax);
-        if (NORM) squares = wave_sum(squares);
+        amax = over_lanes<LANES>(amax, larger);
+        if (NORM) squares = over_lanes<LANES>(squares, [](double a, double b) { return a + b; });
         if constexpr (WAVES > 1) {
             if ((threadIdx.x & 63) == 0) {
-                wave_amax[parity][wave] = amax;
-                if (NORM) wave_squares[parity][wave] = squares;
+                wave_amax[parity][threadIdx.x >> 6] = amax;
+                if (NORM) wave_squares[parity][threadIdx.x >> 6] = squares;
             }
             __syncthreads();
             amax = 0;
@@ -151,33 +150,51 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rows_kernel(con
 
 // ---- dequantise ----
 //
-// A thread makes 16 values of 16 codes.
-template <typename T, typename INDEX>
+// A thread makes 16 bytes of values four times, 256 threads' apart, so that a wave's stores are whole lines.
+// (Once where that leaves most CUs without a workgroup: 13 rows of 4096 2.0 us against 2.7.)
+constexpr int DEQUANT_UNROLL = 4;
+
+template <typename T, typename INDEX, int U>
 __global__ __launch_bounds__(256) void dequantize_kernel(const int8_t* __restrict__ codes, const float* __restrict__ scales,
                                                          int64_t units, INDEX per_row, void* __restrict__ out) {
     constexpr int N = 16 / T::bytes;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= units) return;
-    const u32x4_t c = reinterpret_cast<const u32x4_t*>(codes)[i];
-    const float s = scales[(INDEX)i / per_row];
+    const int64_t base = (int64_t)blockIdx.x * 256 * U + threadIdx.x;
+    uint32_t c[U][N / 4];
+    float s[U];
 #pragma unroll
-    for (int k = 0; k < 16; k += N) {
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = base + u * 256;
+        if (i >= units) continue;
+        if constexpr (N == 8) {
+            const uint2 v = reinterpret_cast<const uint2*>(codes)[i];
+            c[u][0] = v.x;
+            c[u][1] = v.y;
+        } else {
+            c[u][0] = reinterpret_cast<const uint32_t*>(codes)[i];
+        }
+        s[u] = scales[(INDEX)i / per_row];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = base + u * 256;
+        if (i >= units) continue;
         float v[N];
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = rounded((float)((int)(c[(k + e) / 4] << (24 - 8 * ((k + e) & 3))) >> 24) * s);
-        reinterpret_cast<u32x4_t*>(out)[i * (16 / N) + k / N] = round_piece<T>(v);
+        for (int e = 0; e < N; ++e) v[e] = rounded((float)((int)(c[u][e / 4] << (24 - 8 * (e & 3))) >> 24) * s[u]);
+        reinterpret_cast<u32x4_t*>(out)[i] = round_piece<T>(v);
     }
 }
 
 // ---- launches ----
 
-template <typename T, bool NORM, int WAVES, int P> hipError_t launch(const RowsParams& p, hipStream_t s) {
-    const int64_t groups = WAVES == 1 ? (p.rows + 3) / 4 : p.rows;
-    rows_kernel<T, NORM, WAVES, P><<<(unsigned)(groups < MAX_GRID ? groups : MAX_GRID), WAVES == 1 ? 256 : WAVES * 64, 0, s>>>(p);
+template <typename T, bool NORM, int THREADS, int P> hipError_t launch(const RowsParams& p, hipStream_t s) {
+    constexpr int ROWS = THREADS <= 64 ? 256 / THREADS : 1;
+    const int64_t groups = (p.rows + ROWS - 1) / ROWS;
+    rows_kernel<T, NORM, THREADS, P><<<(unsigned)(groups < MAX_GRID ? groups : MAX_GRID), THREADS <= 64 ? 256 : THREADS, 0, s>>>(p);
     return hipGetLastError();
 }
 
-// Waves a row and pieces a thread (us): as few pieces as there are where rows are few, since a
+// Threads a row and pieces a thread (us): as few pieces as there are where rows are few, since a
 // row is then one latency after the other (256 rows of 2048 bf16, norm: 3.4 with 4 waves of one piece,
 // 6.8 with one wave of 4; one row of 4096 3.3 with 8 x 1, 4.1 with 4 x 4); where they are many, two
 // pieces of four waves or eight (16384 rows of 2048, quantised: 19.6 with 2 x 2, 23.0 with 1 x 4; 2048
@@ -185,14 +202,18 @@ template <typename T, bool NORM, int WAVES, int P> hipError_t launch(const RowsP
 template <typename T, bool NORM> hipError_t launch_rows(const RowsParams& p, hipStream_t s) {
     const int pieces = p.n * T::bytes / 16;  // n <= 2^24
     const bool few = p.rows <= 512;
-    if (pieces <= 64) return launch<T, NORM, 1, 1>(p, s);
-    if (pieces <= 128) return launch<T, NORM, 1, 2>(p, s);
-    if (pieces <= 256) return NORM || few ? launch<T, NORM, 4, 1>(p, s) : launch<T, NORM, 2, 2>(p, s);
-    if (pieces <= 512) return few ? launch<T, NORM, 8, 1>(p, s) : launch<T, NORM, 4, 2>(p, s);
-    if (pieces <= 1024) return launch<T, NORM, 8, 2>(p, s);
-    if (pieces <= 2048) return few ? launch<T, NORM, 16, 2>(p, s) : launch<T, NORM, 8, 4>(p, s);
-    if (pieces <= 4096) return launch<T, NORM, 16, 4>(p, s);
-    return launch<T, NORM, 16, 0>(p, s);
+    if (pieces <= 4) return launch<T, NORM, 4, 1>(p, s);
+    if (pieces <= 8) return launch<T, NORM, 8, 1>(p, s);
+    if (pieces <= 16) return launch<T, NORM, 16, 1>(p, s);
+    if (pieces <= 32) return launch<T, NORM, 32, 1>(p, s);
+    if (pieces <= 64) return launch<T, NORM, 64, 1>(p, s);
+    if (pieces <= 128) return launch<T, NORM, 64, 2>(p, s);
+    if (pieces <= 256) return NORM || few ? launch<T, NORM, 256, 1>(p, s) : launch<T, NORM, 128, 2>(p, s);
+    if (pieces <= 512) return few ? launch<T, NORM, 512, 1>(p, s) : launch<T, NORM, 256, 2>(p, s);
+    if (pieces <= 1024) return launch<T, NORM, 512, 2>(p, s);
+    if (pieces <= 2048) return few ? launch<T, NORM, 1024, 2>(p, s) : launch<T, NORM, 512, 4>(p, s);
+    if (pieces <= 4096) return launch<T, NORM, 1024, 4>(p, s);
+    return launch<T, NORM, 1024, 0>(p, s);
 }
 
 template <bool NORM> hipError_t launch_rows(int dtype, const RowsParams& p, hipStream_t s) {
@@ -205,12 +226,17 @@ template <bool NORM> hipError_t launch_rows(int dtype, const RowsParams& p, hipS
 
 hipError_t launch_quantize(int dtype, const RowsParams& p, hipStream_t s) { return launch_rows<false>(dtype, p, s); }
 
-template <typename T> hipError_t launch_dequantize(const int8_t* codes, const float* scales, int64_t rows, int n, void* out, hipStream_t s) {
-    const int64_t units = rows * (n / 16);
-    const unsigned grid = (unsigned)((units + 255) / 256);
-    if (units < (1ll << 32)) dequantize_kernel<T, uint32_t><<<grid, 256, 0, s>>>(codes, scales, units, (uint32_t)(n / 16), out);
-    else dequantize_kernel<T, int64_t><<<grid, 256, 0, s>>>(codes, scales, units, (int64_t)(n / 16), out);
+template <typename T, int U> hipError_t launch_dequantize(const int8_t* codes, const float* scales, int64_t units, int per_row, void* out, hipStream_t s) {
+    const unsigned grid = (unsigned)((units + 256 * U - 1) / (256 * U));
+    if (units < (1ll << 32)) dequantize_kernel<T, uint32_t, U><<<grid, 256, 0, s>>>(codes, scales, units, (uint32_t)per_row, out);
+    else dequantize_kernel<T, int64_t, U><<<grid, 256, 0, s>>>(codes, scales, units, (int64_t)per_row, out);
     return hipGetLastError();
+}
+template <typename T> hipError_t launch_dequantize(const int8_t* codes, const float* scales, int64_t rows, int n, void* out, hipStream_t s) {
+    constexpr int N = 16 / T::bytes;
+    const int64_t units = rows * (n / N);
+    if (units < 256 * 256 * DEQUANT_UNROLL) return launch_dequantize<T, 1>(codes, scales, units, n / N, out, s);
+    return launch_dequantize<T, DEQUANT_UNROLL>(codes, scales, units, n / N, out, s);
 }
 
 }  // namespace i8
@@ -238,8 +264,8 @@ int exl3_int8_dequantize(const int8_t* codes, const float* scales, int64_t rows,
     if (bad_dtype(dtype) || bad_row(n) || rows < 0) return EXL3_EINVAL;
     if (rows == 0) return EXL3_OK;
     if (!out || !codes || !scales || misaligned(out) || misaligned(codes) || misaligned(scales, 4)) return EXL3_EINVAL;
-    // 2^37 values: 2^25 - 1 workgroups of 256 pieces would be too many threads for a launch
-    if (n > MAX_ROW || rows > MAX_ROWS || rows * (n / 16) > (int64_t)0xFFFFFF * 256) return EXL3_EUNSUPPORTED;
+    // a launch takes fewer than 2^32 threads: 2^24 - 1 workgroups, of at least 4096 values
+    if (n > MAX_ROW || rows > MAX_ROWS || rows * n > (int64_t)0xFFFFFF * 4096) return EXL3_EUNSUPPORTED;
     if (!apart({values(out, dtype, 1, rows * n, rows * n)}, {{codes, rows * n}, {scales, rows * 4}})) return EXL3_EINVAL;
     hipStream_t s = (hipStream_t)stream;
     const hipError_t e = dtype == EXL3_F16    ? launch_dequantize<exl3::mx::F16>(codes, scales, rows, n, out, s)

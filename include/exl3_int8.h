@@ -48,8 +48,8 @@ int exl3_int8_quantize(const void* x, int32_t dtype, int64_t rows, int32_t n, in
 
 /*
  * exl3_int8_dequantize: codes times their row's scale, in fp32, rounded to dtype.
- * out: dtype [rows][n], overwritten.  Errors as above; EXL3_EUNSUPPORTED for more than
- * 2^37 values too.
+ * out: dtype [rows][n], overwritten.  Errors as above; EXL3_EUNSUPPORTED for about
+ * 2^36 values and more too.
  */
 int exl3_int8_dequantize(const int8_t* codes, const float* scales, int64_t rows, int32_t n, void* out, int32_t dtype,
                          void* stream);

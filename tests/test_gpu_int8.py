@@ -45,7 +45,7 @@ def test_quantize_sizes(ex, dtype, rows, n, pad):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("n", [16, 512, 1024, 1040, 2048, 2064, 4096, 4112, 8192, 14336])
+@pytest.mark.parametrize("n", [16, 32, 48, 64, 96, 128, 144, 256, 272, 512, 1024, 1040, 2048, 2064, 4096, 4112, 8192, 14336])
 def test_many_rows(ex, dtype, n):
     """More than the few rows that other waves and pieces are chosen for."""
     rng = np.random.default_rng([21, n])
