@@ -485,9 +485,12 @@ __global__ __launch_bounds__(512, 2) void large_kernel(const ProductParams p, in
     // The next tile from `index` on, or one without rows behind the last; tiles of rows of no
     // group are filled with zeros on the way.
     int index = blockIdx.x;
+    // (with 256 rows there are no registers left for them)
+    KeptGroups groups;
+    if constexpr (!UNITS) groups = keep_groups(p.offsets, p.n_groups, p.rows);
     auto next_tile = [&]() {
         for (; index < tiles; index += gridDim.x) {
-            const ProductTile t = product_tile(p.offsets, p.n_groups, p.rows, xcd_tile(index), ROWS, row_tiles, col_tiles);
+            const ProductTile t = product_tile(p.offsets, p.n_groups, p.rows, xcd_tile(index), ROWS, row_tiles, col_tiles, UNITS ? nullptr : &groups);
             if (t.rows == 0) continue;
             const int n0 = t.col * LARGE_COLS, cols = min(LARGE_COLS, p.n_out - n0);
             if (t.group >= p.n_groups) {
