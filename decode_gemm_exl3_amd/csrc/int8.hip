@@ -491,7 +491,7 @@ __global__ __launch_bounds__(512, 2) void large_kernel(const ProductParams p, in
     auto next_tile = [&]() {
         for (; index < tiles; index += gridDim.x) {
             const ProductTile t = product_tile(p.offsets, p.n_groups, p.rows, xcd_tile(index), ROWS, row_tiles, col_tiles, UNITS ? nullptr : &groups);
-            if (t.rows == 0) continue;
+            if (t.rows == 0) break;  // the tiles of a workgroup rise: there are no more
             const int n0 = t.col * LARGE_COLS, cols = min(LARGE_COLS, p.n_out - n0);
             if (t.group >= p.n_groups) {
                 typedef typename OT::raw raw;
