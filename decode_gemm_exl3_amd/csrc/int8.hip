@@ -1,4 +1,8 @@
 // int8.hip - products of 8-bit rows with 8-bit weights (gfx950).
+//
+// y[r][o] = T(fl(fl(sum_k x[r][k] w[o][k]) xs[r]) ws[o]): the sum exact in 32-bit integers, converted to
+// fp32 (the first rounding, from 2^24 on), each scale one more rounding of fp32, the type T the last.
+// Four kernels for few rows to many; launch_product at the end of the kernels chooses.
 #include <hip/hip_runtime.h>
 
 #include "int8_device.hpp"
@@ -29,8 +33,10 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer(const int8_t* base, int64_t byte
 
 // v_mfma_i32_16x16x64_i8 takes, per lane, 16 codes (a block) of row lane % 16, of the
 // (lane / 16)th of the four blocks of 64 inputs; accumulator i is row 4 (lane / 16) + i of
-// the first operand (an output) against row lane % 16 of the second.  (32 x 32 x 32 issues at
-// the same rate, but holds the clock lower: 8192^3 takes 425 us with this one, 446 with that.)
+// the first operand (an output) against row lane % 16 of the second.  With nothing else to do the
+// card issues 4.80 P multiplications and additions a second of this one (eight waves a CU; 4.44 with
+// four), 4.28 of 32 x 32 x 32 (3.77), which holds the clock lower: 8192^3 took 425 us with this one,
+// 446 with that.
 __device__ inline i32x4_t mfma(const i32x4_t w, const i32x4_t x, const i32x4_t c) { return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, c, 0, 0, 0); }
 
 // Few rows: eight waves, `split` of them on each run of 16 outputs (8 / split runs a
@@ -44,6 +50,10 @@ __device__ inline i32x4_t mfma(const i32x4_t w, const i32x4_t x, const i32x4_t c
 // Block b of row r sits in 16-byte slot b ^ r of the row's 256 bytes: the 16 lanes that LDS
 // serves together (rows 0-3 and 12-15 of one quarter of the wave, 4-11 of the next) then read
 // 16 different slots.
+//
+// Memory bounds it: 13 rows 14336 -> 4096 take 11.4 us (the weight at 5.1 TB/s, what a large copy
+// moves), 3 x 2 tokens of 8 experts 4096 -> 14336 45.7 us.  One row 4096 -> 4096 takes 7.5 us, 2.2 TB/s: launch,
+// the row's latency, its quantisation, the weight's latency.
 enum Rows { STREAMED, STAGED, QUANTISED };
 
 template <typename OT, Rows ROWS>
@@ -281,7 +291,12 @@ __device__ inline void store_tile(const i32x4_t (&acc)[RT][CT], const float (&xs
 // quarter of the tile.  T = 32: each wave the whole tile over a quarter of the stage's
 // inputs, and the waves' sums meet in LDS at the end; four times the workgroups where 64 x 64
 // tiles would leave most of the card idle.  Block b of row r sits in slot b ^ (r & 15) of the
-// row's 256 bytes.
+// row's 256 bytes.  PER is a stage's blocks a row: with 8 (128 inputs, slots as in middle_kernel) and
+// five of them two workgroups share a CU.
+//
+// Latency bounds it: start, then a stage's way from memory each time the ring has gone round (333 rows
+// 2064 -> 1001 fp32 7.9 us; 64 rows 4096 -> 4096 7.8; 512 rows 20.5, 0.84 P operations a second).
+// Rings (us, T = 32): 4 stages 7.8 for those 64 rows, two workgroups a CU, 8 stages 8.5, one.
 template <typename OT, int T, int PER, int RING>
 __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int row_tiles, int col_tiles) {
     constexpr int BUF = 2 * T * PER, LOADS = BUF / 256, EACH = 64 / PER;  // slots: rows, then weight rows; loads of a wave and stage; rows of a load
@@ -373,6 +388,7 @@ __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int 
 // weight: the rows are asked for one stage ahead, the weight (which more often comes from
 // memory) two.  Block b of row r sits in 16-byte slot b ^ (r / 2 & 7) of the row's 128 bytes:
 // the 16 lanes that LDS serves together then read 16 different slots of its 256-byte width.
+// The loads' way bounds it: 768 rows 4096 -> 4096 take 28.8 us, 0.9 P operations a second.
 constexpr int STAGE_BLOCKS = 8;
 // Units of the ring of this stage's rows, the next stage's rows and the weight of the one after
 // that, from that of this stage's weight; and that of the next stage's weight.
@@ -466,6 +482,14 @@ __global__ __launch_bounds__(256, 2) void middle_kernel(const ProductParams p, i
 // them in a ring as above; with 128 rows LDS holds three whole stages of 48 KB, and both sides
 // are asked for two ahead.  The ring does not run dry between tiles: the last stages of a tile ask
 // for the first of the next, and its results leave from registers.
+//
+// What bounds it: the power that the matrix cores draw at these values (2048 rows 8192 -> 28672: they
+// are busy 0.79 of the cycles, at 1.67 GHz; all zeros run at 2.18 GHz and take 30 % less time), and the
+// results, which all workgroups store at once between tiles (8192^3: 384 us, without them 354).
+// 8192^3 takes 384 us by itself, 2.9 P operations a second, and 490 in a long run of them; 2048 rows
+// 8192 -> 28672 359, and 16384 rows in 64 groups 2048 -> 2816 144 with 128 rows a tile.
+// Two groups that take turns against all eight waves alike: a stage's reads then wait behind each other.
+// One side's loads in each half of a stage, against all in the first: 8192^3 384 us, 415.
 constexpr int LARGE_COLS = 256;
 
 template <typename OT, int RT>
@@ -647,9 +671,8 @@ inline int64_t expected_tiles(const ProductParams& p, int high) {
     return p.rows / high + (p.n_groups < p.rows ? p.n_groups : p.rows) / 2 + 1;
 }
 
-// The time of a product in tiles, in us per 4096 inputs, from whole rounds of 256 workgroups
-// (us, 4096 inputs): 128 x 128 tiles two a CU, 28 for one of them and 39 for both; 128 x 256 36.7;
-// 256 x 256 52.
+// The time of a product in tiles, in us per 4096 inputs, by the rounds that 256 CUs take, as
+// measured: 128 x 128 tiles 28 for one a CU and 39 for two at once; 128 x 256 36.7; 256 x 256 52.
 inline double middle_time(const ProductParams& p) {
     const int64_t each = (expected_tiles(p, 128) * ((p.n_out + 127) / 128) + CUS - 1) / CUS;
     return (double)(each / 2) * 39 + (double)(each % 2) * 28;
@@ -659,6 +682,24 @@ inline double large_time(const ProductParams& p, int rt, int64_t n_out) {
     return (double)rounds * (rt == 8 ? 52 : 36.7);
 }
 
+// Rules by the average group, as the host doesn't know the route; times in us.
+//
+// Held rows: 128 rows in 64 groups 2048 -> 2816 52, streamed 62; 512 rows in 256 groups 1024 -> 1024 44 and 58; equal
+// at as many rows as are held (8 a group 76.9 and 75.9).
+// Streamed few-rows tiles, beyond 16 rows only while one round of workgroups makes them: against 32 x 32 tiles
+// 17 rows 14336 -> 4096 16.7 and 19.2, 128 rows 4096 -> 1024 6.3 and 7.1, but 32 rows 4096 -> 8192 11.8 and 9.6.  In
+// groups up to 8: 1024 rows in 64 groups 2048 -> 2816 93, in 128 x 256 tiles 75.
+// 32 x 32 tiles while the card holds all of them: against 64 x 64 ones 96 rows 4096 -> 4096 11.2 and 12.3, 256 rows
+// 4096 -> 2048 9.1 and 11.7, 128 rows 14336 -> 4096 31.8 and 35.2.
+// 64 x 64 tiles in stages of 256 inputs while there is one a CU, in stages of 128 where there are two: the latter
+// against the former 512 rows 4096 -> 4096 20.5 and 23.1, 2048 rows 4096 -> 1024 17.1 and 22.6, but 256 rows
+// 4096 -> 4096 14.3 and 12.7, 256 rows 14336 -> 4096 41.2 and 35.3.  128 x 128 ones beyond: 768 rows 4096 -> 4096
+// 28.8, 64 x 64 ones 33.4.
+// 128 x 128, 128 x 256 and 256 x 256 by the rounds that they take (the times above): 768 rows 4096 -> 4096 28.8, 31.5,
+// 44.9; 2048 rows 38.9, 34.8, 46.5; 4096 rows 74, 67, 54; 1000 rows 4096 -> 28672 133, 126, 102; 8192^3 508, 465, 384; 16384 rows
+// in 64 groups 2048 -> 2816 159, 143, 155.
+// Whole rounds of 256 x 256 and the rest in 128 x 256 tiles: 2048 rows 8192 -> 28672 359, all of them large 366; only
+// where it saves 5 %, for the second launch.
 template <typename OT> hipError_t launch_product(const ProductParams& p, hipStream_t s) {
     if (p.x) return launch_small<OT, QUANTISED>(p, s);
     const int64_t m = typical_rows(p.rows, p.n_groups), runs = (p.n_out + 15) / 16;

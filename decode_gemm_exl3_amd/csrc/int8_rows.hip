@@ -16,6 +16,9 @@ namespace i8 {
 // it enters the scale alone.
 //
 // Squares are summed in 64 bits: those of fp32 and bf16 values pass the range of fp32.
+//
+// Memory bounds it: 8192 rows of 8192 fp16 with a residual and their sum kept, 470 MB, take 95.8 us (4.9 TB/s;
+// a large copy moves 5.0), 16384 rows of 2048 quantised 19.6 us.  A single row is launch and latencies: 2.9 us.
 
 // N consecutive weights from column c on.
 template <int N> __device__ inline void load_weights(const void* w, int dtype, int c, float (&out)[N]) {
@@ -152,6 +155,7 @@ __global__ __launch_bounds__(THREADS <= 64 ? 256 : THREADS) void rows_kernel(con
 //
 // A thread makes 16 bytes of values four times, 256 threads' apart, so that a wave's stores are whole lines.
 // (Once where that leaves most CUs without a workgroup: 13 rows of 4096 2.0 us against 2.7.)
+// Memory bounds it: 8192 rows of 8192 to fp16, 201 MB, take 33.1 us, 6.1 TB/s (codes just made are in the cache).
 constexpr int DEQUANT_UNROLL = 4;
 
 template <typename T, typename INDEX, int U>
