@@ -59,6 +59,11 @@ template <typename T, bool VEC> __device__ inline void store_columns(void* base,
     __builtin_memcpy(static_cast<char*>(base) + at * T::bytes, &r, 16);
 }
 
+// 4 bytes of -infinity.
+template <typename T> constexpr uint32_t LOWEST = 0xFF800000u;
+template <> constexpr uint32_t LOWEST<F16> = 0xFC00FC00u;
+template <> constexpr uint32_t LOWEST<BF16> = 0xFF80FF80u;
+
 // What a lane asks for of a token: its pieces of the logits, and the token's slot `lane`.
 template <int Q> struct Asked {
     u32x4_t piece[Q];
@@ -75,7 +80,7 @@ template <typename T, int LANES, int Q, bool VEC> __device__ inline Asked<Q> ask
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         const int c = (q * LANES + lane) * N;
-        r.piece[q] = u32x4_t{0, 0, 0, 0};
+        r.piece[q] = u32x4_t{LOWEST<T>, LOWEST<T>, LOWEST<T>, LOWEST<T>};  // columns behind the last
         if (token < p.tokens && c < p.experts) r.piece[q] = load_columns<T, VEC>(p.logits, (int64_t)token * p.experts + c, p.experts - c);
     }
     return r;
@@ -101,21 +106,26 @@ template <int LANES, bool COUNT> __device__ inline bool counts_token(const Param
     return ((all >> first) & ((1ull << (LANES & 63)) - 1)) != 0;
 }
 
-// e^d of d <= 0 as 2^y, y = fl(d / ln 2); 0 below -104, where fp32 ends (v_exp_f32 gives 0 below
-// -87 already).  y is off by up to its own size times 2^-24, which makes a relative 1.2 |d| 2^-24 of
-// the result: less than a tenth of a step of the 16-bit gradients, and of their loss that far down
-// (|d| = 10) 7e-7 a token.  For fp32 logits the result takes (1 + (d / ln 2 - y) ln 2) too, four instructions.
-template <typename T> __device__ inline float exp_below(float d) {
-    constexpr float INV_LN2 = 1.44269502f, INV_LN2_LOW = 1.92596299e-8f, LN2 = 0.693147182f;  // 1 / ln 2 in two parts
+constexpr float INV_LN2 = 1.44269502f, INV_LN2_LOW = 1.92596299e-8f, LN2 = 0.693147182f;  // 1 / ln 2 in two parts
+
+// e^d of d <= 0 to a step of fp32: 2^y with y = fl(d / ln 2), which is off by up to its own size times 2^-24,
+// times 1 + (d / ln 2 - y) ln 2; 0 below -104, where fp32 ends.
+__device__ inline float exp_below(float d) {
     d = fmaxf(d, -104.f);
     const float y = d * INV_LN2, e = __builtin_amdgcn_exp2f(y);
-    if constexpr (T::bytes == 2) return e;
     const float rest = __builtin_fmaf(d, INV_LN2_LOW, __builtin_fmaf(d, INV_LN2, -y));
     return __builtin_fmaf(e * LN2, rest, e);
 }
 
-// The softmax of a token's logits: probabilities of this lane's columns, 0 behind the last.
-template <typename T, int LANES, int Q> __device__ inline void softmax(const Params& p, const u32x4_t (&piece)[Q], int lane, float (&v)[Q][16 / T::bytes]) {
+// The softmax of a token's logits: v times the result are the probabilities of this lane's columns, v
+// is 0 behind the last.  VEC: pieces behind the last column hold -infinity, others lie whole before it.
+//
+// For 16-bit logits v = 2^y, y = fl(x / ln 2 - K) in one step, K the largest x / ln 2 rounded, which
+// all of a token's v share: what K is off by cancels.  y is off by its own size times 2^-24, a relative
+// 0.85 |y| 2^-24 of v: less than a tenth of a step of the gradients' types, and of the loss that far down (v
+// = e^-10) 7e-7 a token.  (Four instructions more for fp32 logits, above.)  Largest logits of 2^20 and more,
+// whose K is off by much, take the difference first.
+template <typename T, bool VEC, int LANES, int Q> __device__ inline float softmax(const Params& p, const u32x4_t (&piece)[Q], int lane, float (&v)[Q][16 / T::bytes]) {
     constexpr int N = 16 / T::bytes;
     const float lowest = -__builtin_inff();
     float top = lowest;
@@ -123,28 +133,33 @@ template <typename T, int LANES, int Q> __device__ inline void softmax(const Par
     for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            v[q][i] = (q * LANES + lane) * N + i < p.experts ? piece_value<T>(piece[q], i) : lowest;
+            v[q][i] = VEC || (q * LANES + lane) * N + i < p.experts ? piece_value<T>(piece[q], i) : lowest;
             top = __builtin_elementwise_maximum(top, v[q][i]);  // a NaN stays one
         }
     top = over_lanes<LANES>(top, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
     const bool bad = !(top < __builtin_inff());  // a NaN or +infinity: all of the token's are NaN
     if (top == lowest) top = 0.f;                // nothing but -infinity: exp gives zeros
     float sum = 0.f;
+    if (T::bytes == 2 && __all(fabsf(top) < 0x1p20f)) {
+        const float k = top * INV_LN2;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[q][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[q][i], INV_LN2, -k));
+    } else {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[q][i] = exp_below(v[q][i] - top);
+    }
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            v[q][i] = exp_below<T>(v[q][i] - top);
-            sum += v[q][i];
-        }
+        for (int i = 0; i < N; ++i) sum += v[q][i];
     sum = over_lanes<LANES>(sum, [](float a, float b) { return a + b; });
     // 1 / sum to a step of fp32: an estimate and one step of Newton's
     const float guess = __builtin_amdgcn_rcpf(sum), newton = __builtin_fmaf(__builtin_fmaf(-sum, guess, 1.f), guess, guess);
-    const float inverse = bad ? __builtin_nanf("") : sum == 0.f ? 0.f : newton;
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[q][i] *= inverse;
+    return bad ? __builtin_nanf("") : sum == 0.f ? 0.f : newton;
 }
 
 // The loss, `along` the sum over the experts of count times sum of probabilities.
@@ -195,12 +210,12 @@ template <typename T, int LANES, int Q, bool VEC> __global__ __launch_bounds__(S
         next = ask<T, LANES, Q, VEC>(p, t0 + step + slot, lane);
         const bool valid = counts_token<LANES, true>(p, t0 + slot, now.id, lane, hist);
         float v[Q][N];
-        softmax<T, LANES, Q>(p, now.piece, lane, v);
+        const float inverse = softmax<T, VEC, LANES, Q>(p, now.piece, lane, v);
         if (valid) {
 #pragma unroll
             for (int q = 0; q < Q; ++q)
 #pragma unroll
-                for (int i = 0; i < N; ++i) acc[q][i] += v[q][i];
+                for (int i = 0; i < N; ++i) acc[q][i] = __builtin_fmaf(v[q][i], inverse, acc[q][i]);
             if (lane == 0) atomicAdd(&hist[p.experts], 1);
         }
     }
@@ -242,13 +257,14 @@ template <typename T, int LANES, int Q, bool VEC> __global__ __launch_bounds__(S
 // experts 7.6 us, most of it the sums' way between XCDs and the arrivals'.
 __global__ __launch_bounds__(FINAL_THREADS) void loss_kernel(const Params p) {
     constexpr int SLICES = FINAL_THREADS / FINAL_EXPERTS, EACH = MAX_BLOCKS / SLICES;
-    static_assert(FINAL_EXPERTS == 64 && EXL3_MOE_MAX_EXPERTS / FINAL_EXPERTS <= 64, "an expert, and a workgroup, a lane");
+    static_assert(FINAL_EXPERTS == 64 && EXL3_MOE_MAX_EXPERTS / FINAL_EXPERTS <= 16, "an expert a lane, and a workgroup of 16");
     __shared__ float sums[SLICES][FINAL_EXPERTS];
     __shared__ int counts[SLICES][FINAL_EXPERTS];
     __shared__ int tokens;
     __shared__ bool last;
     __shared__ double sum_of_all;
     const int lane = threadIdx.x & 63, k = threadIdx.x >> 6, e = blockIdx.x * FINAL_EXPERTS + lane;
+    const int groups = (p.experts + FINAL_EXPERTS - 1) / FINAL_EXPERTS;  // workgroups
     if (threadIdx.x == 0) tokens = 0;
     float part[EACH];
     int part_counts[EACH];
@@ -280,24 +296,24 @@ __global__ __launch_bounds__(FINAL_THREADS) void loss_kernel(const Params p) {
             c += counts[i][lane];
         }
         if (e < p.experts) p.counts[e] = c;
-        double along = (double)c * s;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) along += __shfl_xor(along, d);
+        double along = over_lanes<64>((double)c * s, [](double a, double b) { return a + b; });
         if (threadIdx.x == 0) {
             last = true;
-            if (gridDim.x > 1) {
+            if (groups > 1) {
                 __hip_atomic_store(&p.along[blockIdx.x], __builtin_bit_cast(uint64_t, along), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                last = __hip_atomic_fetch_add(p.arrived, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+                // The store has reached what all XCDs see before the arrival does: it is atomic itself, so a
+                // wait for it is enough, without the write-back of the L2 that a release would add.
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                last = __hip_atomic_fetch_add(p.arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == groups - 1;
             }
         }
-        if (gridDim.x > 1 && __builtin_amdgcn_readfirstlane(last)) {
+        if (groups > 1 && __builtin_amdgcn_readfirstlane(last)) {
             along = 0.0;
-            if (threadIdx.x < gridDim.x)
+            if (lane < groups)
                 along = __builtin_bit_cast(double, __hip_atomic_load(&p.along[threadIdx.x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) along += __shfl_xor(along, d);
+            along = over_lanes<16>(along, [](double a, double b) { return a + b; });
         }
-        sum_of_all = along;
+        if (lane == 0) sum_of_all = along;
     }
     __syncthreads();
     if (threadIdx.x == 0 && last) {
@@ -336,20 +352,20 @@ template <typename T, int LANES, int Q, bool VEC> __global__ __launch_bounds__(B
         next = ask<T, LANES, Q, VEC>(p, token + step, lane);
         const bool valid = counts_token<LANES, false>(p, token, now.id, lane, nullptr);
         float v[Q][N];
-        softmax<T, LANES, Q>(p, now.piece, lane, v);
+        const float inverse = softmax<T, VEC, LANES, Q>(p, now.piece, lane, v);
         float along = 0.f;
 #pragma unroll
         for (int q = 0; q < Q; ++q)
 #pragma unroll
-            for (int i = 0; i < N; ++i) along += v[q][i] * share[q][i];
-        along = over_lanes<LANES>(along, [](float a, float b) { return a + b; });
+            for (int i = 0; i < N; ++i) along = __builtin_fmaf(v[q][i], share[q][i], along);
+        along = over_lanes<LANES>(along, [](float a, float b) { return a + b; }) * inverse * inverse;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const int c = (q * LANES + lane) * N;
             float g[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) g[i] = valid ? factor * (v[q][i] * (share[q][i] - along)) : 0.f;
-            if (token < p.tokens && c < p.experts) store_columns<T, VEC>(p.dlogits, (int64_t)token * p.experts + c, p.experts - c, round_piece<T>(g));
+            for (int i = 0; i < N; ++i) g[i] = factor * (v[q][i] * __builtin_fmaf(share[q][i], inverse, -along));
+            if (token < p.tokens && c < p.experts) store_columns<T, VEC>(p.dlogits, (int64_t)token * p.experts + c, p.experts - c, valid ? round_piece<T>(g) : u32x4_t{0, 0, 0, 0});
         }
     }
 }
