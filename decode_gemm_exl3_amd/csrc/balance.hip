@@ -140,7 +140,7 @@ template <typename T, bool VEC, int LANES, int Q> __device__ inline float softma
     const bool bad = !(top < __builtin_inff());  // a NaN or +infinity: all of the token's are NaN
     if (top == lowest) top = 0.f;                // nothing but -infinity: exp gives zeros
     float sum = 0.f;
-    if (T::bytes == 2 && __all(fabsf(top) < 0x1p20f)) {
+    if (T::bytes == 2 && fabsf(top) < 0x1p20f) {
         const float k = top * INV_LN2;
 #pragma unroll
         for (int q = 0; q < Q; ++q)

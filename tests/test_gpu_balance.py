@@ -312,3 +312,27 @@ def test_training_a_router(ex):
     _, tol = R.balance_tolerances(wide, ids.cpu().numpy(), p, s, 0.35, torch.float32)
     g = gradient(3.5)
     assert (np.abs(x.grad.cpu().double().numpy() - g) <= tol + 4 * 2.0 ** -24 * (np.abs(g) + tol)).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens, experts", [(70, 8), (67, 20), (4000, 64), (300, 257)])
+def test_a_token_without_slots_leaves_the_others_results_as_they_are(ex, tokens, experts, dtype):
+    """Bit for bit, whatever its logits: tokens that share a wave with it too."""
+    dt = DTYPES[dtype]
+    rng = np.random.default_rng([7, tokens, experts])
+    x = torch.from_numpy(rng.standard_normal((tokens, experts))).to(dt)
+    ids = rng.integers(0, experts, (tokens, 2)).astype(np.int32)
+    dropped = rng.random(tokens) < 0.3
+    ids[dropped] = -1
+    one = torch.ones((), device="cuda")
+    results = []
+    for value in (0.0, float("nan"), float("inf"), -float("inf"), torch.finfo(dt).max, torch.finfo(dt).min, 2.0 ** 15):
+        y = x.clone()
+        y[torch.from_numpy(dropped)] = value
+        y, i = y.cuda(), dev(ids)
+        loss, counts = ex.moe_balance_loss(y, i)
+        g = ex.moe_balance_loss_backward(one, y, i, counts)
+        assert not g[torch.from_numpy(dropped).cuda()].any()
+        results.append((loss.view(torch.int32), counts, g.view(torch.int32 if dt == torch.float32 else torch.int16)))
+    for r in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(r, results[0]))
