@@ -232,18 +232,18 @@ __device__ inline int here(int v) {
 // outputs from `col0`, of which those less than `rows` behind row0 are written.  The sums take
 // both scales: xs of this lane's rows, ws of output lane % (16 CT).  A lane holds 4 consecutive
 // outputs of a row; for 16-bit results lanes 16 apart exchange halves of two tiles, so that
-// each has 8.  A store then writes 64 bytes of each of 16 rows.
+// each has 8.  A store then writes 64 bytes of each of 16 rows (32 where CT is 1).
 template <typename OT, int STEP, int RT, int CT>
 __device__ inline void store_tile(const i32x4_t (&acc)[RT][CT], const float (&xs)[RT], float ws, const ProductParams& p, int row0, int rows, int col0) {
     typedef typename OT::raw raw;
     const int lane = here(threadIdx.x & 63), r = lane & 15, q = lane >> 4;
     raw* y = static_cast<raw*>(p.y);
-    auto store = [&](int row, int o, auto v) {  // 16 bytes, or what is left of the row
-        constexpr int N = 16 / OT::bytes;
+    auto store = [&](int row, int o, auto v) {  // 16 bytes (or 8), or what is left of the row
+        constexpr int N = sizeof(v) / OT::bytes;
         raw* const dst = y + (int64_t)(row0 + row) * p.ldy + o;
         if (row >= rows) return;
         if (o + N <= p.n_out) {
-            __builtin_memcpy(dst, &v, 16);  // rows start at any value: an unaligned store
+            __builtin_memcpy(dst, &v, sizeof(v));  // rows start at any value: an unaligned store
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i)
@@ -266,7 +266,14 @@ __device__ inline void store_tile(const i32x4_t (&acc)[RT][CT], const float (&xs
                 for (int i = 0; i < 4; ++i) v[i] = from_f32(OT{}, value(c, i));
                 store(m * STEP + r, col0 + 16 * c + 4 * q, v);
             }
+        } else if constexpr (CT == 1) {
+            typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+            u32x2_t v;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) v[i] = (uint32_t)from_f32(OT{}, value(0, 2 * i)) | ((uint32_t)from_f32(OT{}, value(0, 2 * i + 1)) << 16);
+            store(m * STEP + r, col0 + 4 * q, v);
         } else {
+            static_assert(CT % 2 == 0, "sets of outputs exchange in pairs");
 #pragma unroll
             for (int c = 0; c < CT; c += 2) {
                 u32x4_t v;
@@ -285,26 +292,128 @@ __device__ inline void store_tile(const i32x4_t (&acc)[RT][CT], const float (&xs
     }
 }
 
-// Some rows, or few tiles: a workgroup of four waves owns T rows and T outputs.  Stages of
-// a span (256 bytes a row of both sides) go straight into a ring in LDS, all but one of it
-// ahead: a stage is little work, so it is the bytes in flight that count.  T = 64: each wave a
-// quarter of the tile.  T = 32: each wave the whole tile over a quarter of the stage's
-// inputs, and the waves' sums meet in LDS at the end; four times the workgroups where 64 x 64
-// tiles would leave most of the card idle.  Block b of row r sits in slot b ^ (r & 15) of the
-// row's 256 bytes.  PER is a stage's blocks a row: with 8 (128 inputs, slots as in middle_kernel) and
-// five of them two workgroups share a CU.
+constexpr int STAGE_BLOCKS = 8;  // of a row, in what follows: 128 inputs
+
+// Some rows, or few tiles: a workgroup owns TM rows and TN outputs, each of its waves every WAVESth
+// stage (128 inputs), in a ring of its own in LDS as above: they wait for nobody, so that one wave's loads, another's
+// reads and a third's matrix instructions overlap.  The waves' sums meet in LDS.  Block b of row r sits in slot
+// b ^ (r / 2 & 7) of the row's 128 bytes.
 //
-// Latency bounds it: start, then a stage's way from memory each time the ring has gone round (333 rows
-// 2064 -> 1001 fp32 7.9 us; 64 rows 4096 -> 4096 7.8; 512 rows 20.5, 0.84 P operations a second).
-// Rings (us, T = 32): 4 stages 7.8 for those 64 rows, two workgroups a CU, 8 stages 8.5, one.
-template <typename OT, int T, int PER, int RING>
+// The weight's way to a CU bounds it, 23 to 25 bytes a ns where it comes from memory, and behind that the rows', which
+// each workgroup reads again: 32 rows 14336 -> 4096 take 16.9 us (the weight at 3.5 TB/s), 64 rows 4096 -> 4096 7.8.
+// Waves on their own against four that share a stage and meet at a barrier, in 32 x 32 tiles: the same where the weight
+// comes from memory, 15.1 us against 17.5 for 64 rows 14336 -> 4096 from the caches.
+// Rings of 2 stages of 128 inputs, against 4 of them or 2 of 256 inputs: 64 rows 4096 -> 6144 12.4 us, 15.4 and 14.8, as two
+// workgroups fit a CU; of 3 in 32 x 16 tiles, of which two fit as well (17 rows 14336 -> 4096 14.3, with 2 of 256 inputs 14.9).
+template <typename OT, int TM, int TN, int RING>
+__global__ __launch_bounds__(256) void strip_kernel(const ProductParams p, int row_tiles, int col_tiles) {
+    constexpr int WAVES = 4, PER = STAGE_BLOCKS, RT = TM / 16, CT = TN / 16, BUF = (TM + TN) * PER, EACH = 64 / PER, LOADS = (TM + TN) / EACH;  // rows of a load, loads of a stage
+    auto swizzle = [](int row) { return row >> 1 & 7; };
+    __shared__ i32x4_t lds[WAVES * RING * BUF];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
+    const ProductTile t = product_tile(p.offsets, p.n_groups, p.rows, xcd_tile(blockIdx.x), TM, row_tiles, col_tiles);
+    if (t.rows == 0) return;
+    const int n0 = t.col * TN, cols = min(TN, p.n_out - n0);
+    const int nb = p.n_in / BLOCK, stages = (nb + PER - 1) / PER;
+    i32x4_t* const ring = lds + wave * RING * BUF;
+    // the wave's rows at the end: sets of 16, FINAL waves take turns
+    constexpr int FINAL = RT < WAVES ? RT : WAVES, SETS = RT / FINAL;
+
+    i32x4_t acc[RT][CT];
+    float xs[SETS], ws = 0.f;
+#pragma unroll
+    for (int m = 0; m < SETS; ++m) xs[m] = 0.f;
+#pragma unroll
+    for (int m = 0; m < RT; ++m)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[m][c] = i32x4_t{0, 0, 0, 0};
+    if (t.group < p.n_groups) {
+        const int mine = (stages - wave + WAVES - 1) / WAVES;
+        const int64_t w0 = (int64_t)t.group * p.n_out + n0;
+        const __amdgpu_buffer_rsrc_t bx = buffer(p.xc + (int64_t)t.row0 * p.n_in, (int64_t)t.rows * p.n_in);
+        const __amdgpu_buffer_rsrc_t bw = buffer(p.wc + w0 * p.n_in, (int64_t)cols * p.n_in);
+        // Rows of both sides together, the weight's from TM on.  Load i: rows EACH i and on, slot lane % PER;
+        // rows behind a side's end re-read its last.
+        uint32_t at[LOADS];
+        int block[LOADS];
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int row = EACH * i + lane / PER;
+            block[i] = (lane % PER) ^ swizzle(row);
+            at[i] = (uint32_t)(EACH * i < TM ? min(row, t.rows - 1) : min(row - TM, cols - 1)) * p.n_in + 16 * block[i];
+        }
+        auto ask = [&](int k) {  // behind the last stage: zeros
+            const int st = k < mine ? wave + k * WAVES : stages;
+            i32x4_t* const buf = ring + k % RING * BUF;
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i)
+                load16_to_lds(EACH * i < TM ? bx : bw, buf + i * 64, st * PER + block[i] < nb ? at[i] : OUTSIDE, (uint32_t)st * PER * 16);
+        };
+#pragma unroll
+        for (int k = 0; k < RING; ++k) ask(k);
+#pragma unroll
+        for (int m = 0; m < SETS; ++m) xs[m] = p.xs[t.row0 + min(16 * (m * FINAL + wave % FINAL) + r, t.rows - 1)];
+        ws = p.ws[w0 + min(lane % TN, cols - 1)];
+        for (int k = 0; k < mine; ++k) {
+            __builtin_amdgcn_sched_barrier(0);
+            wait_loads<(RING - 1) * LOADS, false>();
+            __builtin_amdgcn_sched_barrier(0);
+            const i32x4_t* const buf = ring + k % RING * BUF;
+            i32x4_t xv[PER / 4][RT], wv[PER / 4][CT];
+#pragma unroll
+            for (int j = 0; j < PER / 4; ++j) {
+                const int slot = r * PER + ((4 * j + q) ^ swizzle(r));
+#pragma unroll
+                for (int m = 0; m < RT; ++m) xv[j][m] = buf[m * 16 * PER + slot];
+#pragma unroll
+                for (int c = 0; c < CT; ++c) wv[j][c] = buf[(TM + c * 16) * PER + slot];
+            }
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the buffer is read
+            __builtin_amdgcn_sched_barrier(0);
+            ask(k + RING);
+#pragma unroll
+            for (int j = 0; j < PER / 4; ++j)
+#pragma unroll
+                for (int m = 0; m < RT; ++m)
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) acc[m][c] = mfma(wv[j][c], xv[j][m], acc[m][c]);
+        }
+        wait_loads<0, false>();  // nothing is on its way into LDS any more
+    }
+    // each wave's sums over its own ring; then each adds up those of its rows
+    static_assert(RT * CT * 64 <= RING * BUF, "the sums fit");
+#pragma unroll
+    for (int m = 0; m < RT; ++m)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) ring[(m * CT + c) * 64 + lane] = acc[m][c];
+    __syncthreads();
+    if (wave >= FINAL) return;
+    i32x4_t sum[SETS][CT];
+#pragma unroll
+    for (int m = 0; m < SETS; ++m)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            sum[m][c] = i32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int v = 0; v < WAVES; ++v) sum[m][c] += lds[v * RING * BUF + ((m * FINAL + wave) * CT + c) * 64 + lane];
+        }
+    store_tile<OT, 16 * FINAL, SETS, CT>(sum, xs, ws, p, t.row0 + 16 * wave, t.rows - 16 * wave, n0);
+}
+
+// More rows, or outputs: a workgroup of four waves owns 64 rows and 64 outputs, each wave a quarter of
+// the tile.  Stages go straight into a ring in LDS, all but one of it ahead: a stage is little work, so it
+// is the bytes in flight that count.  PER is a stage's blocks a row: 16, block b of row r in slot b ^ (r & 15) of
+// the row's 256 bytes, or 8 (slots as in middle_kernel), with which two workgroups share a CU.
+//
+// A stage's own way bounds it: a barrier, the loads' issue, the reads, the matrix instructions one after the other (256 rows
+// 4096 -> 4096 12.6 us; 512 rows 20.6, 0.83 P operations a second).
+template <typename OT, int PER, int RING>
 __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int row_tiles, int col_tiles) {
-    constexpr int BUF = 2 * T * PER, LOADS = BUF / 256, EACH = 64 / PER;  // slots: rows, then weight rows; loads of a wave and stage; rows of a load
+    constexpr int T = 64, BUF = 2 * T * PER, LOADS = BUF / 256, EACH = 64 / PER;  // slots: rows, then weight rows; loads of a wave and stage; rows of a load
     auto swizzle = [](int row) { return PER == 16 ? row & 15 : row >> 1 & 7; };
-    static_assert(T == 64 || PER == 16, "a quarter of a stage a wave");
     __shared__ i32x4_t lds[RING * BUF];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 15, q = lane >> 4, wy = T == 64 ? wave >> 1 : 0, wx = T == 64 ? wave & 1 : 0;
+    const int r = lane & 15, q = lane >> 4, wy = wave >> 1, wx = wave & 1;
     const ProductTile t = product_tile(p.offsets, p.n_groups, p.rows, xcd_tile(blockIdx.x), T, row_tiles, col_tiles);
     if (t.rows == 0) return;
     const int n0 = t.col * T, cols = min(T, p.n_out - n0);
@@ -349,8 +458,8 @@ __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int 
             ask(st + RING - 1);
             const i32x4_t* const buf = lds + st % RING * BUF;
 #pragma unroll
-            for (int j = 0; j < (T == 64 ? PER / 4 : 1); ++j) {
-                const int slot = r * PER + ((4 * (T == 64 ? j : wave) + q) ^ swizzle(r));
+            for (int j = 0; j < PER / 4; ++j) {
+                const int slot = r * PER + ((4 * j + q) ^ swizzle(r));
                 i32x4_t xv[2], wv[2];
 #pragma unroll
                 for (int m = 0; m < 2; ++m) xv[m] = buf[(wy * 2 + m) * 16 * PER + slot];
@@ -364,21 +473,6 @@ __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int 
         }
         wait_loads<0, true>();  // nothing is on its way into LDS any more
     }
-    if constexpr (T == 32) {
-        // the four waves' sums, added by wave 0, over the ring that every wave has read
-        __syncthreads();
-        i32x4_t* const sums = lds;
-        if (wave > 0) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sums[((wave - 1) * 4 + e) * 64 + lane] = acc[e >> 1][e & 1];
-        }
-        __syncthreads();
-        if (wave > 0) return;
-#pragma unroll
-        for (int v = 0; v < 3; ++v)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e >> 1][e & 1] += sums[(v * 4 + e) * 64 + lane];
-    }
     store_tile<OT, 16, 2, 2>(acc, xs, ws, p, t.row0 + wy * 32, t.rows - wy * 32, n0 + wx * 32);
 }
 
@@ -389,7 +483,6 @@ __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int 
 // memory) two.  Block b of row r sits in 16-byte slot b ^ (r / 2 & 7) of the row's 128 bytes:
 // the 16 lanes that LDS serves together then read 16 different slots of its 256-byte width.
 // The loads' way bounds it: 768 rows 4096 -> 4096 take 28.8 us, 0.9 P operations a second.
-constexpr int STAGE_BLOCKS = 8;
 // Units of the ring of this stage's rows, the next stage's rows and the weight of the one after
 // that, from that of this stage's weight; and that of the next stage's weight.
 __device__ inline int rows_unit(int u) { return u == 4 ? 0 : u + 1; }
@@ -645,9 +738,15 @@ template <typename OT, Rows ROWS> hipError_t launch_small(const ProductParams& p
     return hipGetLastError();
 }
 
-template <typename OT, int T, int PER, int RING> hipError_t launch_medium(const ProductParams& p, hipStream_t s) {
-    const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, T), cols = (p.n_out + T - 1) / T;
-    medium_kernel<OT, T, PER, RING><<<(unsigned)xcd_padded(rows * cols), 256, 0, s>>>(p, (int)rows, (int)cols);
+template <typename OT, int TM, int TN, int RING> hipError_t launch_strip(const ProductParams& p, hipStream_t s) {
+    const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, TM), cols = (p.n_out + TN - 1) / TN;
+    strip_kernel<OT, TM, TN, RING><<<(unsigned)xcd_padded(rows * cols), 256, 0, s>>>(p, (int)rows, (int)cols);
+    return hipGetLastError();
+}
+
+template <typename OT, int PER, int RING> hipError_t launch_medium(const ProductParams& p, hipStream_t s) {
+    const int64_t rows = max_row_tiles(p.offsets != nullptr, p.rows, p.n_groups, 64), cols = (p.n_out + 63) / 64;
+    medium_kernel<OT, PER, RING><<<(unsigned)xcd_padded(rows * cols), 256, 0, s>>>(p, (int)rows, (int)cols);
     return hipGetLastError();
 }
 
@@ -686,15 +785,18 @@ inline double large_time(const ProductParams& p, int rt, int64_t n_out) {
 //
 // Held rows: 128 rows in 64 groups 2048 -> 2816 52, streamed 62; 512 rows in 256 groups 1024 -> 1024 44 and 58; equal
 // at as many rows as are held (8 a group 76.9 and 75.9).
-// Streamed few-rows tiles, beyond 16 rows only while one round of workgroups makes them: against 32 x 32 tiles
-// 17 rows 14336 -> 4096 16.7 and 19.2, 128 rows 4096 -> 1024 6.3 and 7.1, but 32 rows 4096 -> 8192 11.8 and 9.6.  In
-// groups up to 8: 1024 rows in 64 groups 2048 -> 2816 93, in 128 x 256 tiles 75.
-// 32 x 32 tiles while the card holds all of them: against 64 x 64 ones 96 rows 4096 -> 4096 11.2 and 12.3, 256 rows
-// 4096 -> 2048 9.1 and 11.7, 128 rows 14336 -> 4096 31.8 and 35.2.
+// Streamed few-rows tiles, beyond 16 rows only while there is one of them a CU at most: against strips of 32 x 16 64 rows
+// 4096 -> 1024 5.1 and 6.0, 8192 -> 1024 6.3 and 8.9, but with more 17 rows 14336 -> 4096 16.7 and 14.3, 32 rows 20.0 and 16.9.  In
+// groups up to 8 rows: 1024 rows in 64 groups 2048 -> 2816 93, in 64 x 64 tiles 73.
+// Strips of 32 rows and 16, 32 or 64 outputs, the narrowest of which there is one a CU at most: 40 rows 4096 -> 4096 8.6, 7.4 and
+// 9.3; 256 rows 4096 -> 1024 7.9, 6.5, 7.8; 128 rows 14336 -> 4096 44.3, 32.0, 26.9; 256 rows 4096 -> 2048 13.9, 9.1, 8.3; 64 x 64
+// tiles instead of the last 35.3 and 11.9, but 160 rows 4096 -> 4096 (320 strips) 12.5 against 16.3.
 // 64 x 64 tiles in stages of 256 inputs while there is one a CU, in stages of 128 where there are two: the latter
 // against the former 512 rows 4096 -> 4096 20.5 and 23.1, 2048 rows 4096 -> 1024 17.1 and 22.6, but 256 rows
 // 4096 -> 4096 14.3 and 12.7, 256 rows 14336 -> 4096 41.2 and 35.3.  128 x 128 ones beyond: 768 rows 4096 -> 4096
-// 28.8, 64 x 64 ones 33.4.
+// 28.8, 64 x 64 ones 33.4.  Groups of up to 32 rows, which the weights' way from memory bounds, stay with 64 x 64 ones, two
+// a CU: 2048 rows in 64 groups 2048 -> 2816 75.6, in 128 x 128 tiles 79.2, 128 x 256 77.9; 256 rows in 8 groups 4096 -> 14336 95.3, 115.6,
+// 114.7; groups of 64 rows 116, 111 in 128 x 256 tiles.
 // 128 x 128, 128 x 256 and 256 x 256 by the rounds that they take (the times above): 768 rows 4096 -> 4096 28.8, 31.5,
 // 44.9; 2048 rows 38.9, 34.8, 46.5; 4096 rows 74, 67, 54; 1000 rows 4096 -> 28672 133, 126, 102; 8192^3 508, 465, 384; 16384 rows
 // in 64 groups 2048 -> 2816 159, 143, 155.
@@ -704,11 +806,13 @@ template <typename OT> hipError_t launch_product(const ProductParams& p, hipStre
     if (p.x) return launch_small<OT, QUANTISED>(p, s);
     const int64_t m = typical_rows(p.rows, p.n_groups), runs = (p.n_out + 15) / 16;
     if (p.offsets ? m < held_rows(p.n_in) : m <= held_rows(p.n_in)) return launch_small<OT, STAGED>(p, s);
-    if (p.offsets ? m < 8 : m <= 16 || expected_tiles(p, 16) * runs <= 2 * CUS) return launch_small<OT, STREAMED>(p, s);
-    if (expected_tiles(p, 32) * ((p.n_out + 31) / 32) <= 2 * CUS) return launch_medium<OT, 32, 16, 4>(p, s);
+    if (p.offsets ? m < 8 : m <= 16 || expected_tiles(p, 16) * runs <= CUS) return launch_small<OT, STREAMED>(p, s);
+    if (expected_tiles(p, 32) * runs <= CUS) return launch_strip<OT, 32, 16, 3>(p, s);
+    if (expected_tiles(p, 32) * ((p.n_out + 31) / 32) <= CUS) return launch_strip<OT, 32, 32, 2>(p, s);
+    if (expected_tiles(p, 32) * ((p.n_out + 63) / 64) <= CUS) return launch_strip<OT, 32, 64, 2>(p, s);
     const int64_t tiles = expected_tiles(p, 64) * ((p.n_out + 63) / 64);
-    if (tiles <= CUS) return launch_medium<OT, 64, 16, 4>(p, s);
-    if (tiles <= 2 * CUS) return launch_medium<OT, 64, 8, 5>(p, s);
+    if (tiles <= CUS) return launch_medium<OT, 16, 4>(p, s);
+    if (tiles <= 2 * CUS || (p.offsets && m <= 32)) return launch_medium<OT, 8, 5>(p, s);
     const double middle = middle_time(p), low = large_time(p, 4, p.n_out), high = large_time(p, 8, p.n_out);
     // Whole rounds of 256 x 256 tiles, and 128 x 256 ones for the columns left over.
     const int64_t row_tiles = expected_tiles(p, 256), whole = row_tiles * ((p.n_out + LARGE_COLS - 1) / LARGE_COLS) / CUS;
