@@ -521,3 +521,22 @@ def test_linear_of_several_tiles_a_workgroup(ex, m, n_in, n_out, dtype):
                                                                  ([260] * 12, 5, 400, 2816, "fp32"), ([0, 0, 5000], 0, 16, 7000, "bf16"), ([0, 0], 3000, 48, 9000, "fp32")])
 def test_groups_of_several_tiles_a_workgroup(ex, counts, behind, n_in, n_out, dtype):
     check_groups(ex, counts, behind, n_in, n_out, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m, n_in, n_out", [
+    (17, 528, 4090), (33, 16, 2040), (128, 1168, 1022),       # strips of 16 outputs
+    (40, 528, 4001), (65, 144, 2047), (250, 1040, 1000),      # of 32
+    (100, 272, 4040), (33, 48, 8190), (255, 656, 2001),       # of 64
+    (250, 272, 4090), (130, 1040, 5001),                      # 64 x 64 tiles, one a CU
+    (450, 144, 4090), (130, 656, 10001)])                     # and two
+def test_strips_and_tiles_of_some_rows(ex, m, n_in, n_out, dtype):
+    check_product(ex, m, n_in, n_out, dtype, pad=m % 2 * 8)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("counts, n_in, n_out", [
+    ([9, 0, 17, 1, 40, 0, 3, 30], 272, 130), ([20, 11, 0, 33], 528, 1000), ([64, 0, 0, 5], 144, 2050), ([12] * 30 + [0, 100], 400, 1100),
+    ([31, 0, 70, 2] * 6, 1040, 700)])
+def test_groups_of_some_rows(ex, counts, n_in, n_out, dtype):
+    check_groups(ex, counts, 3, n_in, n_out, dtype)
