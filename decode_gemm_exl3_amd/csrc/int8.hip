@@ -785,9 +785,9 @@ inline double large_time(const ProductParams& p, int rt, int64_t n_out) {
 //
 // Held rows: 128 rows in 64 groups 2048 -> 2816 52, streamed 62; 512 rows in 256 groups 1024 -> 1024 44 and 58; equal
 // at as many rows as are held (8 a group 76.9 and 75.9).
-// Streamed few-rows tiles, beyond 16 rows only while there is one of them a CU at most: against strips of 32 x 16 64 rows
-// 4096 -> 1024 5.1 and 6.0, 8192 -> 1024 6.3 and 8.9, but with more 17 rows 14336 -> 4096 16.7 and 14.3, 32 rows 20.0 and 16.9.  In
-// groups up to 8 rows: 1024 rows in 64 groups 2048 -> 2816 93, in 64 x 64 tiles 73.
+// Streamed few-rows tiles while there is one of them a CU at most: against strips of 32 x 16 13 rows 14336 -> 4096 13.6 and
+// 14.0, 64 rows 4096 -> 1024 5.1 and 6.0, 8192 -> 1024 6.3 and 8.9, but with more 17 rows 14336 -> 4096 16.7 and 14.3, 32 rows
+// 20.0 and 16.9; against 32 x 32 ones 13 rows 4096 -> 6144 9.0 and 8.3; 32 rows in 8 groups 4096 -> 14336 101, in 64 x 64 tiles 91.
 // Strips of 32 rows and 16, 32 or 64 outputs, the narrowest of which there is one a CU at most: 40 rows 4096 -> 4096 8.6, 7.4 and
 // 9.3; 256 rows 4096 -> 1024 7.9, 6.5, 7.8; 128 rows 14336 -> 4096 44.3, 32.0, 26.9; 256 rows 4096 -> 2048 13.9, 9.1, 8.3; 64 x 64
 // tiles instead of the last 35.3 and 11.9, but 160 rows 4096 -> 4096 (320 strips) 12.5 against 16.3.
@@ -806,7 +806,7 @@ template <typename OT> hipError_t launch_product(const ProductParams& p, hipStre
     if (p.x) return launch_small<OT, QUANTISED>(p, s);
     const int64_t m = typical_rows(p.rows, p.n_groups), runs = (p.n_out + 15) / 16;
     if (p.offsets ? m < held_rows(p.n_in) : m <= held_rows(p.n_in)) return launch_small<OT, STAGED>(p, s);
-    if (p.offsets ? m < 8 : m <= 16 || expected_tiles(p, 16) * runs <= CUS) return launch_small<OT, STREAMED>(p, s);
+    if (expected_tiles(p, 16) * runs <= CUS) return launch_small<OT, STREAMED>(p, s);
     if (expected_tiles(p, 32) * runs <= CUS) return launch_strip<OT, 32, 16, 3>(p, s);
     if (expected_tiles(p, 32) * ((p.n_out + 31) / 32) <= CUS) return launch_strip<OT, 32, 32, 2>(p, s);
     if (expected_tiles(p, 32) * ((p.n_out + 63) / 64) <= CUS) return launch_strip<OT, 32, 64, 2>(p, s);
