@@ -401,9 +401,9 @@ __global__ __launch_bounds__(256) void strip_kernel(const ProductParams p, int r
 }
 
 // More rows, or outputs: a workgroup of four waves owns 64 rows and 64 outputs, each wave a quarter of
-// the tile.  Stages go straight into a ring in LDS, all but one of it ahead: a stage is little work, so it
-// is the bytes in flight that count.  PER is a stage's blocks a row: 16, block b of row r in slot b ^ (r & 15) of
-// the row's 256 bytes, or 8 (slots as in middle_kernel), with which two workgroups share a CU.
+// the tile.  Stages go straight into a ring in LDS, all but one of it ahead.  PER is a stage's blocks a row: 16, block
+// b of row r in slot b ^ (r & 15) of the row's 256 bytes, or 8 (slots as in middle_kernel), with which two workgroups
+// share a CU and fill each other's waits.
 //
 // A stage's own way bounds it: a barrier, the loads' issue, the reads, the matrix instructions one after the other (256 rows
 // 4096 -> 4096 12.6 us; 512 rows 20.6, 0.83 P operations a second).
