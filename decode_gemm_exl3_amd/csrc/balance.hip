@@ -13,6 +13,7 @@
 #include "../../include/exl3_balance.h"
 #include "lanes_device.hpp"
 #include "pieces_device.hpp"
+#include "slots.hpp"
 #include "spans.hpp"
 
 namespace exl3 {
@@ -90,15 +91,12 @@ template <typename T, int LANES, int Q, bool VEC> __device__ inline Asked<Q> ask
 // token share its slots out.  COUNT: kept slots go into the histogram.
 template <int LANES, bool COUNT> __device__ inline bool counts_token(const Params& p, int token, int64_t id, int lane, int* hist) {
     bool kept = false;
-    for (int j = lane;;) {
-        if (id >= 0 && id < p.experts) {
+    lane_slots<LANES>(token < p.tokens ? p.top_k : 0, lane, id, [&](int j) { return load_id(p, (int64_t)token * p.top_k + j); }, [&](int64_t at) {
+        if (at >= 0 && at < p.experts) {
             kept = true;
-            if (COUNT) atomicAdd(&hist[(int)id], 1);
+            if (COUNT) atomicAdd(&hist[(int)at], 1);
         }
-        j += LANES;
-        if (token >= p.tokens || j >= p.top_k) break;
-        id = load_id(p, (int64_t)token * p.top_k + j);
-    }
+    });
     if constexpr (LANES == 1) return kept;
     const uint64_t all = __ballot(kept);
     if constexpr (LANES == 64) return all != 0;
