@@ -11,6 +11,7 @@ namespace i8 {
 
 constexpr int MAX_ROW = 1 << 24;                // values of a row that the row operators take
 constexpr int64_t MAX_ROWS = (int64_t)1 << 40;
+constexpr int64_t MAX_VALUES = (int64_t)1 << 56;  // rows times values: their bytes stay within 64 bits
 constexpr int64_t MAX_GRID = 1 << 20;           // workgroups of a row operator, which take row after row
 
 // Rows to codes and scales; with a weight, after the norm.
@@ -34,6 +35,7 @@ inline bool misaligned(const void* ptr, uintptr_t to = 16) { return (reinterpret
 inline bool bad_dtype(int32_t d) { return d < EXL3_F16 || d > EXL3_F32; }
 inline int64_t dtype_bytes(int32_t d) { return d == EXL3_F32 ? 4 : 2; }
 inline bool bad_row(int32_t n) { return n < EXL3_INT8_PIECE || n % EXL3_INT8_PIECE != 0; }
+inline bool too_many(int64_t rows, int32_t n) { return n > MAX_ROW || rows > MAX_ROWS || rows > MAX_VALUES / n; }
 inline bool bad_ld(int64_t ldx, int32_t n, int32_t dtype) { return ldx < n || ldx * dtype_bytes(dtype) % 16 != 0; }
 
 // `rows` rows of n values of dtype.

@@ -257,7 +257,7 @@ int exl3_int8_quantize(const void* x, int32_t dtype, int64_t rows, int32_t n, in
     if (bad_dtype(dtype) || bad_row(n) || rows < 0 || bad_ld(ldx, n, dtype)) return EXL3_EINVAL;
     if (rows == 0) return EXL3_OK;
     if (!x || !codes || !scales || misaligned(x) || misaligned(codes) || misaligned(scales, 4)) return EXL3_EINVAL;
-    if (n > MAX_ROW || rows > MAX_ROWS) return EXL3_EUNSUPPORTED;
+    if (too_many(rows, n)) return EXL3_EUNSUPPORTED;
     if (!apart({{codes, rows * n}, {scales, rows * 4}}, {values(x, dtype, rows, n, ldx)})) return EXL3_EINVAL;
     const RowsParams p = {x, ldx, nullptr, 0, nullptr, 0, 0.0, rows, n, codes, scales, nullptr};
     return launch_quantize(dtype, p, (hipStream_t)stream) == hipSuccess ? EXL3_OK : EXL3_EHIP;
@@ -269,7 +269,7 @@ int exl3_int8_dequantize(const int8_t* codes, const float* scales, int64_t rows,
     if (rows == 0) return EXL3_OK;
     if (!out || !codes || !scales || misaligned(out) || misaligned(codes) || misaligned(scales, 4)) return EXL3_EINVAL;
     // a launch takes fewer than 2^32 threads: 2^24 - 1 workgroups, of at least 4096 values
-    if (n > MAX_ROW || rows > MAX_ROWS || rows * n > (int64_t)0xFFFFFF * 4096) return EXL3_EUNSUPPORTED;
+    if (too_many(rows, n) || rows * n > (int64_t)0xFFFFFF * 4096) return EXL3_EUNSUPPORTED;
     if (!apart({values(out, dtype, 1, rows * n, rows * n)}, {{codes, rows * n}, {scales, rows * 4}})) return EXL3_EINVAL;
     hipStream_t s = (hipStream_t)stream;
     const hipError_t e = dtype == EXL3_F16    ? launch_dequantize<exl3::mx::F16>(codes, scales, rows, n, out, s)
@@ -287,7 +287,7 @@ int exl3_int8_rms_norm(const void* x, int32_t dtype, int64_t rows, int32_t n, in
     if (!x || !weight || !codes || !scales || misaligned(x) || misaligned(residual) || misaligned(weight) || misaligned(codes) ||
         misaligned(scales, 4) || misaligned(added))
         return EXL3_EINVAL;
-    if (n > MAX_ROW || rows > MAX_ROWS) return EXL3_EUNSUPPORTED;
+    if (too_many(rows, n)) return EXL3_EUNSUPPORTED;
     if (!apart({{codes, rows * n}, {scales, rows * 4}, values(added, dtype, 1, rows * n, rows * n)},
                {values(x, dtype, rows, n, ldx), values(residual, dtype, rows, n, ldr), values(weight, weight_dtype, 1, n, n)}))
         return EXL3_EINVAL;

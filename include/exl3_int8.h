@@ -40,8 +40,8 @@ extern "C" {
  *   codes  : int8 [rows][n], overwritten
  *   scales : fp32 [rows], overwritten
  * rows == 0 is a no-op.  EXL3_EINVAL for a null or misaligned pointer, a bad dtype,
- * n < 16 or n % 16 != 0, rows < 0 or a bad ldx; EXL3_EUNSUPPORTED for n > 2^24 or
- * rows > 2^40.
+ * n < 16 or n % 16 != 0, rows < 0 or a bad ldx; EXL3_EUNSUPPORTED for n > 2^24,
+ * rows > 2^40 or more than 2^56 values.
  */
 int exl3_int8_quantize(const void* x, int32_t dtype, int64_t rows, int32_t n, int64_t ldx, int8_t* codes,
                        float* scales, void* stream);
