@@ -2,7 +2,7 @@
 //
 // y[r][o] = T(fl(fl(sum_k x[r][k] w[o][k]) xs[r]) ws[o]): the sum exact in 32-bit integers, converted to
 // fp32 (the first rounding, from 2^24 on), each scale one more rounding of fp32, the type T the last.
-// Four kernels for few rows to many; launch_product at the end of the kernels chooses.
+// Five kernels for few rows to many; choose_product (int8_plan.hpp) chooses.
 #include <hip/hip_runtime.h>
 
 #include "int8_device.hpp"
@@ -583,8 +583,6 @@ __global__ __launch_bounds__(256, 2) void middle_kernel(const ProductParams p, i
 // 8192 -> 28672 359, and 16384 rows in 64 groups 2048 -> 2816 144 with 128 rows a tile.
 // Two groups that take turns against all eight waves alike: a stage's reads then wait behind each other.
 // One side's loads in each half of a stage, against all in the first: 8192^3 384 us, 415.
-constexpr int LARGE_COLS = 256;
-
 template <typename OT, int RT>
 __global__ __launch_bounds__(512, 2) void large_kernel(const ProductParams p, int row_tiles, int col_tiles, int tiles) {
     constexpr int CT = 4, ROWS = 32 * RT, UNIT = 256 * STAGE_BLOCKS, STAGE = (ROWS + LARGE_COLS) * STAGE_BLOCKS;
@@ -763,75 +761,32 @@ template <typename OT, int RT> hipError_t launch_large(const ProductParams& p, h
     return hipGetLastError();
 }
 
-// Row tiles of `high` rows that a product is expected to have: with groups, half a
-// tile of each group (or row) is padding.
-inline int64_t expected_tiles(const ProductParams& p, int high) {
-    if (!p.offsets) return (p.rows + high - 1) / high;
-    return p.rows / high + (p.n_groups < p.rows ? p.n_groups : p.rows) / 2 + 1;
-}
-
-// The time of a product in tiles, in us per 4096 inputs, by the rounds that 256 CUs take, as
-// measured: 128 x 128 tiles 28 for one a CU and 39 for two at once; 128 x 256 36.7; 256 x 256 52.
-inline double middle_time(const ProductParams& p) {
-    const int64_t each = (expected_tiles(p, 128) * ((p.n_out + 127) / 128) + CUS - 1) / CUS;
-    return (double)(each / 2) * 39 + (double)(each % 2) * 28;
-}
-inline double large_time(const ProductParams& p, int rt, int64_t n_out) {
-    const int64_t rounds = (expected_tiles(p, 32 * rt) * ((n_out + LARGE_COLS - 1) / LARGE_COLS) + CUS - 1) / CUS;
-    return (double)rounds * (rt == 8 ? 52 : 36.7);
-}
-
-// Rules by the average group, as the host doesn't know the route; times in us.
-//
-// Held rows: 128 rows in 64 groups 2048 -> 2816 52, streamed 62; 512 rows in 256 groups 1024 -> 1024 44 and 58; equal
-// at as many rows as are held (8 a group 76.9 and 75.9).
-// Streamed few-rows tiles while there is one of them a CU at most: against strips of 32 x 16 13 rows 14336 -> 4096 13.6 and
-// 14.0, 64 rows 4096 -> 1024 5.1 and 6.0, 8192 -> 1024 6.3 and 8.9, but with more 17 rows 14336 -> 4096 16.7 and 14.3, 32 rows
-// 20.0 and 16.9; against 32 x 32 ones 13 rows 4096 -> 6144 9.0 and 8.3; 32 rows in 8 groups 4096 -> 14336 101, in 64 x 64 tiles 91.
-// Strips of 32 rows and 16, 32 or 64 outputs, the narrowest of which there is one a CU at most: 40 rows 4096 -> 4096 8.6, 7.4 and
-// 9.3; 256 rows 4096 -> 1024 7.9, 6.5, 7.8; 128 rows 14336 -> 4096 44.3, 32.0, 26.9; 256 rows 4096 -> 2048 13.9, 9.1, 8.3; 64 x 64
-// tiles instead of the last 35.3 and 11.9, but 160 rows 4096 -> 4096 (320 strips) 12.5 against 16.3.
-// 64 x 64 tiles in stages of 256 inputs while there is one a CU, in stages of 128 where there are two: the latter
-// against the former 512 rows 4096 -> 4096 20.5 and 23.1, 2048 rows 4096 -> 1024 17.1 and 22.6, but 256 rows
-// 4096 -> 4096 14.3 and 12.7, 256 rows 14336 -> 4096 41.2 and 35.3.  128 x 128 ones beyond: 768 rows 4096 -> 4096
-// 28.8, 64 x 64 ones 33.4.  Groups of up to 32 rows, which the weights' way from memory bounds, stay with 64 x 64 ones, two
-// a CU: 2048 rows in 64 groups 2048 -> 2816 75.6, in 128 x 128 tiles 79.2, 128 x 256 77.9; 256 rows in 8 groups 4096 -> 14336 95.3, 115.6,
-// 114.7; groups of 64 rows 116, 111 in 128 x 256 tiles.
-// 128 x 128, 128 x 256 and 256 x 256 by the rounds that they take (the times above): 768 rows 4096 -> 4096 28.8, 31.5,
-// 44.9; 2048 rows 38.9, 34.8, 46.5; 4096 rows 74, 67, 54; 1000 rows 4096 -> 28672 133, 126, 102; 8192^3 508, 465, 384; 16384 rows
-// in 64 groups 2048 -> 2816 159, 143, 155.
-// Whole rounds of 256 x 256 and the rest in 128 x 256 tiles: 2048 rows 8192 -> 28672 359, all of them large 366; only
-// where it saves 5 %, for the second launch.
 template <typename OT> hipError_t launch_product(const ProductParams& p, hipStream_t s) {
     if (p.x) return launch_small<OT, QUANTISED>(p, s);
-    const int64_t m = typical_rows(p.rows, p.n_groups), runs = (p.n_out + 15) / 16;
-    if (p.offsets ? m < held_rows(p.n_in) : m <= held_rows(p.n_in)) return launch_small<OT, STAGED>(p, s);
-    if (expected_tiles(p, 16) * runs <= CUS) return launch_small<OT, STREAMED>(p, s);
-    if (expected_tiles(p, 32) * runs <= CUS) return launch_strip<OT, 32, 16, 3>(p, s);
-    if (expected_tiles(p, 32) * ((p.n_out + 31) / 32) <= CUS) return launch_strip<OT, 32, 32, 2>(p, s);
-    if (expected_tiles(p, 32) * ((p.n_out + 63) / 64) <= CUS) return launch_strip<OT, 32, 64, 2>(p, s);
-    const int64_t tiles = expected_tiles(p, 64) * ((p.n_out + 63) / 64);
-    if (tiles <= CUS) return launch_medium<OT, 16, 4>(p, s);
-    if (tiles <= 2 * CUS || (p.offsets && m <= 32)) return launch_medium<OT, 8, 5>(p, s);
-    const double middle = middle_time(p), low = large_time(p, 4, p.n_out), high = large_time(p, 8, p.n_out);
-    // Whole rounds of 256 x 256 tiles, and 128 x 256 ones for the columns left over.
-    const int64_t row_tiles = expected_tiles(p, 256), whole = row_tiles * ((p.n_out + LARGE_COLS - 1) / LARGE_COLS) / CUS;
-    const int64_t cols = whole * CUS / row_tiles * LARGE_COLS;
-    if (!p.offsets && cols > 0 && cols < p.n_out) {
-        const double both = large_time(p, 8, cols) + large_time(p, 4, p.n_out - cols);
-        if (both < 0.95 * high && both < low && both < middle) {
+    const ProductChoice c = choose_product(ProductShape{p.offsets != nullptr, p.rows, p.n_groups, p.n_in, p.n_out});
+    switch (c.kernel) {
+        case SMALL_STAGED: return launch_small<OT, STAGED>(p, s);
+        case SMALL_STREAMED: return launch_small<OT, STREAMED>(p, s);
+        case STRIP_16: return launch_strip<OT, 32, 16, 3>(p, s);
+        case STRIP_32: return launch_strip<OT, 32, 32, 2>(p, s);
+        case STRIP_64: return launch_strip<OT, 32, 64, 2>(p, s);
+        case MEDIUM_LONG: return launch_medium<OT, 16, 4>(p, s);
+        case MEDIUM_SHORT: return launch_medium<OT, 8, 5>(p, s);
+        case MIDDLE: return launch_middle<OT>(p, s);
+        case LARGE_128: return launch_large<OT, 4>(p, s);
+        case LARGE_256: return launch_large<OT, 8>(p, s);
+        case LARGE_BOTH: {
             ProductParams left = p, right = p;
-            left.n_out = (int)cols;
-            right.n_out = (int)(p.n_out - cols);
-            right.wc += cols * p.n_in;
-            right.ws += cols;
-            right.y = static_cast<char*>(p.y) + cols * OT::bytes;
+            left.n_out = c.cols;
+            right.n_out = p.n_out - c.cols;
+            right.wc += (int64_t)c.cols * p.n_in;
+            right.ws += c.cols;
+            right.y = static_cast<char*>(p.y) + (int64_t)c.cols * OT::bytes;
             const hipError_t e = launch_large<OT, 8>(left, s);
             return e == hipSuccess ? launch_large<OT, 4>(right, s) : e;
         }
     }
-    if (middle <= low && middle < high) return launch_middle<OT>(p, s);
-    return low < high ? launch_large<OT, 4>(p, s) : launch_large<OT, 8>(p, s);
+    return hipErrorInvalidValue;  // not reached
 }
 
 hipError_t product(int dtype, const ProductParams& p, hipStream_t s) {
