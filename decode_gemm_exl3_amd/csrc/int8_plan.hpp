@@ -91,35 +91,45 @@ struct ProductChoice {
     int cols;
 };
 
-// Rules by the average group, as the host doesn't know the route; times in us.
+// Rules by the average group, as the host doesn't know the route; times in us, of one series of runs with the
+// weights of several products in turn.
 //
-// Held rows: 128 rows in 64 groups 2048 -> 2816 52, streamed 62; 512 rows in 256 groups 1024 -> 1024 44 and 58; equal
-// at as many rows as are held (8 a group 76.9 and 75.9).
+// Held rows: 128 rows in 64 groups 2048 -> 2816 55, streamed 64; 512 rows in 256 groups 1024 -> 1024 44 and 59; but as many a
+// group as are held (8, 2048 -> 2816) 79, 64 x 64 tiles 69.
 // Streamed few-rows tiles while there is one of them a CU at most: against strips of 32 x 16 13 rows 14336 -> 4096 13.6 and
-// 14.0, 64 rows 4096 -> 1024 5.1 and 6.0, 8192 -> 1024 6.3 and 8.9, but with more 17 rows 14336 -> 4096 16.7 and 14.3, 32 rows
-// 20.0 and 16.9; against 32 x 32 ones 13 rows 4096 -> 6144 9.0 and 8.3; 32 rows in 8 groups 4096 -> 14336 101, in 64 x 64 tiles 91.
-// Strips of 32 rows and 16, 32 or 64 outputs, the narrowest of which there is one a CU at most: 40 rows 4096 -> 4096 8.6, 7.4 and
-// 9.3; 256 rows 4096 -> 1024 7.9, 6.5, 7.8; 128 rows 14336 -> 4096 44.3, 32.0, 26.9; 256 rows 4096 -> 2048 13.9, 9.1, 8.3; 64 x 64
-// tiles instead of the last 35.3 and 11.9, but 160 rows 4096 -> 4096 (320 strips) 12.5 against 16.3.
+// 13.9, 64 rows 4096 -> 1024 5.2 and 6.2, 8192 -> 1024 6.4 and 9.0, but with more 17 rows 14336 -> 4096 16.6 and 14.1, 32 rows
+// 20.0 and 16.7.  Up to 16 rows of more outputs take strips as well: 16 rows 8192 -> 8192 15.1, streamed 16.4, 28672 -> 5120 36.6 and
+// 40.3, 4096 -> 28672 26.2 and 29.5, though a few of them 28672 -> 8192 44.3 and 42.2, 28672 -> 16384 91 and 84, 13 rows 4096 -> 6144
+// 7.5 and 7.3.
+// Strips of 32 rows and 16, 32 or 64 outputs, the narrowest of which there is one a CU at most: 40 rows 4096 -> 4096 7.9, 6.7 and
+// 7.9; 256 rows 4096 -> 1024 8.1, 6.6, 7.9; 128 rows 14336 -> 4096 44.0, 31.8, 26.8; 256 rows 4096 -> 2048 14.1, 9.3, 8.0; 64 x 64
+// tiles instead of the last 35.0 and 12.0, but 160 rows 4096 -> 4096 (320 strips) 12.2 against 14.7.
+// Beyond, up to 16 rows (a group) of long inputs keep to 32 x 32 strips, as larger tiles are slower for rows that are not
+// there: against 64 x 64 and 128 x 256 tiles 16 rows 4096 -> 128256 97, 99 and 121, 4096 -> 40000 37, 40 and 44, two rows
+// 20480 -> 20480 84 and 105, 16 rows in 8 groups 14336 -> 4096 67 and 72, 200 in 16 8192 -> 4096 92 and 102; as fast for 128 in 8 4096 ->
+// 14336 (90.5 and 89.8) and 1024 in 64 4096 -> 2048 (101 and 102), a little slower for 16 rows 14336 -> 28672 (77 and 75).  Short inputs
+// not: 384 rows in 64 groups 2816 -> 2048 74 and 67; nor more rows: 256 in 8 groups 4096 -> 14336 110 and 93.
 // 64 x 64 tiles in stages of 256 inputs while there is one a CU, in stages of 128 where there are two: the latter
-// against the former 512 rows 4096 -> 4096 20.5 and 23.1, 2048 rows 4096 -> 1024 17.1 and 22.6, but 256 rows
-// 4096 -> 4096 14.3 and 12.7, 256 rows 14336 -> 4096 41.2 and 35.3.  128 x 128 ones beyond: 768 rows 4096 -> 4096
-// 28.8, 64 x 64 ones 33.4.  Groups of up to 32 rows, which the weights' way from memory bounds, stay with 64 x 64 ones, two
-// a CU: 2048 rows in 64 groups 2048 -> 2816 75.6, in 128 x 128 tiles 79.2, 128 x 256 77.9; 256 rows in 8 groups 4096 -> 14336 95.3, 115.6,
-// 114.7; groups of 64 rows 116, 111 in 128 x 256 tiles.
-// 128 x 128, 128 x 256 and 256 x 256 by the rounds that they take (the times above): 768 rows 4096 -> 4096 28.8, 31.5,
-// 44.9; 2048 rows 38.9, 34.8, 46.5; 4096 rows 74, 67, 54; 1000 rows 4096 -> 28672 133, 126, 102; 8192^3 508, 465, 384; 16384 rows
-// in 64 groups 2048 -> 2816 159, 143, 155.
-// Whole rounds of 256 x 256 and the rest in 128 x 256 tiles: 2048 rows 8192 -> 28672 359, all of them large 366; only
-// where it saves 5 %, for the second launch.
+// against the former 512 rows 4096 -> 4096 16.9 and 22.7, 2048 rows 4096 -> 1024 16.9 and 22.7, but 256 rows
+// 4096 -> 4096 13.8 and 12.2, 256 rows 14336 -> 4096 40.9 and 34.9.  128 x 128 ones beyond: 768 rows 4096 -> 4096
+// 26.4, 64 x 64 ones 27.0.  Groups of up to 32 rows, which the weights' way from memory bounds, stay with 64 x 64 ones, two
+// a CU: 2048 rows in 64 groups 2048 -> 2816 75.6, in 128 x 128 tiles 79.3, 128 x 256 77.6; 256 rows in 8 groups 4096 -> 14336 93.0, 110,
+// 108; groups of 64 rows 97, 83.5 in 128 x 256 tiles.
+// 128 x 128, 128 x 256 and 256 x 256 by the rounds that they take (the times above): 768 rows 4096 -> 4096 26.4, 28.6,
+// 41.5; 2048 rows 36.9, 33.9, 41.1; 4096 rows 74, 66, 54; 1000 rows 4096 -> 28672 137, 127, 104; 8192^3 545, 477, 391; 16384 rows
+// in 64 groups 2048 -> 2816 162, 150, 154.
+// Whole rounds of 256 x 256 and the rest in 128 x 256 tiles: 2048 rows 8192 -> 28672 372, all of them large 377; only
+// where it saves 5 % by these times, for the second launch.
 EXL3_I8_PLAN ProductChoice choose_product(const ProductShape& p) {
     const int64_t m = typical_rows(p.rows, p.n_groups), runs = ((int64_t)p.n_out + 15) / 16;
     if (p.grouped ? m < held_rows(p.n_in) : m <= held_rows(p.n_in)) return {SMALL_STAGED, 0};
     if (expected_tiles(p, 16) * runs <= CUS) return {SMALL_STREAMED, 0};
     if (expected_tiles(p, 32) * runs <= CUS) return {STRIP_16, 0};
-    if (expected_tiles(p, 32) * (((int64_t)p.n_out + 31) / 32) <= CUS) return {STRIP_32, 0};
-    const int64_t cols64 = ((int64_t)p.n_out + 63) / 64;
+    const int64_t strips = expected_tiles(p, 32) * (((int64_t)p.n_out + 31) / 32), cols64 = ((int64_t)p.n_out + 63) / 64;
+    if (strips <= CUS) return {STRIP_32, 0};
     if (expected_tiles(p, 32) * cols64 <= CUS) return {STRIP_64, 0};
+    // (a launch takes 2^24 workgroups, and there may be twice the tiles that are expected)
+    if (m <= 16 && p.n_in >= 4096 && strips < (1 << 22)) return {STRIP_32, 0};
     const int64_t tiles = expected_tiles(p, 64) * cols64;
     if (tiles <= CUS) return {MEDIUM_LONG, 0};
     if (tiles <= 2 * CUS || (p.grouped && m <= 32)) return {MEDIUM_SHORT, 0};

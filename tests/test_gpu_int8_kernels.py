@@ -24,7 +24,7 @@ def dev(a):
     return (torch.from_numpy(np.ascontiguousarray(a)) if isinstance(a, np.ndarray) else a).cuda()
 
 
-@pytest.mark.parametrize("kernel, groups, rows, behind, n_in, n_out, dtype", [(k, *c) for k, cs in C.GROUPED.items() for c in cs])
+@pytest.mark.parametrize("kernel, groups, rows, behind, n_in, n_out, dtype", [(k, *c) for cases in (C.GROUPED, C.FEW_GROUPED) for k, cs in cases.items() for c in cs])
 def test_groups(ex, kernel, groups, rows, behind, n_in, n_out, dtype):
     """Uneven groups, empty ones whose weights' scales are NaN, rows of no group that hold NaN, results inside a larger buffer."""
     dt, counts = DTYPES[dtype], C.uneven(groups, rows - behind, 0)
@@ -48,6 +48,21 @@ def test_groups(ex, kernel, groups, rows, behind, n_in, n_out, dtype):
             ref = (acc.float() * xs[lo:hi, None] * weight[1][g]).to(dt)
             assert torch.equal(y[lo:hi], ref) and torch.equal(z[lo:hi], ref), ("group", g, c)
     assert not y[at[-1]:].any() and not z[at[-1]:].any()
+
+
+@pytest.mark.parametrize("kernel, m, n_in, n_out, dtype", [(k, *c) for k, cs in C.FEW.items() for c in cs])
+def test_few_rows_of_many_outputs(ex, kernel, m, n_in, n_out, dtype):
+    dt = DTYPES[dtype]
+    rng = np.random.default_rng([33, m, n_in, n_out])
+    x = R.rows(rng, m, n_in + 8, dt).cuda()[:, :n_in]
+    wc, ws = (dev(a) for a in R.weight(rng, n_out, n_in))
+    xc, xs = (dev(a) for a in R.quantize(x))
+    acc = xc.double() @ wc.double().T  # whole numbers below 2^53: exact
+    ref = (acc.float() * xs[:, None] * ws).to(dt)
+    buf = torch.full((m * n_out + 64,), 7.0, dtype=dt, device="cuda")
+    y = ex.int8_linear(x, wc, ws, y=buf[32:32 + m * n_out].view(m, n_out))
+    assert torch.equal(y, ref) and (buf[:32] == 7).all() and (buf[32 + m * n_out:] == 7).all()
+    assert torch.equal(ex.int8_matmul(xc, xs, wc, ws, dt), ref)
 
 
 @pytest.mark.parametrize("kernel", C.LONG)

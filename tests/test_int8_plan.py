@@ -78,3 +78,30 @@ def test_every_number_of_kept_groups_is_covered(choose):
         for groups, rows, behind, *_ in cs:
             counts = C.uneven(groups, rows - behind, 0)
             assert sum(counts) == rows - behind and counts[0] and counts[-1] and (groups < 8 or 0 in counts)
+
+
+# Sizes at which both sides were timed: few rows of long inputs against tiles for rows that are not there, and where those are as fast
+@pytest.mark.parametrize("shape, kernel", [
+    ((0, 16, 1, 4096, 128256), "STRIP_32"), ((0, 16, 1, 4096, 40000), "STRIP_32"), ((0, 2, 1, 20480, 20480), "STRIP_32"),
+    ((0, 5, 1, 8192, 28672), "STRIP_32"), ((1, 12, 8, 14336, 4096), "STRIP_32"), ((1, 16, 8, 14336, 4096), "STRIP_32"),
+    ((1, 200, 16, 8192, 4096), "STRIP_32"), ((1, 128, 8, 4096, 14336), "STRIP_32"),
+    ((1, 256, 8, 4096, 14336), "MEDIUM_SHORT"), ((1, 384, 64, 2816, 2048), "MEDIUM_SHORT"), ((1, 1024, 128, 1024, 1024), "SMALL_STAGED"),
+    ((0, 16, 1, 2048, 28672), "MEDIUM_SHORT"), ((0, 13, 1, 14336, 4096), "SMALL_STREAMED"), ((1, 6, 8, 14336, 4096), "STRIP_64"),
+    ((0, 32, 1, 8192, 28672), "MEDIUM_SHORT"), ((0, 13, 1, 4096, 6144), "STRIP_32")])
+def test_few_rows(choose, shape, kernel):
+    assert choose([shape])[0][0] == kernel
+
+
+def test_few_rows_of_the_gpu_tests_reach_their_kernels(choose):
+    cases = [(k, c) for k, cs in C.FEW.items() for c in cs]
+    assert [(k, c) for (k, _), (_, c) in zip(choose([(0, m, 1, n_in, n_out) for _, (m, n_in, n_out, _) in cases]), cases)] == cases
+    cases = [(k, c) for k, cs in C.FEW_GROUPED.items() for c in cs]
+    assert [(k, c) for (k, _), (_, c) in zip(choose([(1, m, g, n_in, n_out) for _, (g, m, _, n_in, n_out, _) in cases]), cases)] == cases
+
+
+def test_strips_of_few_rows_fit_a_launch(choose):
+    """2^24 workgroups of 256 threads are a launch's end: the largest sizes that the entry points take."""
+    for shape in ((0, 16, 1, 4096, 1 << 24), (1, 4096, 4096, 4096, 1 << 17), (1, 16 * 4096, 4096, 4096, 1 << 17)):
+        kernel, _ = choose([shape])[0]
+        _, rows, groups, _, n_out = shape
+        assert kernel != "STRIP_32" or (rows // 32 + groups + 1) * -(-n_out // 32) + 127 < 1 << 24, shape
