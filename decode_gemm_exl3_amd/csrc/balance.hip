@@ -107,7 +107,8 @@ template <int LANES, bool COUNT> __device__ inline bool counts_token(const Param
 constexpr float INV_LN2 = 1.44269502f, INV_LN2_LOW = 1.92596299e-8f, LN2 = 0.693147182f;  // 1 / ln 2 in two parts
 
 // e^d of d <= 0 to a step of fp32: 2^y with y = fl(d / ln 2), which is off by up to its own size times 2^-24,
-// times 1 + (d / ln 2 - y) ln 2; 0 below -104, where fp32 ends.
+// times 1 + (d / ln 2 - y) ln 2; 0 from 2^-126 (d = -87.3) down, as the instruction makes no subnormal numbers, which
+// the 16-bit way below does neither.  (The largest of -104 keeps -infinity from becoming a NaN.)
 __device__ inline float exp_below(float d) {
     d = fmaxf(d, -104.f);
     const float y = d * INV_LN2, e = __builtin_amdgcn_exp2f(y);

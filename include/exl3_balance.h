@@ -15,7 +15,8 @@
  *       s[e] = c[e] / (V top_k); zeros for a token that does not count.
  * Logits of a token that does not count are not used, whatever they hold.  A logit of
  * -infinity has probability 0, a token with nothing else only zeros; a NaN or +infinity
- * makes its token's probabilities NaN, as a softmax does.
+ * makes its token's probabilities NaN, as a softmax does.  A probability below 2^-126 of
+ * its token's largest (a logit 87.4 and more below) counts as 0.
  *
  * Conventions: as in exl3.h and exl3_moe.h.  Sums over tokens are fp32 in an order that
  * depends on the sizes alone, those over experts 64 bits or fp32: results do not depend
