@@ -186,8 +186,10 @@ template <int COUNT> __device__ inline double block_sum(double v) {
 // columns over the wave's tokens in registers; the next token's logits and slots are on their
 // way meanwhile.  One workgroup alone writes the results.
 //
-// The exponentials, sums and lane exchanges bound it, not memory: 32768 tokens of 256 experts, 8 slots (18 MB of bf16
-// logits and ids), take 8.8 us (2 TB/s); 16 waves a workgroup, so that a CU has enough to issue.
+// 32768 tokens of 256 experts, 8 slots (18 MB of bf16 logits and ids, 3.6 us at a large copy's rate), take 8.8 us. The
+// vector units are busy 0.61 of that, 5 us, with exponentials, sums and lane exchanges; the rest is the start, the first tokens'
+// way from memory and the joins, which nothing covers (the waves wait 0.63 of their time).  16 waves a workgroup, so that a CU
+// has enough to issue.
 template <typename T, int LANES, int Q, bool VEC> __global__ __launch_bounds__(SUM_THREADS) void sum_kernel(const Params p) {
     constexpr int N = 16 / T::bytes, EACH = 64 / LANES, WAVES = SUM_THREADS / 64;
     __shared__ int hist[EXL3_MOE_MAX_EXPERTS + 1];
@@ -253,7 +255,7 @@ template <typename T, int LANES, int Q, bool VEC> __global__ __launch_bounds__(S
 
 // The workgroups' sums to the loss and the counts: a workgroup takes 64 experts, 16 threads each.
 // The last one to arrive adds up what they made, in their order.  Latency bounds it: of 256 workgroups' sums of 256
-// experts 7.4 us, most of it the sums' way between XCDs and the arrivals'.
+// experts 7.4 us in four workgroups, whose waves wait 0.77 of their time, for the sums' way between XCDs and the arrivals'.
 __global__ __launch_bounds__(FINAL_THREADS) void loss_kernel(const Params p) {
     constexpr int SLICES = FINAL_THREADS / FINAL_EXPERTS, EACH = MAX_BLOCKS / SLICES;
     static_assert(FINAL_EXPERTS == 64 && EXL3_MOE_MAX_EXPERTS / FINAL_EXPERTS <= 16, "an expert a lane, and a workgroup of 16");
@@ -322,7 +324,9 @@ __global__ __launch_bounds__(FINAL_THREADS) void loss_kernel(const Params p) {
 }
 
 // dlogits: the shares of this lane's columns stay in registers over all its tokens.  32768 tokens of 256 experts
-// (35 MB) take 14.1 us, 2.5 TB/s: the softmax again.  Up to 1024 workgroups: with 512 14.5 us in a graph, 1024 13.1, 2048 16.2.
+// (35 MB, 6.9 us at a large copy's rate) take 14.1 us: the vector units are busy 0.54 of it, 7 us, and memory about as long; the
+// two overlap little, as a wave has few tokens and only the next one on its way.  Up to 1024 workgroups: with 512 14.5 us in a graph,
+// 1024 13.1, 2048 16.2.
 template <typename T, int LANES, int Q, bool VEC> __global__ __launch_bounds__(BACKWARD_THREADS) void backward_kernel(const Params p) {
     constexpr int N = 16 / T::bytes, EACH = 64 / LANES, WAVES = BACKWARD_THREADS / 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & (LANES - 1), slot = (threadIdx.x & 63) / LANES;

@@ -300,11 +300,13 @@ constexpr int STAGE_BLOCKS = 8;  // of a row, in what follows: 128 inputs
 // b ^ (r / 2 & 7) of the row's 128 bytes.
 //
 // The weight's way to a CU bounds it, 23 to 25 bytes a ns where it comes from memory, and behind that the rows', which
-// each workgroup reads again: 32 rows 14336 -> 4096 take 16.9 us (the weight at 3.5 TB/s), 64 rows 4096 -> 4096 7.8.
+// each workgroup reads again: 32 rows 14336 -> 4096 take 16.7 us (the weight at 3.5 TB/s), 64 rows 4096 -> 4096 6.7.
 // Waves on their own against four that share a stage and meet at a barrier, in 32 x 32 tiles: the same where the weight
 // comes from memory, 15.1 us against 17.5 for 64 rows 14336 -> 4096 from the caches.
-// Rings of 2 stages of 128 inputs, against 4 of them or 2 of 256 inputs: 64 rows 4096 -> 6144 12.4 us, 15.4 and 14.8, as two
-// workgroups fit a CU; of 3 in 32 x 16 tiles, of which two fit as well (17 rows 14336 -> 4096 14.3, with 2 of 256 inputs 14.9).
+// Rings of 2, 3 and 4 stages, us: 32 x 32 tiles, one a CU, 64 rows 4096 -> 4096 6.7, 7.1 and 7.3, 14336 -> 4096 20.5, 21.1 and 21.4
+// (the longer start costs more than what is further ahead brings), and where there are more tiles, two of which a ring of 2 lets a
+// CU hold, 64 rows 4096 -> 6144 9.5, 12.5 and 12.9.  32 x 64 tiles, one a CU: 2 and 3 8.5 and 9.0 at that size, 128 rows 14336 -> 4096 26.9 and
+// 27.1.  32 x 16 tiles: 2, 3 and 4 17 rows 14336 -> 4096 16.7, 14.2 and 14.4, 24 rows 4096 -> 4096 6.1, 6.2 and 6.5: 3.
 template <typename OT, int TM, int TN, int RING>
 __global__ __launch_bounds__(256) void strip_kernel(const ProductParams p, int row_tiles, int col_tiles) {
     constexpr int WAVES = 4, PER = STAGE_BLOCKS, RT = TM / 16, CT = TN / 16, BUF = (TM + TN) * PER, EACH = 64 / PER, LOADS = (TM + TN) / EACH;  // rows of a load, loads of a stage
@@ -406,7 +408,7 @@ __global__ __launch_bounds__(256) void strip_kernel(const ProductParams p, int r
 // share a CU and fill each other's waits.
 //
 // A stage's own way bounds it: a barrier, the loads' issue, the reads, the matrix instructions one after the other (256 rows
-// 4096 -> 4096 12.6 us; 512 rows 20.6, 0.83 P operations a second).
+// 4096 -> 4096 12.2 us; 512 rows 16.9, 1.0 P operations a second).
 template <typename OT, int PER, int RING>
 __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int row_tiles, int col_tiles) {
     constexpr int T = 64, BUF = 2 * T * PER, LOADS = BUF / 256, EACH = 64 / PER;  // slots: rows, then weight rows; loads of a wave and stage; rows of a load
@@ -482,7 +484,7 @@ __global__ __launch_bounds__(256) void medium_kernel(const ProductParams p, int 
 // weight: the rows are asked for one stage ahead, the weight (which more often comes from
 // memory) two.  Block b of row r sits in 16-byte slot b ^ (r / 2 & 7) of the row's 128 bytes:
 // the 16 lanes that LDS serves together then read 16 different slots of its 256-byte width.
-// The loads' way bounds it: 768 rows 4096 -> 4096 take 28.8 us, 0.9 P operations a second.
+// The loads' way bounds it: 768 rows 4096 -> 4096 take 26.4 us, 1.0 P operations a second.
 // Units of the ring of this stage's rows, the next stage's rows and the weight of the one after
 // that, from that of this stage's weight; and that of the next stage's weight.
 __device__ inline int rows_unit(int u) { return u == 4 ? 0 : u + 1; }
@@ -579,8 +581,8 @@ __global__ __launch_bounds__(256, 2) void middle_kernel(const ProductParams p, i
 // What bounds it: the power that the matrix cores draw at these values (2048 rows 8192 -> 28672: they
 // are busy 0.79 of the cycles, at 1.67 GHz; all zeros run at 2.18 GHz and take 30 % less time), and the
 // results, which all workgroups store at once between tiles (8192^3: 384 us, without them 354).
-// 8192^3 takes 384 us by itself, 2.9 P operations a second, and 490 in a long run of them; 2048 rows
-// 8192 -> 28672 359, and 16384 rows in 64 groups 2048 -> 2816 144 with 128 rows a tile.
+// 8192^3 takes 384 to 391 us by itself, 2.8 P operations a second, and 490 in a long run of them; 2048 rows
+// 8192 -> 28672 359 to 372, and 16384 rows in 64 groups 2048 -> 2816 144 to 150 with 128 rows a tile.
 // Two groups that take turns against all eight waves alike: a stage's reads then wait behind each other.
 // One side's loads in each half of a stage, against all in the first: 8192^3 384 us, 415.
 template <typename OT, int RT>

@@ -1,4 +1,4 @@
-"""The committed times of the 8-bit products' kernels say which of them the launch takes, and it is what it takes."""
+"""The committed times of the 8-bit products' kernels say which of them the launch takes, and it is what it takes; derived counters."""
 import csv
 import os
 
@@ -21,3 +21,13 @@ def test_the_chosen_kernels(choose):  # noqa: F811
     for shape, (kernel, _) in zip(shapes, got):
         assert [k for k, (_, chosen) in by[shape].items() if chosen] == [NAMES[kernel]], shape
         assert len(by[shape]) > 1 and all(us > 0 for us, _ in by[shape].values())
+
+
+def test_the_balance_counters():
+    rows = list(csv.DictReader(line for line in open(os.path.join(ROOT, "profiles", "balance_counters.txt")) if not line.startswith("#")))
+    assert [r["kernel"].split("<")[0] for r in rows] == ["sum_kernel", "loss_kernel", "backward_kernel"]
+    for r in rows:
+        v = {k: float(x) for k, x in r.items() if k != "kernel"}
+        cycles = v["sq_busy_cycles"] / 32
+        assert abs(v["clock_ghz"] - cycles / v["run_ns"]) < 6e-4 and abs(v["wait_any"] - v["sq_wait_any"] / v["sq_wave_cycles"]) < 6e-4
+        assert abs(v["valu_busy"] - 4 * v["sq_active_inst_valu"] / 1024 / cycles) < 6e-4 and v["sq_active_inst_valu"] >= v["sq_insts_valu"]
