@@ -104,11 +104,12 @@ struct ProductChoice {
 // Strips of 32 rows and 16, 32 or 64 outputs, the narrowest of which there is one a CU at most: 40 rows 4096 -> 4096 7.9, 6.7 and
 // 7.9; 256 rows 4096 -> 1024 8.1, 6.6, 7.9; 128 rows 14336 -> 4096 44.0, 31.8, 26.8; 256 rows 4096 -> 2048 14.1, 9.3, 8.0; 64 x 64
 // tiles instead of the last 35.0 and 12.0, but 160 rows 4096 -> 4096 (320 strips) 12.2 against 14.7.
-// Beyond, up to 16 rows (a group) of long inputs keep to 32 x 32 strips, as larger tiles are slower for rows that are not
-// there: against 64 x 64 and 128 x 256 tiles 16 rows 4096 -> 128256 97, 99 and 121, 4096 -> 40000 37, 40 and 44, two rows
-// 20480 -> 20480 84 and 105, 16 rows in 8 groups 14336 -> 4096 67 and 72, 200 in 16 8192 -> 4096 92 and 102; as fast for 128 in 8 4096 ->
-// 14336 (90.5 and 89.8) and 1024 in 64 4096 -> 2048 (101 and 102), a little slower for 16 rows 14336 -> 28672 (77 and 75).  Short inputs
-// not: 384 rows in 64 groups 2816 -> 2048 74 and 67; nor more rows: 256 in 8 groups 4096 -> 14336 110 and 93.
+// Beyond, few rows of long inputs keep to 32 x 32 strips, as larger tiles are slower for rows that are not there: up to 16
+// of one weight from 4096 inputs on, against 64 x 64 and 128 x 256 tiles 16 rows 4096 -> 128256 97, 99 and 121, 4096 -> 40000 37, 40 and
+// 44, two rows 20480 -> 20480 84 and 105 (16 rows 14336 -> 28672 77, 75 in the former; of 2048 inputs -> 28672 15.9 and 13.7); up to 8 a
+// group from 8192 on, 16 rows in 8 groups 14336 -> 4096 67 and 72, 32 76.6 and 78.2.  More a group are faster in strips where
+// they are shared out evenly (200 in 16 8192 -> 4096 92 and 102), but not where a few groups have them all (28 and 25 in two of the 16); shorter
+// inputs are as fast (1024 in 64 groups 4096 -> 2048 101 and 102; 38 and 21 in four of the 64) or slower (384 in 64 2816 -> 2048 74 and 67).
 // 64 x 64 tiles in stages of 256 inputs while there is one a CU, in stages of 128 where there are two: the latter
 // against the former 512 rows 4096 -> 4096 16.9 and 22.7, 2048 rows 4096 -> 1024 16.9 and 22.7, but 256 rows
 // 4096 -> 4096 13.8 and 12.2, 256 rows 14336 -> 4096 40.9 and 34.9.  128 x 128 ones beyond: 768 rows 4096 -> 4096
@@ -129,7 +130,7 @@ EXL3_I8_PLAN ProductChoice choose_product(const ProductShape& p) {
     if (strips <= CUS) return {STRIP_32, 0};
     if (expected_tiles(p, 32) * cols64 <= CUS) return {STRIP_64, 0};
     // (a launch takes 2^24 workgroups, and there may be twice the tiles that are expected)
-    if (m <= 16 && p.n_in >= 4096 && strips < (1 << 22)) return {STRIP_32, 0};
+    if (m <= (p.grouped ? 8 : 16) && p.n_in >= (p.grouped ? 8192 : 4096) && strips < (1 << 22)) return {STRIP_32, 0};
     const int64_t tiles = expected_tiles(p, 64) * cols64;
     if (tiles <= CUS) return {MEDIUM_LONG, 0};
     if (tiles <= 2 * CUS || (p.grouped && m <= 32)) return {MEDIUM_SHORT, 0};

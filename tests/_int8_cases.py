@@ -43,5 +43,5 @@ def uneven(groups, rows, seed):
 # Few rows whose outputs are too many for one strip a CU: rows, n_in, n_out, dtype of one weight; and of groups as above
 FEW = {"STRIP_32": [(5, 4112, 20001, "bf16"), (16, 4096, 34001, "fp16"), (11, 4096, 16500, "fp32")],
        "MEDIUM_SHORT": [(9, 2064, 28673, "bf16"), (30, 4096, 20001, "fp16")]}
-FEW_GROUPED = {"STRIP_32": [(8, 13, 2, 8208, 4100, "bf16"), (8, 100, 0, 4096, 6001, "fp16"), (40, 600, 30, 4112, 1050, "fp32")],
-               "MEDIUM_SHORT": [(8, 136, 3, 4096, 4100, "bf16"), (20, 300, 1, 4080, 1500, "fp16")]}
+FEW_GROUPED = {"STRIP_32": [(8, 13, 2, 8208, 4100, "bf16"), (8, 60, 0, 8192, 6001, "fp16"), (40, 300, 30, 8208, 1050, "fp32")],
+               "MEDIUM_SHORT": [(8, 100, 3, 8192, 4100, "bf16"), (20, 150, 1, 8176, 1500, "fp16")]}

@@ -50,6 +50,21 @@ def test_groups(ex, kernel, groups, rows, behind, n_in, n_out, dtype):
     assert not y[at[-1]:].any() and not z[at[-1]:].any()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n_in, n_out", [(64, 40), (4096, 72), (16384, 20), (28672, 33)])
+@pytest.mark.parametrize("rows, ends", [(1, (0, 0)), (1, (0, 1)), (3, (0, 2)), (4, (0, 0)), (4, (0, 4)), (4, (-3, 9)), (9, (0, 5)), (70, (0, 1))])
+def test_one_group_and_rows_behind_it(ex, rows, ends, n_in, n_out, dtype):
+    """Few rows are quantised inside the product, with offsets too."""
+    dt, kept = DTYPES[dtype], max(0, min(ends[1], rows))
+    rng = np.random.default_rng([34, rows, n_in])
+    x = R.rows(rng, rows, n_in, dt)
+    x[kept:] = float("inf")
+    wc, ws = R.weight(rng, 1, n_out, n_in)
+    y = ex.int8_linear(x.cuda(), dev(wc), dev(ws), offsets=torch.tensor(ends, dtype=torch.int32, device="cuda"))
+    xc, xs = R.quantize(x[:kept])
+    assert R.equal(y[:kept], R.product(xc, xs, wc[0], ws[0], dt)) and not y[kept:].any()
+
+
 @pytest.mark.parametrize("kernel, m, n_in, n_out, dtype", [(k, *c) for k, cs in C.FEW.items() for c in cs])
 def test_few_rows_of_many_outputs(ex, kernel, m, n_in, n_out, dtype):
     dt = DTYPES[dtype]

@@ -84,7 +84,8 @@ def test_every_number_of_kept_groups_is_covered(choose):
 @pytest.mark.parametrize("shape, kernel", [
     ((0, 16, 1, 4096, 128256), "STRIP_32"), ((0, 16, 1, 4096, 40000), "STRIP_32"), ((0, 2, 1, 20480, 20480), "STRIP_32"),
     ((0, 5, 1, 8192, 28672), "STRIP_32"), ((1, 12, 8, 14336, 4096), "STRIP_32"), ((1, 16, 8, 14336, 4096), "STRIP_32"),
-    ((1, 200, 16, 8192, 4096), "STRIP_32"), ((1, 128, 8, 4096, 14336), "STRIP_32"),
+    ((1, 32, 8, 14336, 4096), "STRIP_32"), ((1, 64, 8, 14336, 4096), "STRIP_32"),
+    ((1, 200, 16, 8192, 4096), "MEDIUM_SHORT"), ((1, 128, 8, 4096, 14336), "MEDIUM_SHORT"),
     ((1, 256, 8, 4096, 14336), "MEDIUM_SHORT"), ((1, 384, 64, 2816, 2048), "MEDIUM_SHORT"), ((1, 1024, 128, 1024, 1024), "SMALL_STAGED"),
     ((0, 16, 1, 2048, 28672), "MEDIUM_SHORT"), ((0, 13, 1, 14336, 4096), "SMALL_STREAMED"), ((1, 6, 8, 14336, 4096), "STRIP_64"),
     ((0, 32, 1, 8192, 28672), "MEDIUM_SHORT"), ((0, 13, 1, 4096, 6144), "STRIP_32")])
