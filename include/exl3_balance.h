@@ -24,7 +24,9 @@
  * types, sizes below 1 (no tokens: a loss of 0, counts of 0, no gradient), more than
  * EXL3_MOE_MAX_EXPERTS experts, a coefficient that is not finite; EXL3_EUNSUPPORTED for
  * 2^24 tokens or 2^31 slots.  Results and the workspace share no byte with the
- * arguments or each other (EXL3_EINVAL where they do).
+ * arguments or each other (EXL3_EINVAL where they do).  The lanes that hold a token's
+ * logits (16 bytes each, 64 lanes at most) read its slots one after the other: meant for
+ * a few slots a lane, as many more take time in proportion.
  */
 #ifndef EXL3_BALANCE_H
 #define EXL3_BALANCE_H
